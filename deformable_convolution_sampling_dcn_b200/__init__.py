@@ -7,7 +7,10 @@ Thin Python front end of libdcn_b200.so (C ABI in include/dcn_b200.h):
     dcn_deform_conv_forward                  modulated deformable convolution, weight per point (DCNv2)
     deform_agg_forward / deform_agg_backward Sparse4D multi-camera aggregation
     deform_roi_pool_forward                  deformable RoI pooling
-    DCNCoreFunction, DeformAggFunction       autograd wrappers over the above
+    dcn_add_rms_norm_forward / _backward     residual addition + root-mean-square norm, 8-bit output
+    dcn_grad_norm / dcn_clip_grads           global gradient norm over many tensors (GradList), clipping
+    DCNCoreFunction, DeformAggFunction,
+    AddRmsNormFunction                       autograd wrappers over the above
     shard_range                              batch split for one-process-per-GPU runs
 
 PyTorch only allocates device memory and supplies the current stream; every
@@ -19,15 +22,18 @@ from typing import Tuple
 
 import torch
 
-from ._binding import (ABI_VERSION, EXPORTS, DaggParams, DcnError, DcnParams, DroiParams, core_params,
-                       dcn_core_backward, dcn_core_forward, dcn_core_forward_proj, dcn_core_output_hw,
-                       dcn_deform_conv_forward,
+from ._binding import (ABI_VERSION, EXPORTS, AddRmsNorm, DaggParams, DclipParams, DcnError, DcnParams, DnormParams,
+                       DroiParams, GradList, core_params, dcn_add_rms_norm_backward, dcn_add_rms_norm_forward,
+                       dcn_clip_grads, dcn_core_backward, dcn_core_forward, dcn_core_forward_proj, dcn_core_output_hw,
+                       dcn_deform_conv_forward, dcn_grad_norm,
                        deform_agg_backward,
                        deform_agg_forward, deform_roi_pool_forward, lib)
 
 __all__ = ["dcn_core_forward", "dcn_core_forward_proj", "dcn_deform_conv_forward", "dcn_core_backward", "dcn_core_output_hw", "deform_agg_forward",
            "deform_agg_backward", "deform_roi_pool_forward", "DroiParams", "DCNCoreFunction", "DeformAggFunction", "shard_range", "lib", "DcnError",
-           "DcnParams", "DaggParams", "core_params", "EXPORTS", "ABI_VERSION"]
+           "DcnParams", "DaggParams", "core_params", "EXPORTS", "ABI_VERSION", "dcn_add_rms_norm_forward",
+           "dcn_add_rms_norm_backward", "AddRmsNorm", "AddRmsNormFunction", "dcn_grad_norm", "dcn_clip_grads",
+           "GradList", "DnormParams", "DclipParams"]
 
 
 class DCNCoreFunction(torch.autograd.Function):
@@ -63,6 +69,31 @@ class DeformAggFunction(torch.autograd.Function):
         feat, ss, st, loc, w = ctx.saved_tensors
         gf, gl, gw = deform_agg_backward(feat, ss, st, loc, w, grad_out.contiguous())
         return gf, None, None, gl, gw
+
+
+class AddRmsNormFunction(torch.autograd.Function):
+    """autograd over dcn_add_rms_norm_forward/backward: (out, h) of x, residual and weight, all
+    differentiable; residual and weight may be None, h is x + residual (x itself without one)."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps: float = 1e-6):
+        o = dcn_add_rms_norm_forward(x, residual, weight, eps=eps, save_rstd=True)
+        h = x if residual is None else o.residual_out
+        ctx.save_for_backward(h, o.rstd, weight)
+        ctx.eps, ctx.has_residual = eps, residual is not None
+        ctx.set_materialize_grads(False)
+        return o.out, (h.view_as(h) if residual is None else h)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out, grad_h):
+        h, rstd, weight = ctx.saved_tensors
+        if grad_out is None:
+            gw = None if weight is None else torch.zeros_like(weight)
+            return grad_h, (grad_h if ctx.has_residual else None), gw, None
+        gx, gw = dcn_add_rms_norm_backward(grad_out.contiguous(), h, rstd, weight, eps=ctx.eps,
+                                           grad_residual_out=None if grad_h is None else grad_h.contiguous())
+        return gx, (gx if ctx.has_residual else None), gw, None
 
 
 def shard_range(total: int, world: int, rank: int) -> Tuple[int, int]:

@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -28,7 +28,9 @@ EXPORTS = ("dcn_core_output_hw", "dcn_core_forward", "dcn_core_backward", "defor
            "deform_agg_backward", "dcn_status_string", "dcn_last_error_detail", "dcn_abi_version",
            "dcn_take_device_error", "deform_roi_pool_forward", "dcn_core_forward_proj",
            "dcn_selftest_bounded_wait", "dcn_deform_conv_forward", "dcn_probe_rate",
-           "dcn_core_forward_proj_workspace_bytes", "dcn_core_forward_proj_noalloc")
+           "dcn_core_forward_proj_workspace_bytes", "dcn_core_forward_proj_noalloc",
+           "dcn_add_rms_norm_forward", "dcn_add_rms_norm_backward", "dcn_add_rms_norm_backward_workspace_bytes",
+           "dcn_grad_norm", "dcn_clip_grads", "dcn_grad_norm_workspace_bytes")
 ABI_VERSION = 2
 
 
@@ -47,6 +49,16 @@ class DroiParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "W", "C", "num_rois", "pooled_h", "pooled_w",
                                               "sampling")] + \
                [("spatial_scale", ctypes.c_float), ("gamma", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class DnormParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("dtype", "quant", "group")]
+
+
+class DclipParams(ctypes.Structure):
+    _fields_ = [("num_tensors", ctypes.c_int32), ("kind", ctypes.c_int32), ("max_norm", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 class DcnError(RuntimeError):
@@ -95,6 +107,17 @@ def _declare(lib):
     lib.dcn_probe_rate.argtypes = [ctypes.c_int32, ctypes.c_int32, vp, ctypes.c_int64,
                                    ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_char_p), vp]
     lib.dcn_probe_rate.restype = st
+    N, L = ctypes.POINTER(DnormParams), ctypes.POINTER(DclipParams)
+    lib.dcn_add_rms_norm_forward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.dcn_add_rms_norm_backward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp]
+    lib.dcn_add_rms_norm_backward_workspace_bytes.argtypes = [N]
+    lib.dcn_grad_norm.argtypes = [L, vp, vp, vp, vp, vp, ctypes.c_int64, vp]
+    lib.dcn_clip_grads.argtypes = [L, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp]
+    lib.dcn_grad_norm_workspace_bytes.argtypes = [ctypes.c_int32]
+    for f in ("dcn_add_rms_norm_forward", "dcn_add_rms_norm_backward", "dcn_grad_norm", "dcn_clip_grads"):
+        getattr(lib, f).restype = st
+    for f in ("dcn_add_rms_norm_backward_workspace_bytes", "dcn_grad_norm_workspace_bytes"):
+        getattr(lib, f).restype = ctypes.c_int64
     return lib
 
 
@@ -403,3 +426,238 @@ def deform_roi_pool_forward(x, rois, offset, *, pooled=(7, 7), sampling: int = 2
     check(lib().deform_roi_pool_forward(ctypes.byref(p), x.data_ptr(), rois.data_ptr(), offset.data_ptr(),
                                         out.data_ptr(), _stream(x)))
     return out
+
+
+def _launch(device: torch.device, fn, *args) -> None:
+    """fn(*args, stream) on `device` and its current stream; raises on a non-OK status."""
+    if device.index == torch.cuda.current_device():
+        check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _like(name: str, t: torch.Tensor, shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """Checks an argument that has to have this shape, type and device."""
+    _cuda_tensor(name, t, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+def _like_or_new(name, t, shape, dtype, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _like(name, t, shape, dtype, device)
+
+
+def _rows(x: torch.Tensor) -> Tuple[int, int]:
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("x must be [..., cols] with at least one column")
+    cols = x.shape[-1]
+    return x.numel() // cols, cols
+
+
+class AddRmsNorm(NamedTuple):
+    """Outputs of dcn_add_rms_norm_forward; None where a call does not ask for one."""
+    out: Optional[torch.Tensor]
+    residual_out: Optional[torch.Tensor]
+    out8: Optional[torch.Tensor]
+    scale: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+
+
+_QUANT = {None: (0, None), "e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
+
+
+def dcn_add_rms_norm_forward(x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                             weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+                             quant: Optional[str] = None, group: int = 0, keep_out: Optional[bool] = None,
+                             save_rstd: bool = False, out=None, residual_out=None, out8=None, scale=None,
+                             rstd=None) -> AddRmsNorm:
+    """Residual addition and root-mean-square norm over the last dimension; see dcn_b200.h.
+
+    quant "e4m3" or "int8" gives the output in 8 bits (out8, out8 * scale is the
+    norm's output) with one fp32 scale per row, scale [..., 1], or per 128 columns
+    (group=128), scale [..., ceil(cols / 128)].  `out` in the storage type is then
+    left out unless keep_out=True or a buffer is given.  save_rstd=True also
+    returns the statistic that the backward reads.  The buffers default to new
+    tensors; residual_out and out may each be x or residual."""
+    _cuda_tensor("x", x)
+    dt, dev = x.dtype, x.device
+    if dt not in _DTYPE_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    if quant not in _QUANT:
+        raise ValueError(f"quant must be None, 'e4m3' or 'int8', not {quant!r}")
+    code, dt8 = _QUANT[quant]
+    rows, cols = _rows(x)
+    shape = x.shape
+    if residual is not None:
+        _like("residual", residual, shape, dt, dev)
+        residual_out = _like_or_new("residual_out", residual_out, shape, dt, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if weight is not None:
+        _like("weight", weight, (cols,), dt, dev)
+    if code == 0:
+        if keep_out is False:
+            raise ValueError("keep_out=False without an 8-bit output")
+        if out8 is not None or scale is not None or group:
+            raise ValueError("out8, scale and group belong to an 8-bit output")
+    else:
+        if group not in (0, 128):
+            raise ValueError("group must be 0 or 128")
+        out8 = _like_or_new("out8", out8, shape, dt8, dev)
+        scale = _like_or_new("scale", scale, shape[:-1] + ((cols + 127) // 128 if group else 1,), torch.float32, dev)
+    if code == 0 or keep_out or out is not None:
+        out = _like_or_new("out", out, shape, dt, dev)
+        if residual_out is not None and rows and out.data_ptr() == residual_out.data_ptr():
+            raise ValueError("out and residual_out are the same buffer")
+    if save_rstd or rstd is not None:
+        rstd = _like_or_new("rstd", rstd, shape[:-1], torch.float32, dev)
+    p = DnormParams(rows, cols, eps, _DTYPE_CODE[dt], code, group)
+    _launch(dev, lib().dcn_add_rms_norm_forward, ctypes.byref(p), x.data_ptr(),
+            None if residual is None else residual.data_ptr(), None if weight is None else weight.data_ptr(),
+            None if residual_out is None else residual_out.data_ptr(), None if out is None else out.data_ptr(),
+            None if out8 is None else out8.data_ptr(), None if scale is None else scale.data_ptr(),
+            None if rstd is None else rstd.data_ptr())
+    return AddRmsNorm(out, residual_out, out8, scale, rstd)
+
+
+def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
+                              weight: Optional[torch.Tensor] = None, *,
+                              grad_residual_out: Optional[torch.Tensor] = None, eps: float = 1e-6, grad_x=None,
+                              grad_weight=None, workspace: Optional[torch.Tensor] = None):
+    """(grad_x, grad_weight) of dcn_add_rms_norm_forward; see dcn_b200.h.
+
+    h is the forward's residual_out (x without a residual), rstd what it saved;
+    grad_x is the gradient of x and of the residual alike.  grad_weight is None
+    without a weight.  eps is part of rstd and only checked here."""
+    _cuda_tensor("h", h)
+    dt, dev, shape = h.dtype, h.device, h.shape
+    if dt not in _DTYPE_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    rows, cols = _rows(h)
+    _like("grad_out", grad_out, shape, dt, dev)
+    _like("rstd", rstd, shape[:-1], torch.float32, dev)
+    if grad_residual_out is not None:
+        _like("grad_residual_out", grad_residual_out, shape, dt, dev)
+    grad_x = _like_or_new("grad_x", grad_x, shape, dt, dev)
+    p = DnormParams(rows, cols, eps, _DTYPE_CODE[dt], 0, 0)
+    ws_ptr, ws_bytes = None, 0
+    if weight is not None:
+        _like("weight", weight, (cols,), dt, dev)
+        grad_weight = _like_or_new("grad_weight", grad_weight, (cols,), dt, dev)
+        if workspace is None:
+            need = lib().dcn_add_rms_norm_backward_workspace_bytes(ctypes.byref(p))
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        else:
+            _cuda_tensor("workspace", workspace)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif grad_weight is not None:
+        raise ValueError("grad_weight without a weight")
+    _launch(dev, lib().dcn_add_rms_norm_backward, ctypes.byref(p), grad_out.data_ptr(), h.data_ptr(),
+            rstd.data_ptr(), None if weight is None else weight.data_ptr(),
+            None if grad_residual_out is None else grad_residual_out.data_ptr(), grad_x.data_ptr(),
+            None if grad_weight is None else grad_weight.data_ptr(), ws_ptr, ws_bytes)
+    return grad_x, grad_weight
+
+
+class GradList:
+    """The table of gradient buffers that dcn_grad_norm and dcn_clip_grads work on.
+
+    Made once where the buffers stay in place over a training run (both calls
+    also take a plain list and make the table each time).  `out` gives a buffer
+    of the same shape for each gradient, of any storage type, that receives the
+    clipped values; without it clipping is in place.  Buffers must not overlap.
+    The list keeps its tensors alive; a tensor that is given other memory
+    (resize_, set_) needs a new list."""
+
+    def __init__(self, grads: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None):
+        self.grads = list(grads)
+        self.out = None if out is None else list(out)
+        n = len(self.grads)
+        if self.out is not None and len(self.out) != n:
+            raise ValueError(f"{len(self.out)} out buffers for {n} gradients")
+        self.device = None
+        for t in self.grads + (self.out or []):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("gradients and out buffers must be torch.Tensors")
+            if t.dtype not in _DTYPE_CODE:
+                raise TypeError(f"unsupported dtype {t.dtype}")
+            if t.device.type != "cuda":
+                raise ValueError("gradients must be CUDA tensors (the library has no CPU path)")
+            if not t.is_contiguous():
+                raise ValueError("gradients and out buffers must be contiguous")
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError("gradients are on different devices")
+        spans = []
+        for i, g in enumerate(self.grads):
+            o = None if self.out is None else self.out[i]
+            if o is not None and o.shape != g.shape:
+                raise ValueError(f"out[{i}] shape {tuple(o.shape)} != {tuple(g.shape)}")
+            spans.append((g.data_ptr(), g.numel() * g.element_size()))
+            if o is not None and not (o.data_ptr() == g.data_ptr() and o.dtype == g.dtype):
+                spans.append((o.data_ptr(), o.numel() * o.element_size()))
+        end = 0
+        for at, size in sorted(s for s in spans if s[1]):
+            if at < end:
+                raise ValueError("gradient or out buffers overlap")
+            end = at + size
+        self.count = n
+        self._g = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in self.grads])
+        self._n = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in self.grads])
+        self._d = (ctypes.c_int32 * max(n, 1))(*[_DTYPE_CODE[t.dtype] for t in self.grads])
+        self._o = self._od = None
+        if self.out is not None:
+            self._o = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in self.out])
+            self._od = (ctypes.c_int32 * max(n, 1))(*[_DTYPE_CODE[t.dtype] for t in self.out])
+        self._ws = int(lib().dcn_grad_norm_workspace_bytes(n))
+
+
+_NORM_KIND = {2: 0, 2.0: 0, float("inf"): 1}
+
+
+def _grad_call(grads, out, norm_type, norm, workspace):
+    if not isinstance(grads, GradList):
+        grads = GradList(grads, out)
+    elif out is not None:
+        raise ValueError("out belongs to the GradList")
+    if norm_type not in _NORM_KIND:
+        raise ValueError(f"norm_type must be 2 or inf, not {norm_type}")
+    dev = grads.device
+    if dev is None:
+        if norm is None:
+            raise ValueError("no gradients: pass norm, which gives the device")
+        dev = norm.device
+    norm = _like_or_new("norm", norm, (), torch.float32, dev)
+    if workspace is None:
+        workspace = torch.empty(grads._ws, dtype=torch.uint8, device=dev)
+    else:
+        _cuda_tensor("workspace", workspace)
+    return grads, dev, norm, workspace, workspace.numel() * workspace.element_size()
+
+
+def dcn_grad_norm(grads, *, norm_type: float = 2.0, norm=None, workspace=None) -> torch.Tensor:
+    """The 2-norm (or largest magnitude, norm_type inf) of all gradients together, an fp32 scalar on the
+    device; grads is a GradList or a sequence of tensors.  See dcn_b200.h."""
+    grads, dev, norm, workspace, nbytes = _grad_call(grads, None, norm_type, norm, workspace)
+    p = DclipParams(grads.count, _NORM_KIND[norm_type], 0.0, 1.0)
+    _launch(dev, lib().dcn_grad_norm, ctypes.byref(p), grads._g, grads._n, grads._d, norm.data_ptr(),
+            workspace.data_ptr(), nbytes)
+    return norm
+
+
+def dcn_clip_grads(grads, max_norm: float, *, norm_type: float = 2.0, eps: float = 1e-6, out=None, norm=None,
+                   workspace=None) -> torch.Tensor:
+    """Scales all gradients by min(1, max_norm / (norm + eps)), in place or into `out`, and returns the norm
+    before that (fp32 scalar on the device; nothing synchronises).  See dcn_b200.h."""
+    grads, dev, norm, workspace, nbytes = _grad_call(grads, out, norm_type, norm, workspace)
+    p = DclipParams(grads.count, _NORM_KIND[norm_type], max_norm, eps)
+    _launch(dev, lib().dcn_clip_grads, ctypes.byref(p), grads._g, grads._n, grads._d, grads._o, grads._od,
+            norm.data_ptr(), workspace.data_ptr(), nbytes)
+    return norm

@@ -404,3 +404,188 @@ dcn_status deform_agg_backward(const dagg_params *p, const void *feat, const int
 }
 
 }  // extern "C"
+
+namespace {
+
+const int kMaxNormCols = 16384;
+const int64_t kMaxElems = (int64_t)1 << 40;
+
+dcn_status check_norm(const dnorm_params *p) {
+    if (!p) return fail(DCN_ERR_NULL, "params is NULL");
+    if (p->dtype < DCN_F32 || p->dtype > DCN_BF16) return fail(DCN_ERR_UNSUPPORTED, "dtype %d", p->dtype);
+    if (p->rows < 0 || p->cols < 1) return fail(DCN_ERR_SHAPE, "cols must be positive, rows not negative");
+    if (p->cols > kMaxNormCols) return fail(DCN_ERR_UNSUPPORTED, "cols = %d; at most %d", p->cols, kMaxNormCols);
+    if (p->rows > kMaxElems / p->cols) return fail(DCN_ERR_SHAPE, "rows * cols exceeds 2^40");
+    if (!(p->eps > 0.0f) || !isfinite(p->eps)) return fail(DCN_ERR_SHAPE, "eps must be positive and finite");
+    return DCN_OK;
+}
+
+dcnb::NormArgs norm_args(const dnorm_params *p) {
+    dcnb::NormArgs a;
+    memset(&a, 0, sizeof(a));
+    a.rows = p->rows;
+    a.cols = p->cols;
+    a.eps = p->eps;
+    a.dtype = (dcnb::DType)p->dtype;
+    return a;
+}
+
+// The tensor lists of the gradient-norm calls.
+dcn_status check_grads(const dclip_params *p, const void *const *grads, const int64_t *numel, const int32_t *dtypes,
+                       const float *norm, const void *workspace, int64_t workspace_bytes) {
+    if (!p) return fail(DCN_ERR_NULL, "params is NULL");
+    if (p->num_tensors < 0 || p->num_tensors > kMaxDim)
+        return fail(DCN_ERR_SHAPE, "num_tensors must be in [0, 2^20]");
+    if (p->kind != DCN_NORM_L2 && p->kind != DCN_NORM_MAX) return fail(DCN_ERR_UNSUPPORTED, "norm kind %d", p->kind);
+    if (workspace_bytes < 0) return fail(DCN_ERR_SHAPE, "workspace_bytes is negative");
+    if (!norm || !workspace) return fail(DCN_ERR_NULL, "norm and workspace are required");
+    if (p->num_tensors > 0 && (!grads || !numel || !dtypes))
+        return fail(DCN_ERR_NULL, "grads, numel and dtypes are required");
+    if (!aligned(norm, 4) || !aligned(workspace, 16))
+        return fail(DCN_ERR_ALIGN, "norm must be 4-byte aligned, workspace 16-byte aligned");
+    const int64_t need = dcnb::grad_clip_partials(p->num_tensors) * 8;
+    if (workspace_bytes < need)
+        return fail(DCN_ERR_SHAPE, "workspace has %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
+    int64_t total = 0;
+    for (int i = 0; i < p->num_tensors; ++i) {
+        if (numel[i] < 0 || numel[i] > kMaxElems) return fail(DCN_ERR_SHAPE, "numel[%d] is out of range", i);
+        total += numel[i];
+        if (total > kMaxElems) return fail(DCN_ERR_SHAPE, "the tensors have more than 2^40 elements");
+        if (dtypes[i] < DCN_F32 || dtypes[i] > DCN_BF16) return fail(DCN_ERR_UNSUPPORTED, "dtypes[%d] = %d", i, dtypes[i]);
+        if (!numel[i]) continue;
+        if (!grads[i]) return fail(DCN_ERR_NULL, "grads[%d] is NULL", i);
+        if (!aligned(grads[i], dtype_size(dtypes[i]))) return fail(DCN_ERR_ALIGN, "grads[%d] is not aligned to its element", i);
+    }
+    return DCN_OK;
+}
+
+dcnb::ClipArgs clip_args(const dclip_params *p, const void *const *grads, const int64_t *numel, const int32_t *dtypes,
+                         float *norm, void *workspace) {
+    dcnb::ClipArgs a;
+    memset(&a, 0, sizeof(a));
+    a.grads = grads;
+    a.numel = numel;
+    a.dtypes = dtypes;
+    a.num_tensors = p->num_tensors;
+    a.inf = p->kind == DCN_NORM_MAX;
+    a.norm = norm;
+    a.partial = static_cast<double *>(workspace);
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+dcn_status dcn_add_rms_norm_forward(const dnorm_params *p, const void *x, const void *residual, const void *weight,
+                                    void *residual_out, void *out, void *out8, float *scale, float *rstd,
+                                    dcn_stream_t stream) {
+    const dcn_status s = check_norm(p);
+    if (s != DCN_OK) return s;
+    if (p->quant != DCN_QUANT_NONE && p->quant != DCN_QUANT_E4M3 && p->quant != DCN_QUANT_INT8)
+        return fail(DCN_ERR_UNSUPPORTED, "quant %d", p->quant);
+    if (p->group != 0 && p->group != 128) return fail(DCN_ERR_UNSUPPORTED, "group must be 0 or 128");
+    if (p->group && p->quant == DCN_QUANT_NONE) return fail(DCN_ERR_SHAPE, "group without an 8-bit output");
+    if (p->rows == 0) return DCN_OK;
+    const bool q = p->quant != DCN_QUANT_NONE;
+    if (!x) return fail(DCN_ERR_NULL, "x is required");
+    if (!residual != !residual_out) return fail(DCN_ERR_NULL, "residual and residual_out go together");
+    if (q != (out8 != nullptr) || q != (scale != nullptr))
+        return fail(DCN_ERR_NULL, "out8 and scale are given exactly with an 8-bit output");
+    if (!out && !q) return fail(DCN_ERR_NULL, "out is required without an 8-bit output");
+    const size_t es = dtype_size(p->dtype);
+    if (!aligned(x, es) || !aligned(residual, es) || !aligned(weight, es) || !aligned(residual_out, es) ||
+        !aligned(out, es) || !aligned(scale, 4) || !aligned(rstd, 4))
+        return fail(DCN_ERR_ALIGN, "tensors must be aligned to their element");
+    dcnb::NormArgs a = norm_args(p);
+    a.x = x; a.residual = residual; a.weight = weight; a.residual_out = residual_out;
+    a.out = out; a.out8 = out8; a.scale = scale; a.rstd = rstd;
+    a.quant = p->quant;
+    a.group = p->group;
+    a.groups = p->group ? (p->cols + 127) / 128 : 1;
+    return cuda_status(dcnb::launch_norm_forward(a, (cudaStream_t)stream), "dcn_add_rms_norm_forward launch");
+}
+
+int64_t dcn_add_rms_norm_backward_workspace_bytes(const dnorm_params *p) {
+    if (check_norm(p) != DCN_OK) return -1;
+    return (int64_t)dcnb::norm_backward_partial_rows(p->rows, p->cols) * p->cols * 4;
+}
+
+dcn_status dcn_add_rms_norm_backward(const dnorm_params *p, const void *grad_out, const void *h, const float *rstd,
+                                     const void *weight, const void *grad_residual_out, void *grad_x,
+                                     void *grad_weight, void *workspace, int64_t workspace_bytes,
+                                     dcn_stream_t stream) {
+    const dcn_status s = check_norm(p);
+    if (s != DCN_OK) return s;
+    if (workspace_bytes < 0) return fail(DCN_ERR_SHAPE, "workspace_bytes is negative");
+    if (!weight != !grad_weight) return fail(DCN_ERR_NULL, "weight and grad_weight go together");
+    const size_t es = dtype_size(p->dtype);
+    if (!aligned(weight, es) || !aligned(grad_weight, es))
+        return fail(DCN_ERR_ALIGN, "tensors must be aligned to their element");
+    if (p->rows == 0) {
+        if (!grad_weight) return DCN_OK;
+        return cuda_status(cudaMemsetAsync(grad_weight, 0, (size_t)p->cols * es, (cudaStream_t)stream),
+                           "dcn_add_rms_norm_backward memset");
+    }
+    if (!grad_out || !h || !rstd || !grad_x) return fail(DCN_ERR_NULL, "grad_out, h, rstd and grad_x are required");
+    if (!aligned(grad_out, es) || !aligned(h, es) || !aligned(grad_residual_out, es) || !aligned(grad_x, es) ||
+        !aligned(rstd, 4))
+        return fail(DCN_ERR_ALIGN, "tensors must be aligned to their element");
+    dcnb::NormArgs a = norm_args(p);
+    a.partial_rows = dcnb::norm_backward_partial_rows(p->rows, p->cols);
+    if (grad_weight) {
+        if (!workspace) return fail(DCN_ERR_NULL, "workspace is required with a weight");
+        if (!aligned(workspace, 16)) return fail(DCN_ERR_ALIGN, "workspace must be 16-byte aligned");
+        const long long need = (long long)a.partial_rows * p->cols * 4;
+        if (workspace_bytes < need)
+            return fail(DCN_ERR_SHAPE, "workspace has %lld bytes, %lld needed", (long long)workspace_bytes, need);
+    }
+    a.grad_out = grad_out; a.h = h; a.rstd = const_cast<float *>(rstd); a.weight = weight;
+    a.grad_residual_out = grad_residual_out; a.grad_x = grad_x; a.grad_weight = grad_weight;
+    a.partial = static_cast<float *>(workspace);
+    return cuda_status(dcnb::launch_norm_backward(a, (cudaStream_t)stream), "dcn_add_rms_norm_backward launch");
+}
+
+int64_t dcn_grad_norm_workspace_bytes(int32_t num_tensors) {
+    if (num_tensors < 0 || num_tensors > kMaxDim) return -1;
+    return dcnb::grad_clip_partials(num_tensors) * 8;
+}
+
+dcn_status dcn_grad_norm(const dclip_params *p, const void *const *grads, const int64_t *numel, const int32_t *dtypes,
+                         float *norm, void *workspace, int64_t workspace_bytes, dcn_stream_t stream) {
+    const dcn_status s = check_grads(p, grads, numel, dtypes, norm, workspace, workspace_bytes);
+    if (s != DCN_OK) return s;
+    return cuda_status(dcnb::launch_grad_clip(clip_args(p, grads, numel, dtypes, norm, workspace), (cudaStream_t)stream),
+                       "dcn_grad_norm launch");
+}
+
+dcn_status dcn_clip_grads(const dclip_params *p, const void *const *grads, const int64_t *numel, const int32_t *dtypes,
+                          void *const *outs, const int32_t *out_dtypes, float *norm, void *workspace,
+                          int64_t workspace_bytes, dcn_stream_t stream) {
+    const dcn_status s = check_grads(p, grads, numel, dtypes, norm, workspace, workspace_bytes);
+    if (s != DCN_OK) return s;
+    if (!(p->max_norm >= 0.0f) || !isfinite(p->max_norm)) return fail(DCN_ERR_SHAPE, "max_norm must be finite, not negative");
+    if (!(p->eps > 0.0f) || !isfinite(p->eps)) return fail(DCN_ERR_SHAPE, "eps must be positive and finite");
+    if (outs) {
+        if (!out_dtypes && p->num_tensors > 0) return fail(DCN_ERR_NULL, "out_dtypes is required with outs");
+        for (int i = 0; i < p->num_tensors; ++i) {
+            if (out_dtypes[i] < DCN_F32 || out_dtypes[i] > DCN_BF16)
+                return fail(DCN_ERR_UNSUPPORTED, "out_dtypes[%d] = %d", i, out_dtypes[i]);
+            if (!numel[i]) continue;
+            if (!outs[i]) return fail(DCN_ERR_NULL, "outs[%d] is NULL", i);
+            if (!aligned(outs[i], dtype_size(out_dtypes[i])))
+                return fail(DCN_ERR_ALIGN, "outs[%d] is not aligned to its element", i);
+            if (outs[i] == grads[i] && out_dtypes[i] != dtypes[i])
+                return fail(DCN_ERR_UNSUPPORTED, "outs[%d] is its gradient's buffer in another dtype", i);
+        }
+    }
+    dcnb::ClipArgs a = clip_args(p, grads, numel, dtypes, norm, workspace);
+    a.outs = outs;
+    a.out_dtypes = out_dtypes;
+    a.clip = true;
+    a.max_norm = p->max_norm;
+    a.eps = p->eps;
+    return cuda_status(dcnb::launch_grad_clip(a, (cudaStream_t)stream), "dcn_clip_grads launch");
+}
+
+}  // extern "C"

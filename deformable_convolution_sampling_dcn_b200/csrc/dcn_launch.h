@@ -61,6 +61,38 @@ struct RoiArgs {
     DType dtype;
 };
 
+// 8-bit output kinds of the norm (dcn_quant8 of the ABI).
+enum : int { kQuantNone = 0, kQuantE4M3 = 1, kQuantInt8 = 2 };
+
+// Residual addition + root-mean-square norm over rows of `cols` values.
+struct NormArgs {
+    const void *x, *residual, *weight;  // forward; residual and weight may be nullptr
+    void *residual_out, *out, *out8;    // forward; out or out8 may be nullptr
+    float *scale;                       // forward: [rows] or [rows, groups]
+    float *rstd;                        // [rows]: written by the forward (or nullptr), read by the backward
+    const void *h, *grad_out, *grad_residual_out;  // backward; grad_residual_out may be nullptr
+    void *grad_x, *grad_weight;         // backward; grad_weight may be nullptr
+    float *partial;                     // backward: [partial_rows, cols] partial weight gradients
+    int64_t rows;
+    int cols, partial_rows;
+    float eps;
+    int quant, group, groups;           // group: 0 or 128 columns per scale
+    DType dtype;
+};
+
+// Global gradient norm and clipping over tables of tensors (host arrays).
+struct ClipArgs {
+    const void *const *grads;
+    void *const *outs;         // nullptr: in place
+    const int64_t *numel;
+    const int32_t *dtypes, *out_dtypes;
+    int num_tensors;
+    bool inf, clip;            // maximum norm instead of the 2-norm; clip after the norm
+    float max_norm, eps;
+    float *norm;
+    double *partial;           // grad_clip_partials(num_tensors) values
+};
+
 // Each launcher enqueues its kernel(s) on `stream` and returns the
 // cudaGetLastError() of the launch.
 cudaError_t launch_core_forward_generic(const CoreArgs &a, cudaStream_t stream);
@@ -88,5 +120,12 @@ cudaError_t launch_agg_forward(const AggArgs &a, cudaStream_t stream);
 cudaError_t launch_agg_wide(const AggArgs &a, bool bwd, cudaStream_t stream, bool *handled);
 cudaError_t launch_agg_backward(const AggArgs &a, cudaStream_t stream);
 cudaError_t launch_roi_pool_forward(const RoiArgs &a, cudaStream_t stream);
+cudaError_t launch_norm_forward(const NormArgs &a, cudaStream_t stream);
+// The backward, and the rows of partial weight gradients that it needs.
+cudaError_t launch_norm_backward(const NormArgs &a, cudaStream_t stream);
+int norm_backward_partial_rows(int64_t rows, int cols);
+// The norm, with clipping where a.clip, and the partial results that it needs.
+cudaError_t launch_grad_clip(const ClipArgs &a, cudaStream_t stream);
+int64_t grad_clip_partials(int num_tensors);
 
 }  // namespace dcnb

@@ -1,0 +1,82 @@
+// Shared pieces of the row-norm kernels: a team of threads owns one row at a
+// time.  Thread t of the team holds the 16-byte column vectors t, t + TPR,
+// t + 2*TPR, ... of the row (VEC columns each), so consecutive lanes hold
+// consecutive vectors: loads and stores are coalesced, and 128 neighbouring
+// columns sit in 16 (16-bit storage) or 32 (fp32) neighbouring lanes.
+//
+// A team is 8 lanes, a warp, or the whole CTA (TPR = 0).  Rows whose byte
+// length or base address is not a multiple of 16 take the same mapping with
+// element-wise accesses (AL = false).
+#pragma once
+
+#include "dcn_common.cuh"
+
+namespace dcnb {
+
+// NaN-propagating maximum (fmaxf drops NaN).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+struct SumOp {
+    static __device__ __forceinline__ float apply(float a, float b) { return a + b; }
+};
+struct MaxOp {
+    static __device__ __forceinline__ float apply(float a, float b) { return max_nan(a, b); }
+};
+
+template <typename OP, int W> __device__ __forceinline__ float lanes_reduce(float v) {
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) v = OP::apply(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// Reduction over the team.  CTA teams go through `red` (two sets of 32 floats,
+// used in turn, so one barrier per reduction is enough: a warp can be at most
+// one reduction ahead of the slowest reader).
+template <typename OP, int TPR> __device__ __forceinline__ float team_reduce(float v, float *red, int &turn) {
+    if constexpr (TPR != 0) {
+        return lanes_reduce<OP, TPR>(v);
+    } else {
+        v = lanes_reduce<OP, 32>(v);
+        float *r = red + 32 * turn;
+        turn ^= 1;
+        const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) r[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = r[lane < nw ? lane : 0];
+        if (lane >= nw) v = 0.0f;  // neutral: the sums and maxima here are of non-negative values or plain sums
+        return lanes_reduce<OP, 32>(v);
+    }
+}
+
+// The VEC columns starting at column c of a row, as raw storage (zeros past the end).
+template <typename T, bool AL> __device__ __forceinline__ uint4 load_cols(const T *row, int c, int cols) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if constexpr (AL) {
+        if (c < cols) v = *reinterpret_cast<const uint4 *>(row + c);
+    } else {
+        constexpr int VEC = Storage<T>::kVec;
+        T t[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) t[i] = c + i < cols ? row[c + i] : from_f32<T>(0.0f);
+        v = *reinterpret_cast<uint4 *>(t);
+    }
+    return v;
+}
+
+template <typename T, bool AL> __device__ __forceinline__ void store_cols(T *row, int c, int cols, const uint4 &v) {
+    if constexpr (AL) {
+        if (c < cols) *reinterpret_cast<uint4 *>(row + c) = v;
+    } else {
+        constexpr int VEC = Storage<T>::kVec;
+        const T *t = reinterpret_cast<const T *>(&v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (c + i < cols) row[c + i] = t[i];
+    }
+}
+
+}  // namespace dcnb

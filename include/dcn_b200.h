@@ -286,6 +286,114 @@ typedef struct {
 dcn_status deform_roi_pool_forward(const droi_params *p, const void *x, const float *rois,
                                    const float *offset, void *out, dcn_stream_t stream);
 
+/*
+ * Residual addition and root-mean-square norm over the channels of each row,
+ * with the output in the storage type, in 8 bits with scales, or both: what
+ * follows the projection of a residual block (the library's own addition; the
+ * pages' module ends in an ordinary norm layer).
+ *   h    = rnd(x + residual)            residual_out; h = x without a residual
+ *   rstd = 1 / sqrt(mean_c(h^2) + eps)
+ *   y    = h * rstd * weight            out; weight NULL: h * rstd
+ *   out8 = rnd(y * (1 / scale)),  scale = max(max|y| / top, 2^-126)
+ * with the maximum over the row (group = 0) or over each 128 neighbouring
+ * columns (group = 128; the last group of a row may be shorter), top = 448
+ * (DCN_QUANT_E4M3, saturating) or 127 (DCN_QUANT_INT8); out8 * scale is y up
+ * to the 8-bit rounding.  h is rounded to the storage type before the norm is
+ * taken of it; everything after that is fp32 and rounded once, 8-bit codes
+ * from the fp32 value.
+ *   x, residual, residual_out, out  [rows, cols]  storage dtype
+ *   weight                          [cols]        storage dtype, or NULL
+ *   out8                            [rows, cols]  one byte each
+ *   scale   [rows], or [rows, ceil(cols / 128)]   fp32
+ *   rstd    [rows]                                fp32, or NULL; what the backward reads
+ * residual_out is given exactly when residual is, out8 and scale exactly when
+ * quant is not DCN_QUANT_NONE; out may be NULL when out8 is given.
+ * residual_out and out may each be the buffer of x or of residual (a row is
+ * read before any of it is written), but not the same one; buffers that
+ * overlap in any other way give wrong results.
+ * A NaN or infinite h makes the statistics of its row NaN or rstd 0; a scale
+ * over a NaN is NaN (int8 codes of NaN values are 0, e4m3 codes NaN).
+ * cols in [1, 16384], eps > 0.  Tensors are aligned to their element; where
+ * all of them are 16-byte aligned and a row is a multiple of 16 bytes the
+ * kernel moves 16-byte vectors, else elements.  rows == 0 is a no-op.
+ */
+typedef enum { DCN_QUANT_NONE = 0, DCN_QUANT_E4M3 = 1, DCN_QUANT_INT8 = 2 } dcn_quant8;
+
+typedef struct {
+    int64_t rows;
+    int32_t cols;
+    float eps;
+    int32_t dtype;  /* dcn_dtype */
+    int32_t quant;  /* dcn_quant8 (forward only) */
+    int32_t group;  /* 0, or 128 columns per scale (forward only) */
+} dnorm_params;
+
+dcn_status dcn_add_rms_norm_forward(const dnorm_params *p, const void *x, const void *residual,
+                                    const void *weight, void *residual_out, void *out, void *out8,
+                                    float *scale, float *rstd, dcn_stream_t stream);
+
+/*
+ * Gradients of <grad_out, y> + <grad_residual_out, h> of the call above.  With
+ * xh = h * rstd and g = grad_out * weight:
+ *   grad_x      = rstd * (g - xh * mean_c(g * xh)) + grad_residual_out
+ *                 (of x and of residual alike)
+ *   grad_weight = sum over rows of grad_out * xh
+ * h is residual_out of the forward (x without a residual), rstd what it saved.
+ * grad_residual_out NULL: zero.  grad_weight is given exactly when weight is.
+ * grad_x may be the same buffer as grad_out or grad_residual_out.  workspace:
+ * dcn_add_rms_norm_backward_workspace_bytes(p) bytes, 16-byte aligned, needed
+ * with a weight; calls that overlap on the GPU need one each.  Sums are fp32 in
+ * a fixed order: equal calls give equal bits on one kind of GPU.  rows == 0
+ * zeroes grad_weight.
+ */
+dcn_status dcn_add_rms_norm_backward(const dnorm_params *p, const void *grad_out, const void *h,
+                                     const float *rstd, const void *weight,
+                                     const void *grad_residual_out, void *grad_x, void *grad_weight,
+                                     void *workspace, int64_t workspace_bytes, dcn_stream_t stream);
+
+/* Workspace bytes of dcn_add_rms_norm_backward; -1 for invalid params. */
+int64_t dcn_add_rms_norm_backward_workspace_bytes(const dnorm_params *p);
+
+/*
+ * Global norm over many gradient tensors, and clipping (the library's own
+ * addition: what a training step does with the gradients of the backward
+ * calls before its optimiser).
+ *   N = sqrt(sum of g^2 over all elements of all tensors), or max |g|
+ *   c = min(1, max_norm / (N + eps)),   out = rnd(g * c)
+ * grads, outs, numel and the dtype arrays are HOST arrays of num_tensors
+ * entries, read during the call (a captured graph keeps their contents); the
+ * pointers in them are device pointers to dense buffers aligned to their
+ * element.  outs NULL: in place.  Otherwise out_dtypes names the type of each
+ * out buffer (an fp32 master gradient of a 16-bit gradient, say), and a buffer
+ * may be its own gradient's.  Buffers must not overlap otherwise, nor occur
+ * twice.  A tensor with numel 0 is skipped (its pointers may be NULL).
+ * *norm (device, fp32) receives N; no element at all gives 0.  A NaN gradient
+ * gives a NaN norm and NaN gradients, an infinite one an infinite norm and
+ * c = 0.  In place with c = 1 nothing is written.  Squares and sums of fp32
+ * and bf16 gradients are formed in fp64, those of fp16 in fp32 per thread and
+ * fp64 above; the order is fixed, so equal calls give equal bits.
+ * workspace: dcn_grad_norm_workspace_bytes(num_tensors) bytes, 16-byte
+ * aligned; calls that overlap on the GPU need one each.
+ */
+typedef enum { DCN_NORM_L2 = 0, DCN_NORM_MAX = 1 } dcn_norm_kind;
+
+typedef struct {
+    int32_t num_tensors;
+    int32_t kind;     /* dcn_norm_kind */
+    float max_norm;   /* >= 0 (dcn_clip_grads only) */
+    float eps;        /* > 0 (dcn_clip_grads only) */
+} dclip_params;
+
+dcn_status dcn_grad_norm(const dclip_params *p, const void *const *grads, const int64_t *numel,
+                         const int32_t *dtypes, float *norm, void *workspace, int64_t workspace_bytes,
+                         dcn_stream_t stream);
+dcn_status dcn_clip_grads(const dclip_params *p, const void *const *grads, const int64_t *numel,
+                          const int32_t *dtypes, void *const *outs, const int32_t *out_dtypes, float *norm,
+                          void *workspace, int64_t workspace_bytes, dcn_stream_t stream);
+
+/* Workspace bytes of the two calls above; -1 for a negative count. */
+int64_t dcn_grad_norm_workspace_bytes(int32_t num_tensors);
+
 /* Static, human-readable name of a status. */
 const char *dcn_status_string(dcn_status s);
 

@@ -1,0 +1,112 @@
+"""Host-side checks of the norm and gradient-clipping calls (fake,
+never-dereferenced pointers; no call here reaches a kernel launch)."""
+import ctypes
+
+import pytest
+
+from deformable_convolution_sampling_dcn_b200 import _binding as B
+from deformable_convolution_sampling_dcn_b200 import build as build_mod
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_mod.build()
+    return B.lib()
+
+
+def norm(**kw):
+    base = dict(rows=4, cols=64, eps=1e-6, dtype=1, quant=0, group=0)
+    base.update(kw)
+    return B.DnormParams(**base)
+
+
+def fwd(lib, p, x=16, res=None, w=None, res_out=None, out=16, out8=None, scale=None, rstd=None):
+    return lib.dcn_add_rms_norm_forward(ctypes.byref(p), x, res, w, res_out, out, out8, scale, rstd, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(cols=0), B.DCN_ERR_SHAPE), (dict(rows=-1), B.DCN_ERR_SHAPE), (dict(cols=16385), B.DCN_ERR_UNSUPPORTED),
+    (dict(eps=0.0), B.DCN_ERR_SHAPE), (dict(eps=-1.0), B.DCN_ERR_SHAPE), (dict(eps=float("nan")), B.DCN_ERR_SHAPE),
+    (dict(eps=float("inf")), B.DCN_ERR_SHAPE), (dict(dtype=3), B.DCN_ERR_UNSUPPORTED),
+    (dict(quant=3), B.DCN_ERR_UNSUPPORTED), (dict(quant=1, group=64), B.DCN_ERR_UNSUPPORTED),
+    (dict(group=128), B.DCN_ERR_SHAPE), (dict(rows=1 << 36, cols=64), B.DCN_ERR_SHAPE),
+])
+def test_norm_params(lib, kw, status):
+    assert fwd(lib, norm(**kw)) == status
+
+
+def test_norm_pointers(lib):
+    p = norm()
+    assert lib.dcn_add_rms_norm_forward(None, 16, None, None, None, 16, None, None, None, None) == B.DCN_ERR_NULL
+    assert fwd(lib, p, x=None) == B.DCN_ERR_NULL
+    assert fwd(lib, p, out=None) == B.DCN_ERR_NULL
+    assert fwd(lib, p, res=16) == B.DCN_ERR_NULL                 # residual without residual_out
+    assert fwd(lib, p, res_out=16) == B.DCN_ERR_NULL
+    assert fwd(lib, p, out8=16, scale=16) == B.DCN_ERR_NULL      # 8-bit buffers without an 8-bit output
+    assert fwd(lib, norm(quant=1), out8=16) == B.DCN_ERR_NULL
+    assert fwd(lib, norm(quant=2), scale=16) == B.DCN_ERR_NULL
+    assert fwd(lib, p, x=17) == B.DCN_ERR_ALIGN
+    assert fwd(lib, norm(dtype=0), w=18) == B.DCN_ERR_ALIGN
+    assert fwd(lib, norm(quant=1), out8=16, scale=18) == B.DCN_ERR_ALIGN
+    assert fwd(lib, p, rstd=18) == B.DCN_ERR_ALIGN
+    assert fwd(lib, norm(rows=0), x=None, out=None) == B.DCN_OK
+
+
+def test_norm_backward_checks(lib):
+    f, p = lib.dcn_add_rms_norm_backward, norm()
+    need = lib.dcn_add_rms_norm_backward_workspace_bytes(ctypes.byref(p))
+    assert need == 4 * 64 * 4
+    assert lib.dcn_add_rms_norm_backward_workspace_bytes(ctypes.byref(norm(rows=1000))) == 592 * 64 * 4
+    assert lib.dcn_add_rms_norm_backward_workspace_bytes(ctypes.byref(norm(cols=0))) == -1
+    b = ctypes.byref(p)
+    assert f(b, None, 16, 16, None, None, 16, None, None, 0, None) == B.DCN_ERR_NULL
+    assert f(b, 16, 16, 16, 16, None, 16, None, 16, need, None) == B.DCN_ERR_NULL       # weight without grad_weight
+    assert f(b, 16, 16, 16, None, None, 16, 16, 16, need, None) == B.DCN_ERR_NULL
+    assert f(b, 16, 16, 16, 16, None, 16, 16, None, 0, None) == B.DCN_ERR_NULL          # no workspace
+    assert f(b, 16, 16, 16, 16, None, 16, 16, 16, need - 1, None) == B.DCN_ERR_SHAPE
+    assert f(b, 16, 16, 16, 16, None, 16, 16, 16, -1, None) == B.DCN_ERR_SHAPE
+    assert f(b, 16, 16, 16, 16, None, 16, 16, 8, need, None) == B.DCN_ERR_ALIGN
+    assert f(b, 16, 16, 18, None, None, 16, None, None, 0, None) == B.DCN_ERR_ALIGN
+    e = ctypes.byref(norm(rows=0))
+    assert f(e, None, None, None, None, None, None, None, None, 0, None) == B.DCN_OK
+
+
+def grads(ptrs=(64,), numel=(4,), dtypes=(0,), **kw):
+    n = len(ptrs)
+    p = B.DclipParams(kw.get("count", n), kw.get("kind", 0), kw.get("max_norm", 1.0), kw.get("eps", 1e-6))
+    return (p, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*numel), (ctypes.c_int32 * n)(*dtypes))
+
+
+def clip(lib, t, outs=None, od=None, norm=16, ws=16, nbytes=1 << 20):
+    p, g, n, dt = t
+    o = None if outs is None else (ctypes.c_void_p * len(outs))(*outs)
+    odt = None if od is None else (ctypes.c_int32 * len(od))(*od)
+    return lib.dcn_clip_grads(ctypes.byref(p), g, n, dt, o, odt, norm, ws, nbytes, None)
+
+
+def test_clip_checks(lib):
+    need = lib.dcn_grad_norm_workspace_bytes(1)
+    assert need > 0 and lib.dcn_grad_norm_workspace_bytes(-1) == -1
+    assert lib.dcn_grad_norm_workspace_bytes(5000) > lib.dcn_grad_norm_workspace_bytes(900)
+    assert clip(lib, grads(), norm=None) == B.DCN_ERR_NULL
+    assert clip(lib, grads(), ws=None) == B.DCN_ERR_NULL
+    assert clip(lib, grads(), ws=8) == B.DCN_ERR_ALIGN
+    assert clip(lib, grads(), norm=18) == B.DCN_ERR_ALIGN
+    assert clip(lib, grads(), nbytes=need - 1) == B.DCN_ERR_SHAPE
+    assert clip(lib, grads(), nbytes=-1) == B.DCN_ERR_SHAPE
+    assert clip(lib, grads(count=-1)) == B.DCN_ERR_SHAPE
+    assert clip(lib, grads(kind=2)) == B.DCN_ERR_UNSUPPORTED
+    assert clip(lib, grads(max_norm=-1.0)) == B.DCN_ERR_SHAPE
+    assert clip(lib, grads(max_norm=float("inf"))) == B.DCN_ERR_SHAPE
+    assert clip(lib, grads(eps=0.0)) == B.DCN_ERR_SHAPE
+    assert clip(lib, grads(numel=(-1,))) == B.DCN_ERR_SHAPE
+    assert clip(lib, grads(numel=(1 << 41,))) == B.DCN_ERR_SHAPE
+    assert clip(lib, grads(dtypes=(3,))) == B.DCN_ERR_UNSUPPORTED
+    assert clip(lib, grads(ptrs=(None,))) == B.DCN_ERR_NULL
+    assert clip(lib, grads(ptrs=(66,))) == B.DCN_ERR_ALIGN
+    assert clip(lib, grads(), outs=(None,), od=(0,)) == B.DCN_ERR_NULL
+    assert clip(lib, grads(), outs=(66,), od=(0,)) == B.DCN_ERR_ALIGN
+    assert clip(lib, grads(), outs=(128,), od=(5,)) == B.DCN_ERR_UNSUPPORTED
+    assert clip(lib, grads(), outs=(128,)) == B.DCN_ERR_NULL
+    assert clip(lib, grads(), outs=(64,), od=(1,)) == B.DCN_ERR_UNSUPPORTED  # in place in another type
+    assert lib.dcn_grad_norm(None, None, None, None, 16, 16, 1 << 20, None) == B.DCN_ERR_NULL

@@ -1,0 +1,389 @@
+"""Residual addition + root-mean-square norm on the GPU, its 8-bit outputs and
+its gradients, against the definition in 64 bits.
+
+Tolerances (u = 2^-24, half a step of fp32; uT = finfo(T).eps / 2).  The sum of
+squares has at most 32 terms per thread and 10 tree levels, all terms positive:
+relative error below 43u, so rstd is within 43u/2 and 2.5u of its own
+operations, y within 26u, plus uT where it is stored in 16 bits: |y|(32u + uT).
+"""
+import numpy as np
+import pytest
+import torch
+
+import deformable_convolution_sampling_dcn_b200 as d
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+EPS = 1e-6
+
+
+def half_step(dt):
+    return 0.0 if dt == torch.float32 else torch.finfo(dt).eps / 2
+
+
+def tiny(dt):
+    """Half of the smallest subnormal of a 16-bit type (fp16 outputs may be subnormal)."""
+    return torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
+
+
+def inputs(rows, cols, dt, seed, residual=True, weight=True, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(rows, cols, generator=g) * scale).to(dt)
+    r = (torch.randn(rows, cols, generator=g) * 2 * scale).to(dt) if residual else None
+    w = (1 + 0.3 * torch.randn(cols, generator=g)).to(dt) if weight else None
+    return x, r, w
+
+
+def definition(x, r, w, eps=EPS):
+    """(h in its type, y in 64 bits, rstd in 64 bits)."""
+    h = x if r is None else (x.double() + r.double()).to(x.dtype)
+    hd = h.double()
+    rstd = 1.0 / torch.sqrt((hd * hd).mean(-1) + np.float32(eps).astype(np.float64))
+    y = hd * rstd[:, None]
+    return h, (y if w is None else y * w.double()), rstd
+
+
+def gpu(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+# widths: one column, below and above the 8-lane, warp and CTA teams, odd, ragged groups, the largest
+COLS = [1, 2, 7, 8, 31, 32, 64, 100, 127, 128, 129, 136, 250, 256, 257, 512, 513, 520, 1000, 1024, 1032, 2049, 4096,
+        5000, 16384]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", COLS)
+def test_forward(cols, dtype, cuda_dev):
+    dt = DT[dtype]
+    for rows, residual, weight in ((1, True, True), (5, False, True), (37, True, False)):
+        x, r, w = inputs(rows, cols, dt, cols + rows, residual, weight)
+        o = d.dcn_add_rms_norm_forward(*gpu(x, r, w), eps=EPS, save_rstd=True)
+        h, y, rstd = definition(x, r, w)
+        assert o.out8 is None and o.scale is None and (o.residual_out is None) == (r is None)
+        if r is not None:
+            assert torch.equal(o.residual_out.cpu(), h)
+        err = (o.out.double().cpu() - y).abs()
+        assert (err <= y.abs() * (32 * U + half_step(dt)) + tiny(dt)).all(), float((err / y.abs()).max())
+        assert ((o.rstd.double().cpu() - rstd).abs() <= rstd * 26 * U).all()
+
+
+def check_quant(o, y, quant, group):
+    rows, cols = y.shape
+    top, ng = (448.0 if quant == "e4m3" else 127.0), (-(-cols // 128) if group else 1)
+    assert o.scale.shape == (rows, ng) and o.out8.shape == (rows, cols)
+    w = group or cols
+    amax = torch.stack([p.abs().amax(-1) for p in y.split(w, dim=1)], 1)
+    want = (amax / top).clamp(min=2.0 ** -126)
+    s = o.scale.double().cpu()
+    assert ((s - want).abs() <= want * 28 * U).all()  # y, the division and no more
+    sc = s.repeat_interleave(w, 1)[:, :cols]
+    q = o.out8.float().double().cpu()
+    err = (q * sc - y).abs()
+    slack = y.abs() * 32 * U + sc * 2 * U * top  # fp32 y, 1 / scale and their product
+    if quant == "e4m3":  # half a step: 2^-4 of the value, 2^-10 below the smallest normal 2^-6
+        assert (err <= torch.maximum(y.abs() * 2.0 ** -4, sc * 2.0 ** -10) + slack).all()
+    else:
+        assert q.abs().max() <= 127
+        assert (err <= 0.5 * sc + slack).all()
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("quant", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", [1, 8, 24, 64, 100, 128, 136, 200, 256, 300, 512, 1000, 1024, 1160, 2047, 4096, 8200])
+def test_forward_8bit(cols, dtype, quant, group, cuda_dev):
+    for rows, keep in ((1, False), (19, True)):
+        x, r, w = inputs(rows, cols, DT[dtype], 3 * cols + rows)
+        o = d.dcn_add_rms_norm_forward(*gpu(x, r, w), eps=EPS, quant=quant, group=group, keep_out=keep)
+        h, y, _ = definition(x, r, w)
+        assert torch.equal(o.residual_out.cpu(), h)
+        assert (o.out is not None) == keep
+        if keep:
+            err = (o.out.double().cpu() - y).abs()
+            assert (err <= y.abs() * (32 * U + half_step(DT[dtype])) + tiny(DT[dtype])).all()
+        check_quant(o, y, quant, group)
+
+
+def test_many_rows_and_rows_past_a_grid(cuda_dev):
+    """More rows than the persistent grid has teams, a ragged last round."""
+    for rows, cols, dtype in ((148 * 8 * 8 * 2 + 3, 40, "bf16"), (30011, 256, "f16"), (2501, 2048, "f32")):
+        x, r, w = inputs(rows, cols, DT[dtype], 5)
+        o = d.dcn_add_rms_norm_forward(*gpu(x, r, w), eps=EPS, quant="int8")
+        h, y, _ = definition(x, r, w)
+        assert torch.equal(o.residual_out.cpu(), h)
+        check_quant(o, y, "int8", 0)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", [8, 33, 256, 1000, 1032])
+def test_special_values(cols, dtype, cuda_dev):
+    """Zero rows give zeros, a NaN or an infinity stays in its own row."""
+    x, _, w = inputs(7, cols, DT[dtype], 9)
+    x[1] = 0
+    x[3, cols // 2] = float("nan")
+    x[5, 0] = float("inf")
+    o = d.dcn_add_rms_norm_forward(x.cuda(), None, w.cuda(), eps=EPS, quant="e4m3", group=128, keep_out=True)
+    q = d.dcn_add_rms_norm_forward(x.cuda(), None, w.cuda(), eps=EPS, quant="int8")
+    _, y, _ = definition(x, None, w)
+    out = o.out.double().cpu()
+    ok = [0, 1, 2, 4, 6]
+    assert (out[1] == 0).all() and (o.out8[1].float() == 0).all() and (q.out8[1] == 0).all()
+    assert (o.scale[1] == 2.0 ** -126).all()
+    assert ((out[ok] - y[ok]).abs() <= y[ok].abs() * (32 * U + half_step(DT[dtype])) + tiny(DT[dtype])).all()
+    assert out[3].isnan().all() and o.out8[3].float().isnan().all() and o.scale[3].isnan().all()
+    assert q.scale[3].isnan().all() and q.scale[5].isnan().all()
+    assert out[5, 0].isnan() and (out[5, 1:] == 0).all()  # rstd 0: inf * 0, finite * 0
+    assert not q.scale[[0, 1, 2, 4, 6]].isnan().any()
+
+
+def test_large_values_and_tiny_values(cuda_dev):
+    """fp16's largest values and rows far below eps keep their fp32 statistics."""
+    x = torch.full((2, 512), 65504.0, dtype=torch.float16)
+    x[1] = 6e-8
+    o = d.dcn_add_rms_norm_forward(x.cuda(), eps=EPS)
+    _, y, _ = definition(x, None, None)
+    assert ((o.out.double().cpu() - y).abs() <= y.abs() * (32 * U + half_step(torch.float16)) + tiny(torch.float16)).all()
+
+
+def test_unaligned_views_match_aligned(cuda_dev):
+    """Tensors that start off 16-byte boundaries take element-wise accesses and give the same numbers."""
+    for dtype, quant in (("bf16", None), ("f32", "e4m3"), ("f16", "int8")):
+        x, r, w = inputs(11, 264, DT[dtype], 21)
+
+        def off(t):
+            b = torch.empty(t.numel() + 3, dtype=t.dtype, device="cuda")[1:1 + t.numel()].view(t.shape)
+            return b.copy_(t)
+
+        a = d.dcn_add_rms_norm_forward(*gpu(x, r, w), eps=EPS, quant=quant)
+        b = d.dcn_add_rms_norm_forward(off(x), off(r), off(w), eps=EPS, quant=quant)
+        for p, q in zip(a, b):
+            assert (p is None) == (q is None)
+            if p is not None:
+                assert torch.equal(p.float(), q.float())
+
+
+def test_in_place_and_given_buffers(cuda_dev):
+    x, r, w = inputs(13, 256, torch.bfloat16, 31)
+    want = d.dcn_add_rms_norm_forward(*gpu(x, r, w))
+    xg, rg, wg = gpu(x, r, w)
+    o = d.dcn_add_rms_norm_forward(xg, rg, wg, residual_out=rg, out=xg)  # both over their inputs
+    assert o.out is xg and o.residual_out is rg
+    assert torch.equal(xg, want.out) and torch.equal(rg, want.residual_out)
+    xg, rg, _ = gpu(x, r, w)
+    d.dcn_add_rms_norm_forward(xg, rg, wg, residual_out=xg, out=rg)
+    assert torch.equal(rg, want.out) and torch.equal(xg, want.residual_out)
+
+
+def test_rows_beyond_32_bit_offsets(cuda_dev):
+    """Element offsets past 2^32: the last rows of a 4.3 G element bf16 tensor."""
+    rows, cols = 262145, 16384
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(3)
+    last = torch.randn(3, cols, generator=g).to(torch.bfloat16)
+    x[:2].fill_(1.0)
+    x[2:-3].zero_()
+    x[-3:] = last.cuda()
+    o = d.dcn_add_rms_norm_forward(x, eps=EPS, out=x)
+    _, y, _ = definition(last, None, None)
+    got = o.out[-3:].double().cpu()
+    assert ((got - y).abs() <= y.abs() * (32 * U + half_step(torch.bfloat16))).all()
+    assert (o.out[2:-3:50000] == 0).all()
+
+
+# ------------------------------------------------------------------ backward
+
+def backward_definition(gy, h, rstd, w, gh):
+    gy, hd, rs = gy.double(), h.double(), rstd.double()[:, None]
+    xh = hd * rs
+    g = gy if w is None else gy * w.double()
+    dot = (g * xh).mean(-1, keepdim=True)
+    gx = rs * (g - xh * dot)
+    # fp32 error of each part: 4 roundings of g and of the outer operations; the dot's sum has at most
+    # 16 terms per thread, 10 tree levels and 4 roundings per term
+    bound = rs * (6 * g.abs() + xh.abs() * (32 * (g * xh).abs().mean(-1, keepdim=True) + 8 * dot.abs())) * U
+    if gh is not None:
+        gx = gx + gh.double()
+        bound = bound + U * gx.abs()
+    gw = None if w is None else (gy * xh).sum(0)
+    gw_abs = None if w is None else (gy * xh).abs().sum(0)
+    return gx, bound, gw, gw_abs
+
+
+def rows_in_a_chain(rows):
+    """fp32 additions that one partial sum of the weight gradient can see: its rows, up to 32 teams of a
+    CTA, the 592 / 16 rows of partial sums per thread and 16 threads, 4 roundings per term."""
+    return -(-rows // min(rows, 592)) + 32 + 37 + 16 + 4
+
+
+def check_backward(rows, cols, dtype, seed, weight=True, residual=True):
+    dt = DT[dtype]
+    h, gh, w = inputs(rows, cols, dt, seed, residual, weight)
+    gy = torch.randn(rows, cols, generator=torch.Generator().manual_seed(seed + 1)).to(dt)
+    rstd = definition(h, None, None)[2].float()
+    gx, gw = d.dcn_add_rms_norm_backward(*gpu(gy, h, rstd, w), grad_residual_out=None if gh is None else gh.cuda())
+    want, bound, want_w, abs_w = backward_definition(gy, h, rstd, w, gh)
+    err = (gx.double().cpu() - want).abs()
+    assert (err <= bound + want.abs() * (half_step(dt) + 2 * U) + tiny(dt)).all(), float(err.max())
+    assert (gw is None) == (w is None)
+    if w is not None:
+        err = (gw.double().cpu() - want_w).abs()
+        assert (err <= abs_w * rows_in_a_chain(rows) * U + want_w.abs() * half_step(dt) + tiny(dt)).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", COLS)
+def test_backward(cols, dtype, cuda_dev):
+    check_backward(1, cols, dtype, cols)
+    check_backward(23, cols, dtype, cols + 1, residual=False)
+    check_backward(41, cols, dtype, cols + 2, weight=False)
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(20011, 256, "bf16"), (6001, 512, "f32"), (5003, 513, "f16"),
+                                             (3001, 2048, "f32"), (40000, 40, "f32"), (1201, 16384, "bf16")])
+def test_backward_many_rows(rows, cols, dtype, cuda_dev):
+    check_backward(rows, cols, dtype, 7)
+
+
+def test_backward_repeats_bit_for_bit(cuda_dev):
+    h, gh, w = gpu(*inputs(9001, 256, torch.float32, 4))
+    gy = torch.randn_like(h)
+    rstd = torch.rsqrt(h.square().mean(-1) + EPS)
+    a = d.dcn_add_rms_norm_backward(gy, h, rstd, w, grad_residual_out=gh)
+    for _ in range(3):
+        b = d.dcn_add_rms_norm_backward(gy, h, rstd, w, grad_residual_out=gh)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_backward_in_place_and_unaligned(cuda_dev):
+    h, gh, w = inputs(17, 264, torch.bfloat16, 6)
+    gy = torch.randn(17, 264).to(torch.bfloat16)
+    rstd = definition(h, None, None)[2].float().cuda()
+    want = d.dcn_add_rms_norm_backward(*gpu(gy, h), rstd, w.cuda(), grad_residual_out=gh.cuda())
+    for which in ("grad_out", "grad_residual_out"):
+        gyg, hg, wg, ghg = gpu(gy, h, w, gh)
+        got = d.dcn_add_rms_norm_backward(gyg, hg, rstd, wg, grad_residual_out=ghg,
+                                          grad_x=gyg if which == "grad_out" else ghg)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+    def off(t):
+        return torch.empty(t.numel() + 3, dtype=t.dtype, device="cuda")[1:1 + t.numel()].view(t.shape).copy_(t)
+
+    got = d.dcn_add_rms_norm_backward(off(gy), off(h), rstd, off(w), grad_residual_out=off(gh))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_gradients_against_differences(cuda_dev):
+    """Central differences of the 64-bit definition along random directions, fp32 storage."""
+    x, r, w = inputs(6, 96, torch.float32, 8)
+    gy, gh = torch.randn(6, 96), torch.randn(6, 96)
+    xg, rg, wg = (t.cuda().requires_grad_() for t in (x, r, w))
+    y, h = d.AddRmsNormFunction.apply(xg, rg, wg, EPS)
+    torch.autograd.backward([y, h], [gy.cuda(), gh.cuda()])
+
+    def loss(x, r, w):
+        hd = x + r
+        yd = hd / torch.sqrt((hd * hd).mean(-1, keepdim=True) + EPS) * w
+        return float((yd * gy.double()).sum() + (hd * gh.double()).sum())
+
+    base = [t.double() for t in (x, r, w)]
+    for i, leaf in enumerate((xg, rg, wg)):
+        for s in range(3):
+            v = torch.randn(base[i].shape, generator=torch.Generator().manual_seed(s)).double()
+            step = 1e-5
+            up, dn = list(base), list(base)
+            up[i], dn[i] = base[i] + step * v, base[i] - step * v
+            diff = (loss(*up) - loss(*dn)) / (2 * step)
+            got = float((leaf.grad.double().cpu() * v).sum())
+            # 576 terms of fp32 gradients, each within 1e-6 of its size, and the difference's own 1e-8
+            assert abs(got - diff) <= 1e-6 * float((leaf.grad.double().cpu() * v).abs().sum()) + 1e-6
+
+
+def test_autograd_forms(cuda_dev):
+    """No residual, no weight, an unused output, a non-contiguous incoming gradient, leaves used twice."""
+    x = torch.randn(9, 64, device="cuda", requires_grad=True)
+    y, h = d.AddRmsNormFunction.apply(x, None, None, EPS)
+    (y.t().contiguous().t() * 2).sum().backward()
+    xd = x.detach().double().requires_grad_()
+    (xd / torch.sqrt((xd * xd).mean(-1, keepdim=True) + EPS) * 2).sum().backward()
+    assert torch.allclose(x.grad.double(), xd.grad, rtol=1e-4, atol=1e-6)
+    x.grad = None
+    y, h = d.AddRmsNormFunction.apply(x, x, None, EPS)  # the same leaf twice
+    h.sum().backward()
+    assert torch.equal(x.grad, torch.full_like(x, 2.0))
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    x.grad = None
+    y, h = d.AddRmsNormFunction.apply(x, None, w, EPS)
+    y.sum().backward()
+    assert x.grad is not None and w.grad is not None
+
+
+def test_empty_and_streams_and_graph(cuda_dev):
+    w = torch.ones(64, device="cuda")
+    o = d.dcn_add_rms_norm_forward(torch.empty(0, 64, device="cuda"), weight=w, quant="int8", save_rstd=True)
+    assert o.out8.shape == (0, 64) and o.scale.shape == (0, 1) and o.rstd.shape == (0,)
+    gw = torch.full((64,), 7.0, device="cuda")
+    d.dcn_add_rms_norm_backward(torch.empty(0, 64, device="cuda"), torch.empty(0, 64, device="cuda"),
+                                torch.empty(0, device="cuda"), w, grad_weight=gw)
+    assert (gw == 0).all()
+
+    x, r, w = gpu(*inputs(300, 512, torch.bfloat16, 12))
+    gy = torch.randn_like(x)
+    want = d.dcn_add_rms_norm_forward(x, r, w, save_rstd=True)
+    wb = d.dcn_add_rms_norm_backward(gy, want.residual_out, want.rstd, w)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = d.dcn_add_rms_norm_forward(x, r, w)
+    s.synchronize()
+    assert torch.equal(got.out, want.out)
+    # two graphs of the same calls, replayed in turn on new inputs: nothing is shared between them
+    graphs = []
+    for _ in range(2):
+        xs = x.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = d.dcn_add_rms_norm_forward(xs, r, w, save_rstd=True)
+            b = d.dcn_add_rms_norm_backward(gy, o.residual_out, o.rstd, w)
+        graphs.append((g, xs, o, b))
+    graphs[1][1].copy_(x * 2)
+    for g, *_ in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(graphs[0][2].out, want.out)
+    assert torch.equal(graphs[0][3][0], wb[0]) and torch.equal(graphs[0][3][1], wb[1])
+    other = d.dcn_add_rms_norm_forward(x * 2, r, w)
+    assert torch.equal(graphs[1][2].out, other.out)
+
+
+def test_binding_refusals(cuda_dev):
+    x = torch.randn(4, 64, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        d.dcn_add_rms_norm_forward(torch.randn(64, 4, device="cuda").t())
+    with pytest.raises(TypeError):
+        d.dcn_add_rms_norm_forward(x.double())
+    with pytest.raises(TypeError):
+        d.dcn_add_rms_norm_forward(x, x.half())
+    with pytest.raises(ValueError, match="shape"):
+        d.dcn_add_rms_norm_forward(x, x[:3])
+    with pytest.raises(ValueError, match="shape"):
+        d.dcn_add_rms_norm_forward(x, None, torch.ones(63, device="cuda"))
+    with pytest.raises(ValueError, match="quant"):
+        d.dcn_add_rms_norm_forward(x, quant="e5m2")
+    with pytest.raises(ValueError, match="group"):
+        d.dcn_add_rms_norm_forward(x, quant="int8", group=64)
+    with pytest.raises(ValueError, match="same buffer"):
+        d.dcn_add_rms_norm_forward(x, x, out=x, residual_out=x)
+    with pytest.raises(ValueError):
+        d.dcn_add_rms_norm_forward(x, keep_out=False)
+    with pytest.raises(d.DcnError):
+        d.dcn_add_rms_norm_forward(x, eps=0.0)
+    with pytest.raises(d.DcnError):
+        d.dcn_add_rms_norm_forward(torch.zeros(1, 16385, device="cuda"))
+    with pytest.raises(ValueError):
+        d.dcn_add_rms_norm_backward(x, x, torch.ones(4, device="cuda"), grad_weight=torch.ones(64, device="cuda"))
+    with pytest.raises(d.DcnError):
+        d.dcn_add_rms_norm_backward(x, x, torch.ones(4, device="cuda"), torch.ones(64, device="cuda"),
+                                    workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
