@@ -7,6 +7,7 @@ Thin Python front end of libdcn_b200.so (C ABI in include/dcn_b200.h):
     dcn_deform_conv_forward                  modulated deformable convolution, weight per point (DCNv2)
     deform_agg_forward / deform_agg_backward Sparse4D multi-camera aggregation
     deform_roi_pool_forward                  deformable RoI pooling
+    dcn_proj_adapters_forward                1x1 projection with low-rank adapters of many requests
     dcn_add_rms_norm_forward / _backward     residual addition + root-mean-square norm, 8-bit output
     dcn_grad_norm / dcn_clip_grads           global gradient norm over many tensors (GradList), clipping
     DCNCoreFunction, DeformAggFunction,
@@ -22,10 +23,10 @@ from typing import Tuple
 
 import torch
 
-from ._binding import (ABI_VERSION, EXPORTS, AddRmsNorm, DaggParams, DclipParams, DcnError, DcnParams, DnormParams,
-                       DroiParams, GradList, core_params, dcn_add_rms_norm_backward, dcn_add_rms_norm_forward,
+from ._binding import (ABI_VERSION, EXPORTS, AddRmsNorm, DadaptParams, DaggParams, DclipParams, DcnError, DcnParams,
+                       DnormParams, DroiParams, GradList, core_params, dcn_add_rms_norm_backward, dcn_add_rms_norm_forward,
                        dcn_clip_grads, dcn_core_backward, dcn_core_forward, dcn_core_forward_proj, dcn_core_output_hw,
-                       dcn_deform_conv_forward, dcn_grad_norm,
+                       dcn_deform_conv_forward, dcn_grad_norm, dcn_proj_adapters_forward,
                        deform_agg_backward,
                        deform_agg_forward, deform_roi_pool_forward, lib)
 
@@ -33,7 +34,7 @@ __all__ = ["dcn_core_forward", "dcn_core_forward_proj", "dcn_deform_conv_forward
            "deform_agg_backward", "deform_roi_pool_forward", "DroiParams", "DCNCoreFunction", "DeformAggFunction", "shard_range", "lib", "DcnError",
            "DcnParams", "DaggParams", "core_params", "EXPORTS", "ABI_VERSION", "dcn_add_rms_norm_forward",
            "dcn_add_rms_norm_backward", "AddRmsNorm", "AddRmsNormFunction", "dcn_grad_norm", "dcn_clip_grads",
-           "GradList", "DnormParams", "DclipParams"]
+           "GradList", "DnormParams", "DclipParams", "dcn_proj_adapters_forward", "DadaptParams"]
 
 
 class DCNCoreFunction(torch.autograd.Function):

@@ -30,7 +30,8 @@ EXPORTS = ("dcn_core_output_hw", "dcn_core_forward", "dcn_core_backward", "defor
            "dcn_selftest_bounded_wait", "dcn_deform_conv_forward", "dcn_probe_rate",
            "dcn_core_forward_proj_workspace_bytes", "dcn_core_forward_proj_noalloc",
            "dcn_add_rms_norm_forward", "dcn_add_rms_norm_backward", "dcn_add_rms_norm_backward_workspace_bytes",
-           "dcn_grad_norm", "dcn_clip_grads", "dcn_grad_norm_workspace_bytes")
+           "dcn_grad_norm", "dcn_clip_grads", "dcn_grad_norm_workspace_bytes",
+           "dcn_proj_adapters_forward", "dcn_proj_adapters_workspace_bytes")
 ABI_VERSION = 2
 
 
@@ -54,6 +55,11 @@ class DroiParams(ctypes.Structure):
 class DnormParams(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("eps", ctypes.c_float)] + \
                [(n, ctypes.c_int32) for n in ("dtype", "quant", "group")]
+
+
+class DadaptParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("cin", "cout", "rank", "num_adapters", "num_requests", "dtype")]
 
 
 class DclipParams(ctypes.Structure):
@@ -118,6 +124,11 @@ def _declare(lib):
         getattr(lib, f).restype = st
     for f in ("dcn_add_rms_norm_backward_workspace_bytes", "dcn_grad_norm_workspace_bytes"):
         getattr(lib, f).restype = ctypes.c_int64
+    R = ctypes.POINTER(DadaptParams)
+    lib.dcn_proj_adapters_forward.argtypes = [R, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp]
+    lib.dcn_proj_adapters_forward.restype = st
+    lib.dcn_proj_adapters_workspace_bytes.argtypes = [R]
+    lib.dcn_proj_adapters_workspace_bytes.restype = ctypes.c_int64
     return lib
 
 
@@ -661,3 +672,48 @@ def dcn_clip_grads(grads, max_norm: float, *, norm_type: float = 2.0, eps: float
     _launch(dev, lib().dcn_clip_grads, ctypes.byref(p), grads._g, grads._n, grads._d, grads._o, grads._od,
             norm.data_ptr(), workspace.data_ptr(), nbytes)
     return norm
+
+
+def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
+                              a: torch.Tensor, b: torch.Tensor, request_start: torch.Tensor,
+                              request_adapter: torch.Tensor, *, scale: Optional[torch.Tensor] = None,
+                              out: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[..., cout] = bias + x . weight^T + scale[i] * (x . a[i]^T) . b[i]^T, i the adapter of the row's
+    request; see dcn_b200.h.
+
+    x is [..., cin], its leading dimensions flattened to rows; weight [cout, cin], a [adapters, rank, cin],
+    b [adapters, cout, rank], scale [adapters] fp32.  Request s owns rows request_start[s] up to
+    request_start[s + 1] (int32 [requests + 1], on the device) and uses adapter request_adapter[s] (int32
+    [requests], -1 for none).  Rows of no request are not written: in a new `out` they hold no value."""
+    _cuda_tensor("x", x)
+    dt, dev = x.dtype, x.device
+    if dt not in _DTYPE_CODE:
+        raise TypeError(f"unsupported dtype {dt}")
+    rows, cin = _rows(x)
+    if weight.dim() != 2 or a.dim() != 3 or b.dim() != 3 or request_adapter.dim() != 1:
+        raise ValueError("weight must be [cout, cin], a [adapters, rank, cin], b [adapters, cout, rank], "
+                         "request_adapter [requests]")
+    cout, (na, rank), nr = weight.shape[0], a.shape[:2], request_adapter.shape[0]
+    _like("weight", weight, (cout, cin), dt, dev)
+    if bias is not None:
+        _like("bias", bias, (cout,), dt, dev)
+    _like("a", a, (na, rank, cin), dt, dev)
+    _like("b", b, (na, cout, rank), dt, dev)
+    _like("request_start", request_start, (nr + 1,), torch.int32, dev)
+    _like("request_adapter", request_adapter, (nr,), torch.int32, dev)
+    if scale is not None:
+        _like("scale", scale, (na,), torch.float32, dev)
+    out = _like_or_new("out", out, x.shape[:-1] + (cout,), dt, dev)
+    p = DadaptParams(rows, cin, cout, rank, na, nr, _DTYPE_CODE[dt])
+    L = lib()
+    if workspace is None:
+        need = L.dcn_proj_adapters_workspace_bytes(ctypes.byref(p))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    else:
+        _cuda_tensor("workspace", workspace)
+    _launch(dev, L.dcn_proj_adapters_forward, ctypes.byref(p), x.data_ptr(), weight.data_ptr(),
+            None if bias is None else bias.data_ptr(), a.data_ptr(), b.data_ptr(),
+            None if scale is None else scale.data_ptr(), request_start.data_ptr(), request_adapter.data_ptr(),
+            out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out

@@ -589,3 +589,65 @@ dcn_status dcn_clip_grads(const dclip_params *p, const void *const *grads, const
 }
 
 }  // extern "C"
+
+namespace {
+
+dcn_status check_adapters(const dadapt_params *p, dcnb::AdapterArgs *a) {
+    if (!p) return fail(DCN_ERR_NULL, "params is NULL");
+    if (p->dtype != DCN_F16 && p->dtype != DCN_BF16)
+        return fail(DCN_ERR_UNSUPPORTED, "the projection with adapters takes fp16 or bf16 (dtype %d)", p->dtype);
+    if (p->rows < 0 || p->cin < 1 || p->cout < 1 || p->rank < 1 || p->num_adapters < 0 || p->num_requests < 0)
+        return fail(DCN_ERR_SHAPE, "cin, cout and rank must be positive, the counts not negative");
+    if (p->cin % 8 || p->cout % 8 || p->rank % 8)
+        return fail(DCN_ERR_UNSUPPORTED, "cin, cout and rank must be multiples of 8 (%d, %d, %d)", p->cin, p->cout, p->rank);
+    if (p->cin > 65536 || p->cout > 65536 || p->rank > 128)
+        return fail(DCN_ERR_UNSUPPORTED, "cin and cout must be at most 65536, rank at most 128");
+    const int64_t big = (int64_t)1 << 30;
+    if (p->rows > big || p->num_requests > kMaxDim || p->num_adapters > kMaxDim ||
+        (int64_t)p->num_adapters * p->cout > big || (int64_t)p->num_adapters * p->rank > big)
+        return fail(DCN_ERR_SHAPE, "a size exceeds its limit");
+    memset(a, 0, sizeof(*a));
+    a->rows = p->rows;
+    a->cin = p->cin; a->cout = p->cout; a->rank = p->rank;
+    a->adapters = p->num_adapters; a->requests = p->num_requests;
+    a->dtype = (dcnb::DType)p->dtype;
+    return DCN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t dcn_proj_adapters_workspace_bytes(const dadapt_params *p) {
+    dcnb::AdapterArgs a;
+    if (check_adapters(p, &a) != DCN_OK) return -1;
+    return (int64_t)dcnb::proj_adapters_workspace(a);
+}
+
+dcn_status dcn_proj_adapters_forward(const dadapt_params *p, const void *x, const void *weight, const void *bias,
+                                     const void *a, const void *b, const float *scale, const int32_t *request_start,
+                                     const int32_t *request_adapter, void *out, void *workspace,
+                                     int64_t workspace_bytes, dcn_stream_t stream) {
+    dcnb::AdapterArgs g;
+    const dcn_status s = check_adapters(p, &g);
+    if (s != DCN_OK) return s;
+    if (workspace_bytes < 0) return fail(DCN_ERR_SHAPE, "workspace_bytes is negative");
+    if (p->rows == 0 || p->num_requests == 0) return DCN_OK;
+    if (!x || !weight || !request_start || !request_adapter || !out || !workspace)
+        return fail(DCN_ERR_NULL, "x, weight, request_start, request_adapter, out and workspace are required");
+    if (p->num_adapters > 0 && (!a || !b)) return fail(DCN_ERR_NULL, "a and b are required with adapters");
+    if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(a, 16) || !aligned(b, 16) ||
+        !aligned(out, 16) || !aligned(workspace, 16))
+        return fail(DCN_ERR_ALIGN, "x, weight, bias, a, b, out and workspace must be 16-byte aligned");
+    if (!aligned(scale, 4) || !aligned(request_start, 4) || !aligned(request_adapter, 4))
+        return fail(DCN_ERR_ALIGN, "scale and the request tables must be 4-byte aligned");
+    const size_t need = dcnb::proj_adapters_workspace(g);
+    if ((size_t)workspace_bytes < need)
+        return fail(DCN_ERR_SHAPE, "workspace has %lld bytes, %zu needed", (long long)workspace_bytes, need);
+    g.x = x; g.weight = weight; g.bias = bias; g.a = a; g.b = b; g.scale = scale;
+    g.start = request_start; g.which = request_adapter;
+    g.out = out; g.workspace = workspace;
+    return cuda_status(dcnb::launch_proj_adapters(g, (cudaStream_t)stream), "dcn_proj_adapters_forward launch");
+}
+
+}  // extern "C"

@@ -93,6 +93,19 @@ struct ClipArgs {
     double *partial;           // grad_clip_partials(num_tensors) values
 };
 
+// Pointwise projection with low-rank adapters of many requests (fp16/bf16).
+struct AdapterArgs {
+    const void *x, *weight, *bias;  // [rows, cin], [cout, cin], [cout] or nullptr
+    const void *a, *b;              // [adapters, rank, cin], [adapters, cout, rank]
+    const float *scale;             // [adapters] or nullptr (ones)
+    const int32_t *start, *which;   // [requests + 1] row starts, [requests] adapters
+    void *out;                      // [rows, cout]
+    void *workspace;                // proj_adapters_workspace() bytes
+    int64_t rows;
+    int cin, cout, rank, adapters, requests;
+    DType dtype;
+};
+
 // Each launcher enqueues its kernel(s) on `stream` and returns the
 // cudaGetLastError() of the launch.
 cudaError_t launch_core_forward_generic(const CoreArgs &a, cudaStream_t stream);
@@ -127,5 +140,7 @@ int norm_backward_partial_rows(int64_t rows, int cols);
 // The norm, with clipping where a.clip, and the partial results that it needs.
 cudaError_t launch_grad_clip(const ClipArgs &a, cudaStream_t stream);
 int64_t grad_clip_partials(int num_tensors);
+cudaError_t launch_proj_adapters(const AdapterArgs &a, cudaStream_t stream);
+size_t proj_adapters_workspace(const AdapterArgs &a);
 
 }  // namespace dcnb

@@ -1,0 +1,31 @@
+// Pieces shared by the kernels of the projection with low-rank adapters: the
+// requests' row ranges and adapters, and the launch interface of the two
+// routes (many rows: dcn_proj_adapters.cu, few rows: dcn_proj_adapters_rows.cu).
+#pragma once
+
+#include "dcn_common.cuh"
+#include "dcn_launch.h"
+
+namespace dcnb {
+
+// Bit of the device error word: a request named an adapter outside [-1, num_adapters).
+enum : unsigned { kDevErrBadAdapter = 2u };
+
+constexpr int kMaxSmallRows = 64;
+
+// Adapter of request s: -1 for none.  An index out of range counts as none.
+__device__ __forceinline__ int adapter_of(const int32_t *which, int s, int num_adapters) {
+    const int a = which[s];
+    return a >= 0 && a < num_adapters ? a : -1;
+}
+
+__device__ __forceinline__ void report_bad_adapter(int a, int num_adapters, unsigned int *err) {
+    if (a < -1 || a >= num_adapters) atomicOr(err, kDevErrBadAdapter);
+}
+
+size_t adapters_small_workspace(const AdapterArgs &a);
+size_t adapters_large_workspace(const AdapterArgs &a);
+cudaError_t launch_adapters_small(const AdapterArgs &a, cudaStream_t stream);
+cudaError_t launch_adapters_large(const AdapterArgs &a, cudaStream_t stream);
+
+}  // namespace dcnb

@@ -287,6 +287,53 @@ dcn_status deform_roi_pool_forward(const droi_params *p, const void *x, const fl
                                    const float *offset, void *out, dcn_stream_t stream);
 
 /*
+ * Pointwise projection with low-rank adapters of many requests beside the
+ * shared weight: the 1x1 projection of dcn_core_forward_proj where every
+ * request (an image, a prompt, a single token) may have fine-tuned it for
+ * itself (the library's own addition).  Row m of request s with adapter
+ * a = request_adapter[s]:
+ *   out[m, :] = bias + W x[m] + scale[a] * B[a] (A[a] x[m])
+ *   x       [rows, cin]               storage dtype (fp16 or bf16)
+ *   weight  [cout, cin]               storage dtype, shared
+ *   bias    [cout]                    storage dtype, or NULL
+ *   a       [num_adapters, rank, cin], b [num_adapters, cout, rank]  storage dtype
+ *   scale   [num_adapters]            fp32, or NULL for ones
+ *   request_start   [num_requests + 1] int32, device memory, ascending: request s
+ *                   owns rows request_start[s] .. request_start[s + 1] - 1 (none, if equal)
+ *   request_adapter [num_requests]     int32, device memory; -1: no adapter
+ *   out     [rows, cout]              storage dtype
+ * Rows before request_start[0] and from request_start[num_requests] on (a
+ * padded batch) are left as they were.  Values of request_start are cut to
+ * [0, rows]; an order that is not ascending gives wrong values but no access
+ * out of range.  An adapter outside [-1, num_adapters) counts as none and sets
+ * bit 1 of the device error word (dcn_take_device_error).
+ * Sums are fp32.  With at most 64 rows A[a] x stays in fp32; with more it is
+ * scaled and rounded once to the storage dtype, as an operand of the second
+ * tensor-core product.  Values of one row do not depend on other requests'.
+ * cin, cout and rank are multiples of 8, cin and cout up to 65536, rank up to
+ * 128; rows up to 2^30; num_requests and num_adapters up to 2^20, with
+ * num_adapters * cout and num_adapters * rank up to 2^30.  x, weight, bias, a, b
+ * and out are 16-byte aligned.  fp32 returns DCN_ERR_UNSUPPORTED.
+ * workspace: dcn_proj_adapters_workspace_bytes(p) bytes, 16-byte aligned; calls
+ * that overlap on the GPU need one each.  rows == 0 or num_requests == 0 is a
+ * no-op; num_adapters may be 0 (a and b may then be NULL).
+ */
+typedef struct {
+    int64_t rows;
+    int32_t cin, cout, rank, num_adapters, num_requests;
+    int32_t dtype; /* dcn_dtype: DCN_F16 or DCN_BF16 */
+} dadapt_params;
+
+dcn_status dcn_proj_adapters_forward(const dadapt_params *p, const void *x, const void *weight,
+                                     const void *bias, const void *a, const void *b, const float *scale,
+                                     const int32_t *request_start, const int32_t *request_adapter,
+                                     void *out, void *workspace, int64_t workspace_bytes,
+                                     dcn_stream_t stream);
+
+/* Workspace bytes of dcn_proj_adapters_forward; -1 for invalid params. */
+int64_t dcn_proj_adapters_workspace_bytes(const dadapt_params *p);
+
+/*
  * Residual addition and root-mean-square norm over the channels of each row,
  * with the output in the storage type, in 8 bits with scales, or both: what
  * follows the projection of a residual block (the library's own addition; the
@@ -403,8 +450,10 @@ const char *dcn_last_error_detail(void);
 
 /* Device-side error word: kernels that wait on their own asynchronous
  * copies bound every wait (1 s); if one ran out the kernel sets bit 0 of this
- * word and returns without finishing its outputs.  This call synchronises
- * the device, returns the word and clears it; -1 if the read itself failed.
+ * word and returns without finishing its outputs.  Bit 1: a request of
+ * dcn_proj_adapters_forward named an adapter that does not exist.  This call
+ * synchronises the device, returns the word and clears it; -1 if the read
+ * itself failed.
  * 0 after every normal run. */
 int32_t dcn_take_device_error(void);
 

@@ -110,3 +110,44 @@ def test_clip_checks(lib):
     assert clip(lib, grads(), outs=(128,)) == B.DCN_ERR_NULL
     assert clip(lib, grads(), outs=(64,), od=(1,)) == B.DCN_ERR_UNSUPPORTED  # in place in another type
     assert lib.dcn_grad_norm(None, None, None, None, 16, 16, 1 << 20, None) == B.DCN_ERR_NULL
+
+
+def adapt(**kw):
+    base = dict(rows=100, cin=64, cout=64, rank=16, num_adapters=3, num_requests=4, dtype=1)
+    base.update(kw)
+    return B.DadaptParams(**base)
+
+
+def proj(lib, p, x=16, w=16, bias=16, a=16, b=16, scale=16, start=16, which=16, out=16, ws=16, nbytes=1 << 30):
+    return lib.dcn_proj_adapters_forward(ctypes.byref(p), x, w, bias, a, b, scale, start, which, out, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=0), B.DCN_ERR_UNSUPPORTED), (dict(rows=-1), B.DCN_ERR_SHAPE), (dict(cin=0), B.DCN_ERR_SHAPE),
+    (dict(cin=60), B.DCN_ERR_UNSUPPORTED), (dict(cout=4), B.DCN_ERR_UNSUPPORTED), (dict(rank=4), B.DCN_ERR_UNSUPPORTED),
+    (dict(rank=136), B.DCN_ERR_UNSUPPORTED), (dict(cin=65544), B.DCN_ERR_UNSUPPORTED),
+    (dict(rows=(1 << 30) + 1), B.DCN_ERR_SHAPE), (dict(num_adapters=1 << 20, cout=2048), B.DCN_ERR_SHAPE),
+    (dict(num_requests=-1), B.DCN_ERR_SHAPE), (dict(num_adapters=-1), B.DCN_ERR_SHAPE),
+])
+def test_adapter_params(lib, kw, status):
+    p = adapt(**kw)
+    assert proj(lib, p) == status
+    assert lib.dcn_proj_adapters_workspace_bytes(ctypes.byref(p)) == -1
+
+
+def test_adapter_pointers(lib):
+    p = adapt()
+    need = lib.dcn_proj_adapters_workspace_bytes(ctypes.byref(p))
+    assert need == 100 * 16 * 2  # many rows: t in the storage type
+    assert lib.dcn_proj_adapters_workspace_bytes(ctypes.byref(adapt(rows=10))) == 10 * (16 + 1) * 4
+    for name in ("x", "w", "start", "which", "out", "ws", "a", "b"):
+        assert proj(lib, p, **{name: None}) == B.DCN_ERR_NULL, name
+    for name in ("x", "w", "bias", "a", "b", "out", "ws"):
+        assert proj(lib, p, **{name: 8}) == B.DCN_ERR_ALIGN, name
+    for name in ("scale", "start", "which"):
+        assert proj(lib, p, **{name: 18}) == B.DCN_ERR_ALIGN, name
+    assert proj(lib, p, nbytes=need - 1) == B.DCN_ERR_SHAPE
+    assert proj(lib, p, nbytes=-1) == B.DCN_ERR_SHAPE
+    assert proj(lib, adapt(rows=0), x=None, out=None) == B.DCN_OK
+    assert proj(lib, adapt(num_requests=0), x=None) == B.DCN_OK
+    assert lib.dcn_proj_adapters_forward(None, 16, 16, 16, 16, 16, 16, 16, 16, 16, 16, 1 << 20, None) == B.DCN_ERR_NULL

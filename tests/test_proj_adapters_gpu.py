@@ -1,0 +1,283 @@
+"""Projection with low-rank adapters of many requests on the GPU against 64 bits.
+
+Tolerance per element (u = 2^-24, uT = finfo(T).eps / 2): the contraction has
+cin + rank products, exact in fp32, and every addition loses at most one step,
+2u of the running sum, which the sum of magnitudes bounds; with more than 64
+rows t = scale * A x is rounded once (uT, and tiny(T) below its normals); the
+result is rounded once.
+"""
+import pytest
+import torch
+
+import deformable_convolution_sampling_dcn_b200 as d
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def make(lens, which, cin, cout, rank, adapters, dtype, seed, bias=True, scale=True, rows=None, first=0):
+    """Inputs on the CPU; `rows` more than the requests cover leaves padding behind, `first` before."""
+    g = torch.Generator().manual_seed(seed)
+    dt = DT[dtype]
+    start = [first]
+    for n in lens:
+        start.append(start[-1] + n)
+    rows = start[-1] if rows is None else rows
+    s = dict(
+        x=torch.randn(rows, cin, generator=g).to(dt), weight=(torch.randn(cout, cin, generator=g) * cin ** -0.5).to(dt),
+        bias=(torch.randn(cout, generator=g) * 0.2).to(dt) if bias else None,
+        a=(torch.randn(adapters, rank, cin, generator=g) * cin ** -0.5).to(dt),
+        b=(torch.randn(adapters, cout, rank, generator=g) * rank ** -0.5).to(dt),
+        scale=(0.5 + torch.rand(adapters, generator=g)) if scale else None,
+        start=torch.tensor(start, dtype=torch.int32), which=torch.tensor(which, dtype=torch.int32))
+    return s
+
+
+def definition(s):
+    """(y, tolerance) in 64 bits."""
+    dt = s["x"].dtype
+    uT = torch.finfo(dt).eps / 2
+    tiny = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
+    x, w = s["x"].double(), s["weight"].double()
+    y, mag = x @ w.t(), x.abs() @ w.abs().t()
+    if s["bias"] is not None:
+        y, mag = y + s["bias"].double(), mag + s["bias"].double().abs()
+    tr = torch.zeros_like(y)
+    start = s["start"].tolist()
+    for i, ad in enumerate(s["which"].tolist()):
+        lo, hi = start[i], start[i + 1]
+        if ad < 0 or ad >= s["a"].shape[0] or lo >= hi:
+            continue
+        sc = float(s["scale"][ad]) if s["scale"] is not None else 1.0
+        a, b = s["a"][ad].double(), s["b"][ad].double()
+        t, tm = sc * (x[lo:hi] @ a.t()), sc * (x[lo:hi].abs() @ a.abs().t())
+        y[lo:hi] += t @ b.t()
+        mag[lo:hi] += tm @ b.abs().t()
+        tr[lo:hi] = (t.abs() * uT + tiny) @ b.abs().t()
+    n = x.shape[1] + s["a"].shape[1] + 16
+    tol = mag * n * 2 * U + y.abs() * uT + tiny
+    if x.shape[0] > 64:
+        tol = tol + tr * (1 + 2 * uT)
+    return y, tol
+
+
+def call(s, dev="cuda", **kw):
+    t = {k: None if v is None else v.to(dev) for k, v in s.items()}
+    return d.dcn_proj_adapters_forward(t["x"], t["weight"], t["bias"], t["a"], t["b"], t["start"], t["which"],
+                                       scale=t["scale"], **kw)
+
+
+def check(s, y, rows=slice(None)):
+    torch.cuda.synchronize()
+    assert d._binding.take_device_error() == 0
+    want, tol = definition(s)
+    err = (y.double().cpu() - want).abs()
+    ok = err <= tol
+    assert ok[rows].all(), (float((err / tol)[rows].max()), int((~ok[rows]).sum()))
+
+
+# rows of each request, adapter of each, cin, cout, rank, adapters
+SMALL = [
+    ([1], [0], 8, 8, 8, 1),
+    ([1], [-1], 64, 64, 16, 1),
+    ([1] * 8, [0, 1, 2, -1, 3, 0, 0, 2], 512, 512, 16, 4),
+    ([1] * 9, [2, 1, 2, 1, 0, 0, 0, 2, -1], 520, 136, 24, 3),
+    ([1] * 17, list(range(16)) + [-1], 1000, 264, 8, 16),
+    ([1] * 48, [i % 7 - 1 for i in range(48)], 2048, 1032, 64, 6),
+    ([3, 0, 5, 0, 0, 20, 4], [1, 0, -1, 2, 1, 0, 1], 256, 128, 128, 3),   # short requests, empty ones
+    ([64], [0], 4096, 256, 32, 1),
+    ([33, 31], [1, 1], 96, 72, 40, 2),
+]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("i", range(len(SMALL)))
+def test_few_rows(i, dtype, cuda_dev):
+    s = make(*SMALL[i], dtype, 10 + i)
+    check(s, call(s))
+
+
+LARGE = [
+    ([65], [0], 64, 64, 16, 1),
+    ([128], [0], 8, 8, 8, 1),
+    ([100, 28, 1], [0, 1, 0], 64, 72, 8, 2),
+    ([1] * 130, [i % 5 - 1 for i in range(130)], 128, 64, 16, 4),           # 128 requests in one tile
+    ([127, 1, 128, 0, 2, 0, 254], [0, -1, 1, 1, 2, 0, 1], 200, 136, 24, 3),  # at, before and behind tile borders
+    ([1600, 1600, 7], [2, -1, 0], 512, 512, 16, 3),
+    ([300, 0, 0, 500, 33], [1, 0, 0, 0, 1], 1000, 520, 64, 2),
+    ([700], [0], 520, 264, 128, 1),                                          # two blocks of rank
+    ([90, 40, 200], [1, 0, 1], 72, 1032, 72, 2),                             # a ragged second block of rank
+    ([20000, 13, 5000], [0, 1, 1], 64, 256, 8, 2),                           # several tiles per CTA
+]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("i", range(len(LARGE)))
+def test_many_rows(i, dtype, cuda_dev):
+    s = make(*LARGE[i], dtype, 30 + i)
+    check(s, call(s))
+
+
+@pytest.mark.parametrize("lens,which", [([5, 6], [0, 1]), ([100, 33], [1, 0])])
+def test_without_bias_or_scale(lens, which, cuda_dev):
+    s = make(lens, which, 136, 80, 16, 2, "f16", 50, bias=False, scale=False)
+    check(s, call(s))
+
+
+@pytest.mark.parametrize("rows,first,lens", [(40, 0, [7, 12]), (40, 5, [7, 12]), (300, 0, [100, 60]),
+                                             (300, 9, [150, 100]), (64, 0, [0, 0]), (500, 0, [0, 0])])
+def test_rows_of_no_request_stay(rows, first, lens, cuda_dev):
+    """Padding before the first and behind the last request is left as it was, whatever x holds there."""
+    s = make(lens, [1, 0], 64, 96, 16, 2, "bf16", 60, rows=rows, first=first)
+    end = first + sum(lens)
+    s["x"][end:] = float("nan")
+    s["x"][:first] = float("inf")
+    out = torch.full((rows, 96), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = call(s, out=out)
+    assert y is out
+    assert (out[:first] == 7).all() and (out[end:] == 7).all()
+    check(s, y, slice(first, end))
+
+
+@pytest.mark.parametrize("lens", [[4, 4, 4], [60, 40, 100]])
+def test_one_requests_infinities_stay_its_own(lens, cuda_dev):
+    """NaN and infinities in one request's rows or adapter reach no other request in the same tile."""
+    s = make(lens, [0, 1, 2], 64, 64, 16, 3, "f16", 70)
+    want, tol = definition(s)
+    lo, hi = lens[0], lens[0] + lens[1]
+    s["a"][1, 3] = float("inf")
+    s["b"][1, 5:9] = float("nan")
+    s["x"][lo, 0] = float("inf")
+    s["x"][hi - 1, 1] = float("nan")
+    y = call(s).double().cpu()
+    others = list(range(lo)) + list(range(hi, sum(lens)))
+    assert ((y - want).abs() <= tol)[others].all()
+    assert not torch.isfinite(y[lo:hi]).all(1).any()
+
+
+def test_bad_adapter_index_is_reported(cuda_dev):
+    for lens in ([3, 4], [100, 90]):
+        s = make(lens, [7, 1], 64, 64, 16, 2, "bf16", 80)
+        y = call(s)
+        torch.cuda.synchronize()
+        assert d._binding.take_device_error() == 2
+        want, tol = definition(s)  # counts it as none
+        assert ((y.double().cpu() - want).abs() <= tol).all()
+        s["which"][0] = -2
+        call(s)
+        torch.cuda.synchronize()
+        assert d._binding.take_device_error() == 2
+        assert d._binding.take_device_error() == 0
+
+
+def test_tables_out_of_range_stay_in_bounds(cuda_dev):
+    """Starts outside [0, rows]: cut off; the rows of the well-formed requests are right."""
+    for rows in (50, 400):
+        s = make([rows // 2, rows - rows // 2], [0, 1], 64, 64, 16, 2, "f16", 81)
+        bad = dict(s, start=torch.tensor([-5, rows // 2, rows + 1000], dtype=torch.int32))
+        y = call(bad)
+        check(s, y)
+
+
+@pytest.mark.parametrize("n", [1024, 1025, 3000])
+def test_many_requests(n, cuda_dev):
+    """Request tables in shared memory and beyond it."""
+    lens = [(i * 7) % 3 for i in range(n)]
+    s = make(lens, [i % 4 - 1 for i in range(n)], 64, 64, 8, 3, "f16", n)
+    check(s, call(s))
+    lens = [1 if i % (n // 40) == 0 else 0 for i in range(n)]  # few rows, many empty requests
+    s = make(lens, [i % 4 - 1 for i in range(n)], 64, 64, 8, 3, "f16", n)
+    assert s["x"].shape[0] <= 64
+    check(s, call(s))
+
+
+def test_no_adapters_and_empty(cuda_dev):
+    for rows in (5, 200):
+        s = make([rows], [-1], 64, 64, 16, 1, "f16", 90)
+        s["a"], s["b"], s["scale"] = s["a"][:0], s["b"][:0], s["scale"][:0]
+        check(s, call(s))
+    s = make([0], [0], 64, 64, 16, 1, "f16", 91)
+    assert call(s).shape == (0, 64)
+    s = make([], [], 64, 64, 16, 1, "f16", 92, rows=10)
+    out = torch.full((10, 64), 3.0, dtype=torch.float16, device="cuda")
+    call(s, out=out)
+    assert (out == 3).all()
+
+
+def test_leading_dimensions(cuda_dev):
+    """A batch of images: requests are its images, each H * W rows."""
+    s = make([30] * 4, [0, 1, -1, 1], 64, 72, 16, 2, "bf16", 93)
+    flat = call(s)
+    s["x"] = s["x"].view(4, 5, 6, 64)
+    y = call(s)
+    assert y.shape == (4, 5, 6, 72) and torch.equal(y.view(120, 72), flat)
+
+
+@pytest.mark.parametrize("lens", [[1] * 20, [200, 100]])
+def test_streams_graphs_and_repeats(lens, cuda_dev):
+    n = len(lens)
+    s = make(lens, [i % 3 - 1 for i in range(n)], 512, 256, 16, 2, "bf16", 94)
+    t = {k: v.cuda() for k, v in s.items()}
+    args = (t["x"], t["weight"], t["bias"], t["a"], t["b"], t["start"], t["which"])
+    want = d.dcn_proj_adapters_forward(*args, scale=t["scale"])
+    check(s, want)
+    assert torch.equal(d.dcn_proj_adapters_forward(*args, scale=t["scale"]), want)
+    # two streams at once, each with its own workspace
+    outs = []
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            outs += [d.dcn_proj_adapters_forward(*args, scale=t["scale"]) for _ in range(5)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    # two captured graphs, replayed in turn after the request table changed
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = d.dcn_proj_adapters_forward(*args, scale=t["scale"])
+        graphs.append((g, o))
+    s["which"] = (s["which"] + 2) % 3 - 1
+    t["which"].copy_(s["which"])
+    for g, o in graphs:
+        o.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    for _, o in graphs:
+        check(s, o)
+
+
+def test_binding_refusals(cuda_dev):
+    s = {k: v.cuda() for k, v in make([4], [0], 64, 64, 16, 1, "f16", 95).items()}
+
+    def go(**kw):
+        t = dict(s, **kw)
+        return d.dcn_proj_adapters_forward(t["x"], t["weight"], t["bias"], t["a"], t["b"], t["start"], t["which"],
+                                           scale=t["scale"], workspace=t.get("ws"))
+
+    with pytest.raises(TypeError):
+        go(weight=s["weight"].bfloat16())
+    with pytest.raises(ValueError):
+        go(weight=s["weight"][:, :32].contiguous())
+    with pytest.raises(ValueError):
+        go(b=s["b"][:, :32].contiguous())
+    with pytest.raises(TypeError):
+        go(start=s["start"].long())
+    with pytest.raises(ValueError):
+        go(start=s["start"][:1])
+    with pytest.raises(TypeError):
+        go(scale=s["scale"].half())
+    with pytest.raises(ValueError, match="CUDA"):
+        go(which=s["which"].cpu())
+    with pytest.raises(d.DcnError):
+        go(ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    f = {k: v.float() if v.is_floating_point() else v for k, v in s.items()}
+    with pytest.raises(d.DcnError) as e:
+        d.dcn_proj_adapters_forward(f["x"], f["weight"], f["bias"], f["a"], f["b"], f["start"], f["which"])
+    assert e.value.status == d._binding.DCN_ERR_UNSUPPORTED
+    odd = {k: v.cuda() for k, v in make([4], [0], 60, 64, 16, 1, "f16", 95).items()}
+    with pytest.raises(d.DcnError):
+        go(**{k: odd[k] for k in ("x", "weight", "a")})
