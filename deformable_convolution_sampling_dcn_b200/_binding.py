@@ -439,29 +439,30 @@ def deform_roi_pool_forward(x, rois, offset, *, pooled=(7, 7), sampling: int = 2
     return out
 
 
-def _launch(device: torch.device, fn, *args) -> None:
-    """fn(*args, stream) on `device` and its current stream; raises on a non-OK status."""
-    if device.index == torch.cuda.current_device():
-        check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+def _launch(index: int, fn, *args) -> None:
+    """fn(*args, stream) on CUDA device `index` and its current stream; raises on a non-OK status.
+
+    The small calls of this section are host-bound (a launch takes 3 us), so the
+    device and stream are read through torch's own C accessors: 0.2 us against
+    2.5 us for torch.cuda.current_stream(device).cuda_stream."""
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != DCN_OK:
+        check(status)
 
 
-def _like(name: str, t: torch.Tensor, shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
-    """Checks an argument that has to have this shape, type and device."""
+def _like(name: str, t: torch.Tensor, shape, dtype: torch.dtype, index: int) -> torch.Tensor:
+    """Checks an argument that has to have this shape and type, on CUDA device `index`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index and \
+            t.is_contiguous():
+        return t
     _cuda_tensor(name, t, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return t
-
-
-def _like_or_new(name, t, shape, dtype, device) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _like(name, t, shape, dtype, device)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
 def _rows(x: torch.Tensor) -> Tuple[int, int]:
@@ -497,7 +498,7 @@ def dcn_add_rms_norm_forward(x: torch.Tensor, residual: Optional[torch.Tensor] =
     returns the statistic that the backward reads.  The buffers default to new
     tensors; residual_out and out may each be x or residual."""
     _cuda_tensor("x", x)
-    dt, dev = x.dtype, x.device
+    dt, dev = x.dtype, x.get_device()
     if dt not in _DTYPE_CODE:
         raise TypeError(f"unsupported dtype {dt}")
     if quant not in _QUANT:
@@ -507,7 +508,8 @@ def dcn_add_rms_norm_forward(x: torch.Tensor, residual: Optional[torch.Tensor] =
     shape = x.shape
     if residual is not None:
         _like("residual", residual, shape, dt, dev)
-        residual_out = _like_or_new("residual_out", residual_out, shape, dt, dev)
+        residual_out = torch.empty_like(x) if residual_out is None else \
+            _like("residual_out", residual_out, shape, dt, dev)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if weight is not None:
@@ -520,14 +522,17 @@ def dcn_add_rms_norm_forward(x: torch.Tensor, residual: Optional[torch.Tensor] =
     else:
         if group not in (0, 128):
             raise ValueError("group must be 0 or 128")
-        out8 = _like_or_new("out8", out8, shape, dt8, dev)
-        scale = _like_or_new("scale", scale, shape[:-1] + ((cols + 127) // 128 if group else 1,), torch.float32, dev)
+        out8 = torch.empty_like(x, dtype=dt8) if out8 is None else _like("out8", out8, shape, dt8, dev)
+        ss = shape[:-1] + ((cols + 127) // 128 if group else 1,)
+        scale = x.new_empty(ss, dtype=torch.float32) if scale is None else _like("scale", scale, ss, torch.float32, dev)
     if code == 0 or keep_out or out is not None:
-        out = _like_or_new("out", out, shape, dt, dev)
+        out = torch.empty_like(x) if out is None else _like("out", out, shape, dt, dev)
         if residual_out is not None and rows and out.data_ptr() == residual_out.data_ptr():
             raise ValueError("out and residual_out are the same buffer")
-    if save_rstd or rstd is not None:
-        rstd = _like_or_new("rstd", rstd, shape[:-1], torch.float32, dev)
+    if rstd is not None:
+        _like("rstd", rstd, shape[:-1], torch.float32, dev)
+    elif save_rstd:
+        rstd = x.new_empty(shape[:-1], dtype=torch.float32)
     p = DnormParams(rows, cols, eps, _DTYPE_CODE[dt], code, group)
     _launch(dev, lib().dcn_add_rms_norm_forward, ctypes.byref(p), x.data_ptr(),
             None if residual is None else residual.data_ptr(), None if weight is None else weight.data_ptr(),
@@ -547,7 +552,7 @@ def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: tor
     grad_x is the gradient of x and of the residual alike.  grad_weight is None
     without a weight.  eps is part of rstd and only checked here."""
     _cuda_tensor("h", h)
-    dt, dev, shape = h.dtype, h.device, h.shape
+    dt, dev, shape = h.dtype, h.get_device(), h.shape
     if dt not in _DTYPE_CODE:
         raise TypeError(f"unsupported dtype {dt}")
     rows, cols = _rows(h)
@@ -555,15 +560,16 @@ def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: tor
     _like("rstd", rstd, shape[:-1], torch.float32, dev)
     if grad_residual_out is not None:
         _like("grad_residual_out", grad_residual_out, shape, dt, dev)
-    grad_x = _like_or_new("grad_x", grad_x, shape, dt, dev)
+    grad_x = torch.empty_like(h) if grad_x is None else _like("grad_x", grad_x, shape, dt, dev)
     p = DnormParams(rows, cols, eps, _DTYPE_CODE[dt], 0, 0)
     ws_ptr, ws_bytes = None, 0
     if weight is not None:
         _like("weight", weight, (cols,), dt, dev)
-        grad_weight = _like_or_new("grad_weight", grad_weight, (cols,), dt, dev)
+        grad_weight = torch.empty_like(weight) if grad_weight is None else \
+            _like("grad_weight", grad_weight, (cols,), dt, dev)
         if workspace is None:
             need = lib().dcn_add_rms_norm_backward_workspace_bytes(ctypes.byref(p))
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            workspace = h.new_empty(max(need, 16), dtype=torch.uint8)
         else:
             _cuda_tensor("workspace", workspace)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -592,7 +598,7 @@ class GradList:
         n = len(self.grads)
         if self.out is not None and len(self.out) != n:
             raise ValueError(f"{len(self.out)} out buffers for {n} gradients")
-        self.device = None
+        self.device = None  # index
         for t in self.grads + (self.out or []):
             if not isinstance(t, torch.Tensor):
                 raise TypeError("gradients and out buffers must be torch.Tensors")
@@ -603,8 +609,8 @@ class GradList:
             if not t.is_contiguous():
                 raise ValueError("gradients and out buffers must be contiguous")
             if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
+                self.device = t.get_device()
+            elif t.get_device() != self.device:
                 raise ValueError("gradients are on different devices")
         spans = []
         for i, g in enumerate(self.grads):
@@ -628,6 +634,15 @@ class GradList:
             self._o = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in self.out])
             self._od = (ctypes.c_int32 * max(n, 1))(*[_DTYPE_CODE[t.dtype] for t in self.out])
         self._ws = int(lib().dcn_grad_norm_workspace_bytes(n))
+        self._protos = None
+
+    def _new(self, index: int):
+        """A norm and a workspace of a call's own (two calls may overlap on the GPU)."""
+        if self._protos is None:  # empty_like of these takes half the time of torch.empty
+            dev = torch.device("cuda", index)
+            self._protos = (torch.empty((), dtype=torch.float32, device=dev),
+                            torch.empty(self._ws, dtype=torch.uint8, device=dev))
+        return torch.empty_like(self._protos[0]), torch.empty_like(self._protos[1])
 
 
 _NORM_KIND = {2: 0, 2.0: 0, float("inf"): 1}
@@ -644,12 +659,14 @@ def _grad_call(grads, out, norm_type, norm, workspace):
     if dev is None:
         if norm is None:
             raise ValueError("no gradients: pass norm, which gives the device")
-        dev = norm.device
-    norm = _like_or_new("norm", norm, (), torch.float32, dev)
-    if workspace is None:
-        workspace = torch.empty(grads._ws, dtype=torch.uint8, device=dev)
-    else:
+        dev = norm.get_device()
+    if norm is not None:
+        _like("norm", norm, (), torch.float32, dev)
+    if workspace is not None:
         _cuda_tensor("workspace", workspace)
+    if norm is None or workspace is None:
+        n, w = grads._new(dev)
+        norm, workspace = n if norm is None else norm, w if workspace is None else workspace
     return grads, dev, norm, workspace, workspace.numel() * workspace.element_size()
 
 
@@ -687,7 +704,7 @@ def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optio
     request_start[s + 1] (int32 [requests + 1], on the device) and uses adapter request_adapter[s] (int32
     [requests], -1 for none).  Rows of no request are not written: in a new `out` they hold no value."""
     _cuda_tensor("x", x)
-    dt, dev = x.dtype, x.device
+    dt, dev = x.dtype, x.get_device()
     if dt not in _DTYPE_CODE:
         raise TypeError(f"unsupported dtype {dt}")
     rows, cin = _rows(x)
@@ -704,12 +721,13 @@ def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optio
     _like("request_adapter", request_adapter, (nr,), torch.int32, dev)
     if scale is not None:
         _like("scale", scale, (na,), torch.float32, dev)
-    out = _like_or_new("out", out, x.shape[:-1] + (cout,), dt, dev)
+    shape = x.shape[:-1] + (cout,)
+    out = x.new_empty(shape) if out is None else _like("out", out, shape, dt, dev)
     p = DadaptParams(rows, cin, cout, rank, na, nr, _DTYPE_CODE[dt])
     L = lib()
     if workspace is None:
         need = L.dcn_proj_adapters_workspace_bytes(ctypes.byref(p))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = x.new_empty(max(need, 16), dtype=torch.uint8)
     else:
         _cuda_tensor("workspace", workspace)
     _launch(dev, L.dcn_proj_adapters_forward, ctypes.byref(p), x.data_ptr(), weight.data_ptr(),

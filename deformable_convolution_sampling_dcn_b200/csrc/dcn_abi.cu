@@ -508,7 +508,7 @@ dcn_status dcn_add_rms_norm_forward(const dnorm_params *p, const void *x, const 
 
 int64_t dcn_add_rms_norm_backward_workspace_bytes(const dnorm_params *p) {
     if (check_norm(p) != DCN_OK) return -1;
-    return (int64_t)dcnb::norm_backward_partial_rows(p->rows, p->cols) * p->cols * 4;
+    return (int64_t)dcnb::norm_backward_partial_rows(p->rows, p->cols, (dcnb::DType)p->dtype) * p->cols * 4;
 }
 
 dcn_status dcn_add_rms_norm_backward(const dnorm_params *p, const void *grad_out, const void *h, const float *rstd,
@@ -532,7 +532,7 @@ dcn_status dcn_add_rms_norm_backward(const dnorm_params *p, const void *grad_out
         !aligned(rstd, 4))
         return fail(DCN_ERR_ALIGN, "tensors must be aligned to their element");
     dcnb::NormArgs a = norm_args(p);
-    a.partial_rows = dcnb::norm_backward_partial_rows(p->rows, p->cols);
+    a.partial_rows = dcnb::norm_backward_partial_rows(p->rows, p->cols, (dcnb::DType)p->dtype);
     if (grad_weight) {
         if (!workspace) return fail(DCN_ERR_NULL, "workspace is required with a weight");
         if (!aligned(workspace, 16)) return fail(DCN_ERR_ALIGN, "workspace must be 16-byte aligned");

@@ -136,7 +136,7 @@ cudaError_t launch_roi_pool_forward(const RoiArgs &a, cudaStream_t stream);
 cudaError_t launch_norm_forward(const NormArgs &a, cudaStream_t stream);
 // The backward, and the rows of partial weight gradients that it needs.
 cudaError_t launch_norm_backward(const NormArgs &a, cudaStream_t stream);
-int norm_backward_partial_rows(int64_t rows, int cols);
+int norm_backward_partial_rows(int64_t rows, int cols, DType dtype);
 // The norm, with clipping where a.clip, and the partial results that it needs.
 cudaError_t launch_grad_clip(const ClipArgs &a, cudaStream_t stream);
 int64_t grad_clip_partials(int num_tensors);

@@ -177,11 +177,8 @@ template <typename T, int TPR, int NV, bool AL>
 cudaError_t launch_one(const NormArgs &a, int threads, const DeviceInfo *dev, cudaStream_t stream) {
     const int teams = TPR == 0 ? 1 : threads / TPR;
     const long long need = (a.rows + teams - 1) / teams;
-    int per_sm = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, norm_forward_kernel<T, TPR, NV, AL>,
-                                                                  threads, 0);
-    if (e != cudaSuccess) return e;
-    const long long most = (long long)dev->sms * (per_sm < 1 ? 1 : per_sm);
+    // 2048 threads an SM (the kernels stay below 64 registers, at 32 and fewer they all fit)
+    const long long most = (long long)dev->sms * (2048 / threads);
     norm_forward_kernel<T, TPR, NV, AL><<<(unsigned)(need < most ? need : most), threads, 0, stream>>>(a);
     return cudaGetLastError();
 }

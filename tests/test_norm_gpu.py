@@ -213,9 +213,10 @@ def backward_definition(gy, h, rstd, w, gh):
 
 
 def rows_in_a_chain(rows):
-    """fp32 additions that one partial sum of the weight gradient can see: its rows, up to 32 teams of a
-    CTA, the 592 / 16 rows of partial sums per thread and 16 threads, 4 roundings per term."""
-    return -(-rows // min(rows, 592)) + 32 + 37 + 16 + 4
+    """fp32 additions that one partial sum of the weight gradient can see: its rows (at least 148 CTAs share
+    many rows, one CTA takes few), 2 shuffles and 16 warps of a CTA, 1184 / 128 rows of partial sums per
+    thread and 7 tree levels, 4 roundings per term."""
+    return -(-rows // 148) + 64 + 2 + 16 + 10 + 7 + 4
 
 
 def check_backward(rows, cols, dtype, seed, weight=True, residual=True):
