@@ -139,7 +139,8 @@ def test_adapter_pointers(lib):
     p = adapt()
     need = lib.dcn_proj_adapters_workspace_bytes(ctypes.byref(p))
     assert need == 100 * 16 * 2  # many rows: t in the storage type
-    assert lib.dcn_proj_adapters_workspace_bytes(ctypes.byref(adapt(rows=10))) == 10 * (16 + 1) * 4
+    # few rows: t in fp32, and fp32 partial sums of 16 rows for one block of the weight
+    assert lib.dcn_proj_adapters_workspace_bytes(ctypes.byref(adapt(rows=10))) == (10 * 16 + 2 * 16 * 128) * 4
     for name in ("x", "w", "start", "which", "out", "ws", "a", "b"):
         assert proj(lib, p, **{name: None}) == B.DCN_ERR_NULL, name
     for name in ("x", "w", "bias", "a", "b", "out", "ws"):
