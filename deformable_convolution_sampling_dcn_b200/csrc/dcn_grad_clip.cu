@@ -4,15 +4,20 @@
 //
 // The host hands the tensors over as a table in the kernel's parameters (no
 // copy, no device allocation; a captured graph keeps it).  Tensors are cut
-// into chunks of kChunk elements, aligned to 16 bytes of the gradient's own
-// address, and the CTAs take chunks in turn.  The first kernel leaves one
-// partial result per CTA, the second adds the partial results in a fixed
-// order (no atomics: the norm is the same from run to run), derives c and
-// rewrites the gradients.
+// into chunks of 1024 16-byte vectors, four for each thread of a CTA, aligned
+// to 16 bytes of the gradient's own address; every CTA takes a contiguous run
+// of chunks, so it looks its first tensor up once and walks on from there.
+// The first kernel leaves one partial result per CTA, the second adds the
+// partial results in a fixed order (no atomics: the norm is the same from run
+// to run), derives c and rewrites the gradients.
 //
-// The squares of bf16 and fp32 gradients leave the range of fp32 (1e-23^2
-// underflows, 1e20^2 overflows), so they are formed and summed in fp64; fp16
-// squares and their per-thread sums fit fp32.
+// Bound: device memory, the gradients being read twice.  The second pass walks
+// the runs backwards and starts with what the first pass read last, which L2
+// still holds.
+//
+// The squares of a vector (4 fp32, exact 8 of 16 bits) are added in fp32, the
+// vectors in fp64.  Where that sum leaves [2^-90, 2^125) the squares are formed
+// in fp64 instead: 1e-23^2 underflows fp32 and 1e20^2 overflows it.
 #include <math_constants.h>
 
 #include "dcn_device.h"
@@ -22,9 +27,11 @@
 namespace dcnb {
 namespace {
 
-constexpr int kChunk = 16384;      // elements
 constexpr int kThreads = 256;
-constexpr int kMaxCtas = 1184;     // 8 x 148
+constexpr int kUnroll = 4;         // vectors of a thread in a chunk, all in flight at once
+constexpr int kChunkVecs = kThreads * kUnroll;
+constexpr int kMaxCtas = 1184;     // of the norm: 8 on each of 148 SMs, all resident
+constexpr int kScaleCtas = 888;    // of the scaling: 6 (its registers allow no more)
 
 struct Entry {
     const void *g;
@@ -58,36 +65,54 @@ template <typename T> __host__ __device__ __forceinline__ int shift_of(const voi
     return (int)((reinterpret_cast<uintptr_t>(p) % 16) / sizeof(T));
 }
 
-template <typename T> struct Acc {
-    using type = double;
-};
-template <> struct Acc<__half> {
-    using type = float;
-};
-
-// Partial result of elements [v0, v0 + kChunk) of the shifted grid.
-template <typename T, bool INF> __device__ __forceinline__ double chunk_norm(const T *g, int64_t n, int64_t v0) {
+// The kUnroll vectors of this thread in the chunk that starts at vector q0 of the shifted grid.
+template <typename T> __device__ __forceinline__ void load_chunk(const T *g, int64_t n, int64_t q0, uint4 *v) {
     constexpr int VEC = Storage<T>::kVec;
     const int sh = shift_of<T>(g);
-    const T *base = g - sh;  // 16-byte aligned; elements before g are never read
-    typename Acc<T>::type s = 0;
-    float m = 0.0f;
+    const T *base = g - sh;  // 16-byte aligned; elements before g and past its end are never read
     const int64_t end = n + sh;
-    for (int64_t v = v0 + threadIdx.x * VEC; v < v0 + kChunk && v < end; v += kThreads * VEC) {
-        float f[VEC];
-        if (v >= sh && v + VEC <= end) {
-            unpack16<T>(*reinterpret_cast<const uint4 *>(base + v), f);
-        } else {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) f[j] = (v + j >= sh && v + j < end) ? to_f32(base[v + j]) : 0.0f;
-        }
+    for (int i = 0; i < kUnroll; ++i) {
+        const int64_t e = (q0 + i * kThreads + threadIdx.x) * VEC;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (e >= sh && e + VEC <= end) {
+            v[i] = *reinterpret_cast<const uint4 *>(base + e);
+        } else if (e < end) {
+            T t[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            if (INF) m = max_nan(m, fabsf(f[j]));
-            else s += (typename Acc<T>::type)f[j] * (typename Acc<T>::type)f[j];
+            for (int j = 0; j < VEC; ++j) t[j] = e + j >= sh && e + j < end ? base[e + j] : from_f32<T>(0.0f);
+            v[i] = *reinterpret_cast<uint4 *>(t);
         }
     }
-    return INF ? (double)m : (double)s;
+}
+
+// Partial result of a chunk.
+template <typename T, bool INF> __device__ __forceinline__ double chunk_norm(const T *g, int64_t n, int64_t q0) {
+    constexpr int VEC = Storage<T>::kVec;
+    uint4 v[kUnroll];
+    load_chunk<T>(g, n, q0, v);
+    double s = 0.0;
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        float f[VEC];
+        unpack16<T>(v[i], f);
+        if (INF) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) m = max_nan(m, fabsf(f[j]));
+        } else {
+            float q = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) q = fmaf(f[j], f[j], q);
+            if (q >= 0x1p-90f && q < 0x1p125f) {
+                s += (double)q;
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) s += (double)f[j] * (double)f[j];
+            }
+        }
+    }
+    return INF ? (double)m : s;
 }
 
 __device__ __forceinline__ double combine(double a, double b, bool inf) {
@@ -107,18 +132,26 @@ __device__ __forceinline__ double cta_combine(double v, bool inf) {
     return v;
 }
 
+// The chunks of CTA b of n: [chunks * b / n, chunks * (b + 1) / n).
+__device__ __forceinline__ uint32_t run_begin(uint32_t chunks, uint32_t b, uint32_t n) {
+    return (uint32_t)((uint64_t)chunks * b / n);
+}
+
 template <int CAP, bool INF>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ Table<CAP> t, double *partial) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t chunks = t.e[t.count - 1].end_chunk;
+    const uint32_t c0 = run_begin(chunks, blockIdx.x, gridDim.x), c1 = run_begin(chunks, blockIdx.x + 1, gridDim.x);
     double s = 0.0;
-    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int i = find_entry(t, c);
+    int i = find_entry(t, c0);
+    for (uint32_t c = c0; c < c1; ++c) {
+        while (t.e[i].end_chunk <= c) ++i;
         const Entry &e = t.e[i];
-        const int64_t v0 = (int64_t)(c - (i ? t.e[i - 1].end_chunk : 0)) * kChunk;
+        const int64_t q0 = (int64_t)(c - (i ? t.e[i - 1].end_chunk : 0)) * kChunkVecs;
         double p;
-        if (e.gt == (int)DType::F32) p = chunk_norm<float, INF>(static_cast<const float *>(e.g), e.n, v0);
-        else if (e.gt == (int)DType::F16) p = chunk_norm<__half, INF>(static_cast<const __half *>(e.g), e.n, v0);
-        else p = chunk_norm<__nv_bfloat16, INF>(static_cast<const __nv_bfloat16 *>(e.g), e.n, v0);
+        if (e.gt == (int)DType::F32) p = chunk_norm<float, INF>(static_cast<const float *>(e.g), e.n, q0);
+        else if (e.gt == (int)DType::F16) p = chunk_norm<__half, INF>(static_cast<const __half *>(e.g), e.n, q0);
+        else p = chunk_norm<__nv_bfloat16, INF>(static_cast<const __nv_bfloat16 *>(e.g), e.n, q0);
         s = combine(s, p, INF);
     }
     s = cta_combine(s, INF);
@@ -128,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
 // The norm from the partial results, by every thread of a CTA.
 __device__ __forceinline__ float total_norm(const double *partial, int n, bool inf) {
     double v = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) v = combine(v, partial[i], inf);
+    for (int i = threadIdx.x; i < n; i += kThreads) v = combine(v, __ldcg(partial + i), inf);
     v = cta_combine(v, inf);
     return (float)(inf ? v : sqrt(v));
 }
@@ -138,65 +171,80 @@ __global__ void __launch_bounds__(kThreads) grad_norm_final_kernel(const double 
     if (threadIdx.x == 0) *norm = v;
 }
 
+// A vector's VEC products as storage type O: one store of 8, 16 or 32 bytes (whole sectors of L2 for a warp).
+template <typename O, int VEC> __device__ __forceinline__ void store_vec(O *dst, const float *f) {
+    constexpr int OV = Storage<O>::kVec;
+    if constexpr (VEC == 2 * OV) {
+        const uint4 lo = pack16<O>(f), hi = pack16<O>(f + OV);
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(lo.x), "r"(lo.y), "r"(lo.z),
+                     "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                     : "memory");
+    } else if constexpr (VEC == OV) {
+        *reinterpret_cast<uint4 *>(dst) = pack16<O>(f);
+    } else {
+        float h[OV] = {};
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) h[j] = f[j];
+        const uint4 p = pack16<O>(h);
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(p.x, p.y);
+    }
+}
+
 template <typename T, typename O>
-__device__ __forceinline__ void chunk_scale(const T *g, O *out, int64_t n, int64_t v0, float coef) {
-    constexpr int VEC = Storage<T>::kVec, OV = Storage<O>::kVec;
+__device__ __forceinline__ void chunk_scale(const T *g, O *out, int64_t n, int64_t q0, float coef) {
+    constexpr int VEC = Storage<T>::kVec, OB = VEC * (int)sizeof(O);  // bytes of a vector's store
+    uint4 v[kUnroll];
+    load_chunk<T>(g, n, q0, v);
     const int sh = shift_of<T>(g);
-    const T *base = g - sh;
-    O *obase = out - sh;
-    const bool wide = reinterpret_cast<uintptr_t>(obase) % (VEC * sizeof(O) < 16 ? VEC * sizeof(O) : 16) == 0;
     const int64_t end = n + sh;
-    for (int64_t v = v0 + threadIdx.x * VEC; v < v0 + kChunk && v < end; v += kThreads * VEC) {
-        if (wide && v >= sh && v + VEC <= end) {
-            float f[VEC];
-            unpack16<T>(*reinterpret_cast<const uint4 *>(base + v), f);
+    const bool wide = (reinterpret_cast<uintptr_t>(out) - sh * sizeof(O)) % OB == 0;
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) f[j] *= coef;
-            if constexpr (VEC >= OV) {
+    for (int i = 0; i < kUnroll; ++i) {
+        const int64_t e = (q0 + i * kThreads + threadIdx.x) * VEC;
+        if (e >= end) break;
+        float f[VEC];
+        unpack16<T>(v[i], f);
 #pragma unroll
-                for (int j = 0; j < VEC / OV; ++j)
-                    reinterpret_cast<uint4 *>(obase + v)[j] = pack16<O>(f + j * OV);
-            } else {  // fp32 gradients into 16-bit buffers: 8 bytes
-                float h[OV] = {};
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) h[j] = f[j];
-                const uint4 p = pack16<O>(h);
-                *reinterpret_cast<uint2 *>(obase + v) = make_uint2(p.x, p.y);
-            }
+        for (int j = 0; j < VEC; ++j) f[j] *= coef;
+        O *dst = out + (e - sh);
+        if (wide && e >= sh && e + VEC <= end) {
+            store_vec<O, VEC>(dst, f);
         } else {
 #pragma unroll
             for (int j = 0; j < VEC; ++j)
-                if (v + j >= sh && v + j < end) obase[v + j] = from_f32<O>(to_f32(base[v + j]) * coef);
+                if (e + j >= sh && e + j < end) dst[j] = from_f32<O>(f[j]);
         }
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void chunk_scale_to(const Entry &e, int64_t v0, float coef) {
+template <typename T> __device__ __forceinline__ void chunk_scale_to(const Entry &e, int64_t q0, float coef) {
     const T *g = static_cast<const T *>(e.g);
-    if (e.ot == (int)DType::F32) chunk_scale<T, float>(g, static_cast<float *>(e.out), e.n, v0, coef);
-    else if (e.ot == (int)DType::F16) chunk_scale<T, __half>(g, static_cast<__half *>(e.out), e.n, v0, coef);
-    else chunk_scale<T, __nv_bfloat16>(g, static_cast<__nv_bfloat16 *>(e.out), e.n, v0, coef);
+    if (e.ot == (int)DType::F32) chunk_scale<T, float>(g, static_cast<float *>(e.out), e.n, q0, coef);
+    else if (e.ot == (int)DType::F16) chunk_scale<T, __half>(g, static_cast<__half *>(e.out), e.n, q0, coef);
+    else chunk_scale<T, __nv_bfloat16>(g, static_cast<__nv_bfloat16 *>(e.out), e.n, q0, coef);
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
     grad_scale_kernel(const __grid_constant__ Table<CAP> t, const double *partial, int n_partial, int inf,
                       float max_norm, float eps, float *norm, int write_norm) {
+    const uint32_t chunks = t.e[t.count - 1].end_chunk;
+    const uint32_t c0 = run_begin(chunks, blockIdx.x, gridDim.x), c1 = run_begin(chunks, blockIdx.x + 1, gridDim.x);
+    int i = find_entry(t, c1 - 1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results
     const float total = total_norm(partial, n_partial, inf != 0);
     if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
     const float q = max_norm / (total + eps);
     const float coef = q > 1.0f ? 1.0f : q;  // a NaN norm gives NaN gradients
-    const uint32_t chunks = t.e[t.count - 1].end_chunk;
-    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-        const int i = find_entry(t, c);
+    for (uint32_t c = c1; c-- > c0;) {
+        while (i && t.e[i - 1].end_chunk > c) --i;
         const Entry &e = t.e[i];
         // in place, a factor of one changes nothing
         if (coef == 1.0f && e.g == e.out && e.gt == e.ot) continue;
-        const int64_t v0 = (int64_t)(c - (i ? t.e[i - 1].end_chunk : 0)) * kChunk;
-        if (e.gt == (int)DType::F32) chunk_scale_to<float>(e, v0, coef);
-        else if (e.gt == (int)DType::F16) chunk_scale_to<__half>(e, v0, coef);
-        else chunk_scale_to<__nv_bfloat16>(e, v0, coef);
+        const int64_t q0 = (int64_t)(c - (i ? t.e[i - 1].end_chunk : 0)) * kChunkVecs;
+        if (e.gt == (int)DType::F32) chunk_scale_to<float>(e, q0, coef);
+        else if (e.gt == (int)DType::F16) chunk_scale_to<__half>(e, q0, coef);
+        else chunk_scale_to<__nv_bfloat16>(e, q0, coef);
     }
 }
 
@@ -204,8 +252,9 @@ size_t type_size(DType t) { return t == DType::F32 ? 4 : 2; }
 
 uint32_t chunks_of(const ClipArgs &a, int i) {
     if (a.numel[i] == 0) return 0;
-    const int64_t sh = (int64_t)((reinterpret_cast<uintptr_t>(a.grads[i]) % 16) / type_size((DType)a.dtypes[i]));
-    return (uint32_t)((a.numel[i] + sh + kChunk - 1) / kChunk);
+    const int64_t es = (int64_t)type_size((DType)a.dtypes[i]);
+    const int64_t bytes = a.numel[i] * es + (int64_t)(reinterpret_cast<uintptr_t>(a.grads[i]) % 16);
+    return (uint32_t)((bytes + kChunkVecs * 16 - 1) / (kChunkVecs * 16));
 }
 
 // Fills a table with the non-empty tensors from `first` on; returns the next tensor.
@@ -228,9 +277,9 @@ template <int CAP> int fill(const ClipArgs &a, int first, Table<CAP> &t) {
     return i;
 }
 
-template <int CAP> int grid_of(const Table<CAP> &t) {
+template <int CAP> int grid_of(const Table<CAP> &t, int most) {
     const uint32_t c = t.e[t.count - 1].end_chunk;
-    return (int)(c < (uint32_t)kMaxCtas ? c : (uint32_t)kMaxCtas);
+    return (int)(c < (uint32_t)most ? c : (uint32_t)most);
 }
 
 template <int CAP> cudaError_t run(const ClipArgs &a, cudaStream_t stream) {
@@ -240,7 +289,7 @@ template <int CAP> cudaError_t run(const ClipArgs &a, cudaStream_t stream) {
     for (int i = 0; i < a.num_tensors;) {
         i = fill(a, i, t);
         if (!t.count) break;
-        const int grid = grid_of(t);
+        const int grid = grid_of(t, kMaxCtas);
         if (a.inf) grad_norm_kernel<CAP, true><<<grid, kThreads, 0, stream>>>(t, a.partial + n_partial);
         else grad_norm_kernel<CAP, false><<<grid, kThreads, 0, stream>>>(t, a.partial + n_partial);
         const cudaError_t e = cudaGetLastError();
@@ -257,9 +306,19 @@ template <int CAP> cudaError_t run(const ClipArgs &a, cudaStream_t stream) {
         if (tables > 1 || !first) i = fill(a, i, t);
         else i = a.num_tensors;  // the one table is still there
         if (!t.count) break;
-        grad_scale_kernel<CAP><<<grid_of(t), kThreads, 0, stream>>>(t, a.partial, n_partial, a.inf, a.max_norm, a.eps,
-                                                                  a.norm, first);
-        const cudaError_t e = cudaGetLastError();
+        // a programmatic dependent: it reads nothing that the norm kernel writes before its wait, and writes
+        // nothing before it either
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)grid_of(t, kScaleCtas));
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, grad_scale_kernel<CAP>, t, (const double *)a.partial, n_partial,
+                                                 (int)a.inf, a.max_norm, a.eps, a.norm, first);
         if (e != cudaSuccess) return e;
         first = 0;
     }

@@ -410,15 +410,15 @@ int64_t dcn_add_rms_norm_backward_workspace_bytes(const dnorm_params *p);
  * grads, outs, numel and the dtype arrays are HOST arrays of num_tensors
  * entries, read during the call (a captured graph keeps their contents); the
  * pointers in them are device pointers to dense buffers aligned to their
- * element.  outs NULL: in place.  Otherwise out_dtypes names the type of each
+ * element, of at most 2^40 elements in all.  outs NULL: in place.  Otherwise out_dtypes names the type of each
  * out buffer (an fp32 master gradient of a 16-bit gradient, say), and a buffer
  * may be its own gradient's.  Buffers must not overlap otherwise, nor occur
  * twice.  A tensor with numel 0 is skipped (its pointers may be NULL).
  * *norm (device, fp32) receives N; no element at all gives 0.  A NaN gradient
  * gives a NaN norm and NaN gradients, an infinite one an infinite norm and
- * c = 0.  In place with c = 1 nothing is written.  Squares and sums of fp32
- * and bf16 gradients are formed in fp64, those of fp16 in fp32 per thread and
- * fp64 above; the order is fixed, so equal calls give equal bits.
+ * c = 0.  In place with c = 1 nothing is written.  The squares of 16 bytes of
+ * gradients are added in fp32 (in fp64 where they would leave its range), all
+ * else in fp64; the order is fixed, so equal calls give equal bits.
  * workspace: dcn_grad_norm_workspace_bytes(num_tensors) bytes, 16-byte
  * aligned; calls that overlap on the GPU need one each.
  */

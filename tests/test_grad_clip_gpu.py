@@ -1,9 +1,9 @@
 """Global gradient norm and clipping on the GPU against 64 bits.
 
-Tolerances (u = 2^-24): the norm of fp32 and bf16 tensors is summed in fp64 and
-rounded once: 2u.  fp16 squares are summed in fp32 over at most 64 values per
-thread before fp64: 66u on the sum, 33u on the root.  The factor adds 3
-roundings, the product one, a 16-bit output half a step.
+Tolerances (u = 2^-24): 4 fp32 squares, fused into their sum, are added in fp32
+(at most 4u of the sum), or 8 exact squares of 16 bits (7u); everything above is
+fp64 and the root is rounded once: at most 3.5u + u on the norm.  The factor
+adds 3 roundings, the product one, a 16-bit output half a step.
 """
 import math
 
@@ -32,7 +32,7 @@ def norm64(ts, kind=2.0):
 
 
 def norm_tol(dt):
-    return 35 * U if dt == torch.float16 else 2 * U
+    return 5 * U
 
 
 def check_clip(ts, got, norm, max_norm, eps, out_dt, tol_n):
@@ -96,9 +96,9 @@ def test_table_sizes(n, cuda_dev):
     ts = tensors(sizes, torch.float32, n)
     gs = [t.cuda() for t in ts]
     lst = d.GradList(gs)
-    assert abs(float(d.dcn_grad_norm(lst)) - norm64(ts)) <= 2 * U * norm64(ts)
+    assert abs(float(d.dcn_grad_norm(lst)) - norm64(ts)) <= 5 * U * norm64(ts)
     norm = d.dcn_clip_grads(lst, 0.1)
-    check_clip(ts, gs, norm, 0.1, 1e-6, torch.float32, 2 * U)
+    check_clip(ts, gs, norm, 0.1, 1e-6, torch.float32, 5 * U)
 
 
 def test_mixed_types(cuda_dev):
@@ -106,10 +106,10 @@ def test_mixed_types(cuda_dev):
     gs = [t.cuda() for t in ts]
     norm = d.dcn_clip_grads(gs, 1.0)
     n = norm64(ts)
-    assert abs(float(norm) - n) <= 35 * U * n
+    assert abs(float(norm) - n) <= 5 * U * n
     for t, g in zip(ts, gs):
         want = t.double() / (n + 1e-6)
-        assert ((g.double().cpu() - want).abs() <= want.abs() * (torch.finfo(t.dtype).eps / 2 + 45 * U) + 1e-7).all()
+        assert ((g.double().cpu() - want).abs() <= want.abs() * (torch.finfo(t.dtype).eps / 2 + 12 * U) + 1e-7).all()
 
 
 @pytest.mark.parametrize("dtype", list(DT))
@@ -128,7 +128,7 @@ def test_magnitudes_outside_fp32_squares(cuda_dev):
         for v in (1e-30, 1e25):
             t = torch.full((30000,), v).to(dt)
             n = norm64([t])
-            assert abs(float(d.dcn_grad_norm([t.cuda()])) - n) <= 2 * U * n
+            assert abs(float(d.dcn_grad_norm([t.cuda()])) - n) <= 5 * U * n
 
 
 def test_non_finite(cuda_dev):
@@ -179,12 +179,12 @@ def test_repeats_bit_for_bit_streams_and_graphs(cuda_dev):
         graphs.append((g, n))
     graphs[0][0].replay()
     torch.cuda.synchronize()
-    check_clip(ts, gs, graphs[0][1], 1.0, 1e-6, torch.float32, 2 * U)
+    check_clip(ts, gs, graphs[0][1], 1.0, 1e-6, torch.float32, 5 * U)
     for g, t in zip(gs, ts):
         g.copy_(t * 3)
     graphs[1][0].replay()
     torch.cuda.synchronize()
-    check_clip([t * 3 for t in ts], gs, graphs[1][1], 1.0, 1e-6, torch.float32, 2 * U)
+    check_clip([t * 3 for t in ts], gs, graphs[1][1], 1.0, 1e-6, torch.float32, 5 * U)
 
 
 def test_more_than_32_bit_elements(cuda_dev):
