@@ -9,6 +9,7 @@ is no CPU path.  If the shared library is missing the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional, Sequence, Tuple
@@ -137,6 +138,8 @@ def lib(path: Optional[str] = None):
     global _lib
     if path is not None:
         return _declare(ctypes.CDLL(path))
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -456,7 +459,7 @@ def _launch(index: int, fn, *args) -> None:
 
 def _like(name: str, t: torch.Tensor, shape, dtype: torch.dtype, index: int) -> torch.Tensor:
     """Checks an argument that has to have this shape and type, on CUDA device `index`."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index and \
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape and \
             t.is_contiguous():
         return t
     _cuda_tensor(name, t, dtype)
@@ -466,10 +469,10 @@ def _like(name: str, t: torch.Tensor, shape, dtype: torch.dtype, index: int) -> 
 
 
 def _rows(x: torch.Tensor) -> Tuple[int, int]:
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    if not shape or shape[-1] < 1:
         raise ValueError("x must be [..., cols] with at least one column")
-    cols = x.shape[-1]
-    return x.numel() // cols, cols
+    return x.numel() // shape[-1], shape[-1]
 
 
 class AddRmsNorm(NamedTuple):
@@ -691,6 +694,12 @@ def dcn_clip_grads(grads, max_norm: float, *, norm_type: float = 2.0, eps: float
     return norm
 
 
+@functools.lru_cache(maxsize=1024)
+def _adapters_workspace_bytes(*sizes) -> int:
+    """Workspace of a problem of these sizes (a function of them alone); 16 where they are refused."""
+    return max(16, lib().dcn_proj_adapters_workspace_bytes(ctypes.byref(DadaptParams(*sizes))))
+
+
 def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],
                               a: torch.Tensor, b: torch.Tensor, request_start: torch.Tensor,
                               request_adapter: torch.Tensor, *, scale: Optional[torch.Tensor] = None,
@@ -708,10 +717,10 @@ def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optio
     if dt not in _DTYPE_CODE:
         raise TypeError(f"unsupported dtype {dt}")
     rows, cin = _rows(x)
-    if weight.dim() != 2 or a.dim() != 3 or b.dim() != 3 or request_adapter.dim() != 1:
-        raise ValueError("weight must be [cout, cin], a [adapters, rank, cin], b [adapters, cout, rank], "
-                         "request_adapter [requests]")
-    cout, (na, rank), nr = weight.shape[0], a.shape[:2], request_adapter.shape[0]
+    ws, sa, sr = weight.shape, a.shape, request_adapter.shape
+    if len(ws) != 2 or len(sa) != 3 or len(sr) != 1:
+        raise ValueError("weight must be [cout, cin], a [adapters, rank, cin], request_adapter [requests]")
+    cout, na, rank, nr = ws[0], sa[0], sa[1], sr[0]
     _like("weight", weight, (cout, cin), dt, dev)
     if bias is not None:
         _like("bias", bias, (cout,), dt, dev)
@@ -722,12 +731,15 @@ def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optio
     if scale is not None:
         _like("scale", scale, (na,), torch.float32, dev)
     shape = x.shape[:-1] + (cout,)
-    out = x.new_empty(shape) if out is None else _like("out", out, shape, dt, dev)
-    p = DadaptParams(rows, cin, cout, rank, na, nr, _DTYPE_CODE[dt])
+    if out is not None:
+        _like("out", out, shape, dt, dev)
+    else:
+        out = torch.empty_like(x) if cout == cin else x.new_empty(shape)
+    sizes = (rows, cin, cout, rank, na, nr, _DTYPE_CODE[dt])
+    p = DadaptParams(*sizes)
     L = lib()
     if workspace is None:
-        need = L.dcn_proj_adapters_workspace_bytes(ctypes.byref(p))
-        workspace = x.new_empty(max(need, 16), dtype=torch.uint8)
+        workspace = x.new_empty(_adapters_workspace_bytes(*sizes), dtype=torch.uint8)
     else:
         _cuda_tensor("workspace", workspace)
     _launch(dev, L.dcn_proj_adapters_forward, ctypes.byref(p), x.data_ptr(), weight.data_ptr(),

@@ -9,19 +9,25 @@
 // output lanes leaves the other rows alone (a product with zeros instead would
 // carry an infinity of one request's adapter into its neighbours' rows).
 //
-// Two launches of one kernel.  SHRINK forms t for every pair (tile of 128 rows,
-// request in it) and stores the request's rows, scaled and then rounded once
-// to the storage type, which the operands of the second product have.  Along
-// the rows either the tile or the request advances, so tile + request numbers
-// the pairs.  EXPAND runs over the tiles of y, 128 rows x BN channels: the
-// blocks of x and W first, then those of t and B.  EXPAND is a programmatic
-// dependent of SHRINK and waits for it only before its first load of t.
+// SHRINK forms t for every pair (tile of 128 rows, request in it) and stores
+// the request's rows, scaled and then rounded once to the storage type, which
+// the operands of the second product have.  Along the rows either the tile or
+// the request advances, so tile + request numbers the pairs.
+//
+// EXPAND runs over the tiles of y: the blocks of x and W first, then those of t
+// and B.  A tile is 256 rows x BN channels by a pair of CTAs (cta_group::2):
+// each CTA stages its own 128 rows and half of the channels, 32 KB for every 256
+// x 256 x 64 products, because what an SM can fetch from L2 bounds the kernel
+// (128 x 256 tiles of single CTAs: 48 KB for 128 x 256 x 64).  EXPAND is a
+// programmatic dependent of SHRINK and waits for it only before its first load
+// of t.
 //
 // Both are persistent and warp-specialised: warp 0 streams the 64-wide blocks
 // of both operands by TMA (128-byte swizzle, zero fill past every edge) through
-// a ring, one thread of warp 1 issues tcgen05.mma into one of two tensor-memory
-// accumulators, warps 2..5 read the finished one back, finish it and store.
-// Every wait is bounded and gives up when another role has aborted.
+// a ring, one thread of warp 1 (of the pair's first CTA) issues tcgen05.mma into
+// one of two tensor-memory accumulators, warps 2..5 read the finished one back,
+// finish it and store.  Every wait is bounded and gives up when another role of
+// the CTA has aborted.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
@@ -33,7 +39,7 @@
 namespace dcnb {
 namespace {
 
-constexpr int kBM = 128;
+constexpr int kBM = 128;                 // rows of a CTA
 constexpr int kBK = 64;
 constexpr int kABytes = kBM * kBK * 2;
 constexpr int kThreads = 6 * 32;
@@ -47,10 +53,10 @@ struct LargeParams {
     const void *bias;
     void *t;               // [rows, rank]
     void *out;
-    int MT, NT;            // tiles of rows, of output channels
-    int BN;                // output channels (SHRINK: rank rounded up to 16) of a tile
+    int NT;                // EXPAND: tiles of output channels
+    int BN;                // EXPAND: output channels of a tile; SHRINK: rank rounded up to 16
     int stages, tmem_cols;
-    long long jobs;        // tiles of y, or pairs of a tile and a request
+    long long jobs;        // EXPAND: tiles of y; SHRINK: pairs of a tile and a request
     unsigned int *err;
 };
 
@@ -85,6 +91,268 @@ struct Requests {
     }
 };
 
+// Shared memory of a CTA: the ring, the barriers, the tensor-memory address, the abort flag and the request
+// table.
+struct Smem {
+    unsigned char *ring;
+    uint32_t full, empty, acc_full, acc_empty, drain;  // barriers: kMaxStages, kMaxStages, 2, 2, 1
+    uint32_t *tmem_slot;
+    volatile int *abort_flag;
+    int32_t *cache;  // [requests + 1] starts, [requests] adapters
+    __device__ __forceinline__ Smem(unsigned char *raw, int ring_bytes) {
+        ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+        uint64_t *bars = reinterpret_cast<uint64_t *>(ring + ring_bytes);
+        full = smem_u32(bars);
+        empty = full + 8 * kMaxStages;
+        acc_full = empty + 8 * kMaxStages;
+        acc_empty = acc_full + 16;
+        drain = acc_empty + 16;
+        tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kMaxStages + 5);
+        abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+        cache = reinterpret_cast<int32_t *>(tmem_slot + 2);
+    }
+    // by one thread; `readers` warps empty an accumulator
+    __device__ __forceinline__ void init(int readers) const {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, readers);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    // by all threads, before a CTA barrier
+    __device__ __forceinline__ Requests requests(const LargeParams &p) const {
+        Requests r;
+        const bool cached = p.requests <= kReqCache;
+        if (cached) {
+            for (int i = threadIdx.x; i <= p.requests; i += kThreads) cache[i] = p.start[i];
+            for (int i = threadIdx.x; i < p.requests; i += kThreads) cache[p.requests + 1 + i] = p.which[i];
+        }
+        r.start = cached ? cache : p.start;
+        r.which = cached ? cache + p.requests + 1 : p.which;
+        r.count = p.requests;
+        r.rows = p.rows;
+        r.adapters = p.adapters;
+        return r;
+    }
+};
+
+// Position in the ring.
+struct Slot {
+    uint32_t s = 0, pass = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == (uint32_t)stages) {
+            s = 0;
+            ++pass;
+        }
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    adapters_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
+                           const LargeParams p) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const int sbytes = kABytes + p.BN * kBK * 2;  // BN a multiple of 16: a stage is a multiple of 1 KB
+    const Smem sm(smem_raw, p.stages * sbytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) sm.init(4);
+    const Requests req = sm.requests(p);
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sm.tmem_slot)),
+                     "r"(p.tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *sm.tmem_slot;
+    if (blockIdx.x == 0 && warp >= 2)
+        for (int i = threadIdx.x - 64; i < p.requests; i += 128) report_bad_adapter(req.which[i], p.adapters, p.err);
+    const int KB = (p.cin + kBK - 1) / kBK;
+
+    if (warp == 0) {
+        // ---- producer
+        if (lane == 0) {
+            Slot at;
+            long long issued = 0;
+            bool ok = true;
+            for (long long j = blockIdx.x; j < p.jobs && ok; j += gridDim.x) {
+                const int r = req.of_pair(j);
+                if (r < 0) continue;
+                const int row = (int)(j - r) * kBM, arow = req.adapter(r) * p.rank;
+                for (int kb = 0; kb < KB; ++kb) {
+                    const uint32_t full = sm.full + 8 * at.s;
+                    if (at.pass >= 1 && !wait_or_abort(sm.empty + 8 * at.s, (at.pass - 1) & 1, sm.abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(full, (uint32_t)sbytes);
+                    const uint32_t st = smem_u32(sm.ring) + at.s * sbytes;
+                    tma_load_2d(st, &xmap, full, kb * kBK, row);
+                    tma_load_2d(st + kABytes, &amap, full, kb * kBK, arow);
+                    ++issued;
+                    at.next(p.stages);
+                }
+            }
+            if (!ok) raise_abort(sm.abort_flag, p.err);
+            // the last load of every stage has landed before the CTA may exit
+            for (long long j = issued - 1; j >= 0 && j >= issued - p.stages; --j)
+                mbar_wait_bounded(sm.full + 8 * (uint32_t)(j % p.stages), (uint32_t)(j / p.stages) & 1, kTcWaitNs);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- one thread issues the products
+        if (lane == 0) {
+            const uint32_t idesc = instr_desc_f16(std::is_same<T, __nv_bfloat16>::value ? 1 : 0, p.BN);
+            const uint64_t a0 = smem_desc_sw128(smem_u32(sm.ring)), b0 = smem_desc_sw128(smem_u32(sm.ring + kABytes));
+            const uint32_t sstep = (uint32_t)sbytes >> 4;
+            Slot at;
+            int local = 0;
+            bool ok = true, issued = false;
+            for (long long j = blockIdx.x; j < p.jobs && ok; j += gridDim.x) {
+                if (req.of_pair(j) < 0) continue;
+                const int buf = local & 1;
+                if (local >= 2 && !wait_or_abort(sm.acc_empty + 8 * buf, ((local >> 1) - 1) & 1, sm.abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t dcol = tmem + (uint32_t)(buf * p.BN);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait_or_abort(sm.full + 8 * at.s, at.pass & 1, sm.abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = a0 + at.s * sstep, bd = b0 + at.s * sstep;
+                    // steps of 16 elements = 2 descriptor units; columns past cin are zeros
+                    mma_f16(dcol, ad, bd, idesc, kb != 0);
+                    mma_f16(dcol, ad + 2, bd + 2, idesc, 1u);
+                    mma_f16(dcol, ad + 4, bd + 4, idesc, 1u);
+                    mma_f16(dcol, ad + 6, bd + 6, idesc, 1u);
+                    issued = true;
+                    mma_commit(sm.empty + 8 * at.s);
+                    at.next(p.stages);
+                }
+                if (!ok) break;
+                mma_commit(sm.acc_full + 8 * buf);
+                ++local;
+            }
+            if (!ok) raise_abort(sm.abort_flag, p.err);
+            if (issued) {
+                // every product has finished before tensor memory is freed
+                mma_commit(sm.drain);
+                mbar_wait_bounded(sm.drain, 0, kTcWaitNs);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- epilogue: warp w reads tensor-memory lanes 32 * (w % 4) .. +31 = rows of the tile
+        const int quad = warp & 3;
+        int local = 0;
+        for (long long j = blockIdx.x; j < p.jobs; j += gridDim.x) {
+            const int r = req.of_pair(j);
+            if (r < 0) continue;
+            const int row = (int)(j - r) * kBM + quad * 32 + lane, buf = local & 1;
+            const bool mine = row >= req.at(r) && row < req.at(r + 1);
+            const float mul = p.scale ? p.scale[req.adapter(r)] : 1.0f;
+            T *dst = static_cast<T *>(p.t) + (long long)row * p.rank;
+            if (!wait_or_abort(sm.acc_full + 8 * buf, (local >> 1) & 1, sm.abort_flag)) {
+                raise_abort(sm.abort_flag, p.err);
+                break;
+            }
+            tc_fence_after();
+            for (int c = 0; c < p.rank; c += 16) {  // warp-uniform
+                float v[16];
+                tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * p.BN + c), v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] *= mul;
+                if (mine) {
+                    *reinterpret_cast<uint4 *>(dst + c) = pack16<T>(v);
+                    if (c + 8 < p.rank) *reinterpret_cast<uint4 *>(dst + c + 8) = pack16<T>(v + 8);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sm.acc_empty + 8 * buf);
+            ++local;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols)
+                     : "memory");
+    }
+}
+
+// ---- CTA pairs
+
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of the pair's first CTA's variable that is at `addr` in this one.
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Load into this CTA's shared memory that completes on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+// 256 rows: the first CTA's 128 and the second's; N columns, half of the operand in each CTA.
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same, adding only to the accumulator rows whose bit in `off` is clear.
+__device__ __forceinline__ void mma_pair_rows(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              const uint32_t *off) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7, %8, %9, %10, %11}, p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]), "r"(off[4]),
+        "r"(off[5]), "r"(off[6]), "r"(off[7])
+        : "memory");
+}
+// Arrive on `bar` of both CTAs once every product this thread issued so far is complete.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
 // Bits [lo, hi) of a word; bounds outside [0, 32] are cut off.
 __device__ __forceinline__ uint32_t lane_bits(int lo, int hi) {
     lo = max(lo, 0);
@@ -93,236 +361,163 @@ __device__ __forceinline__ uint32_t lane_bits(int lo, int hi) {
     return (hi == 32 ? 0xffffffffu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
 }
 
-// A product that updates only the accumulator lanes (rows) whose bit in `off` is clear.
-__device__ __forceinline__ void mma_f16_lanes(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                              const uint32_t *off) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.eq.b32 p, 0, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3])
-        : "memory");
-}
+constexpr int kPairRows = 2 * kBM;
 
-template <typename T, bool SHRINK>
-__global__ void __launch_bounds__(kThreads, 1)
-    adapters_gemm_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
-                         const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap bmap,
-                         const LargeParams p) {
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    adapters_expand_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
+                           const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap bmap,
+                           const LargeParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char *ring = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const int bbytes = p.BN * kBK * 2, sbytes = kABytes + bbytes;  // BN a multiple of 16: a stage is a multiple of 1 KB
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + p.stages * sbytes);
-    // full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * kMaxStages + 5);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int32_t *cache = reinterpret_cast<int32_t *>(tmem_slot + 2);  // [requests + 1] starts, [requests] adapters
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages, accf0 = empty0 + 8 * kMaxStages;
-    const uint32_t acce0 = accf0 + 16, drain = acce0 + 16;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    if (SHRINK) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(full0 + 8 * i, 1);
-            mbar_init(empty0 + 8 * i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(accf0 + 8 * i, 1);
-            mbar_init(acce0 + 8 * i, 4);
-        }
-        mbar_init(drain, 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    const bool cached = p.requests <= kReqCache;
-    if (cached) {
-        for (int i = threadIdx.x; i <= p.requests; i += kThreads) cache[i] = p.start[i];
-        for (int i = threadIdx.x; i < p.requests; i += kThreads) cache[p.requests + 1 + i] = p.which[i];
-    }
+    const int sbytes = kABytes + p.BN / 2 * kBK * 2;
+    const Smem sm(smem_raw, p.stages * sbytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cta_rank();
+    const long long pair0 = blockIdx.x / 2, pairs = gridDim.x / 2;
+    if (threadIdx.x == 0) sm.init(8);  // the epilogue warps of both CTAs
+    const Requests req = sm.requests(p);
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sm.tmem_slot)),
                      "r"(p.tmem_cols)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // the other CTA's barriers and tensor memory are ready
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    Requests req;
-    req.start = cached ? cache : p.start;
-    req.which = cached ? cache + p.requests + 1 : p.which;
-    req.count = p.requests;
-    req.rows = p.rows;
-    req.adapters = p.adapters;
-    if (SHRINK && blockIdx.x == 0 && warp >= 2)
-        for (int i = threadIdx.x - 64; i < p.requests; i += 128) report_bad_adapter(req.which[i], p.adapters, p.err);
+    const uint32_t tmem = *sm.tmem_slot;
     const int KB = (p.cin + kBK - 1) / kBK, RB = (p.rank + kBK - 1) / kBK;
 
     if (warp == 0) {
-        // ---- producer
+        // ---- producer: this CTA's rows and half of the channels; both CTAs' loads complete on the first one's
+        // barrier, which expects the bytes of both
         if (lane == 0) {
-            uint32_t s = 0, pass = 0;
+            Slot at;
             long long issued = 0;
             bool ok = true, waited = false;
-            auto load = [&](const CUtensorMap *am, int a0, int a1, const CUtensorMap *bm, int b0, int b1) {
-                if (pass >= 1 && !wait_or_abort(empty0 + 8 * s, (pass - 1) & 1, abort_flag)) return false;
-                mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)sbytes);
-                unsigned char *st = ring + s * sbytes;
-                tma_load_2d(smem_u32(st), am, full0 + 8 * s, a0, a1);
-                tma_load_2d(smem_u32(st + kABytes), bm, full0 + 8 * s, b0, b1);
+            const uint32_t full0 = in_first_cta(sm.full);
+            auto load = [&](const CUtensorMap *am, int k, int row, const CUtensorMap *bm, int brow) {
+                if (at.pass >= 1 && !wait_or_abort(sm.empty + 8 * at.s, (at.pass - 1) & 1, sm.abort_flag)) return false;
+                if (rank == 0) mbar_arrive_expect_tx(sm.full + 8 * at.s, (uint32_t)(2 * sbytes));
+                const uint32_t st = smem_u32(sm.ring) + at.s * sbytes;
+                tma_load_2d_pair(st, am, full0 + 8 * at.s, k, row);
+                tma_load_2d_pair(st + kABytes, bm, full0 + 8 * at.s, k, brow);
                 ++issued;
-                if (++s == (uint32_t)p.stages) {
-                    s = 0;
-                    ++pass;
-                }
+                at.next(p.stages);
                 return true;
             };
-            for (long long j = blockIdx.x; j < p.jobs && ok && !*abort_flag; j += gridDim.x) {
-                if (SHRINK) {
-                    const int r = req.of_pair(j);
-                    if (r < 0) continue;
-                    const int tile = (int)(j - r), ad = req.adapter(r);
-                    for (int kb = 0; kb < KB && ok; ++kb)
-                        ok = load(&xmap, kb * kBK, tile * kBM, &wmap, kb * kBK, ad * p.rank);
-                } else {
-                    const int tile = (int)(j / p.NT), n0 = (int)(j % p.NT) * p.BN;
-                    for (int kb = 0; kb < KB && ok; ++kb) ok = load(&xmap, kb * kBK, tile * kBM, &wmap, kb * kBK, n0);
-                    if (ok && !waited) {
-                        // t comes from the SHRINK kernel: visible from here on, to the TMA too
-                        asm volatile("griddepcontrol.wait;" ::: "memory");
-                        asm volatile("fence.proxy.async;" ::: "memory");
-                        waited = true;
-                    }
-                    for (int r = req.first_ending_after(tile * kBM); ok && r < p.requests; ++r) {
-                        if (req.at(r) >= (tile + 1) * kBM) break;
-                        const int ad = req.adapter(r);
-                        if (ad < 0 || req.at(r + 1) <= req.at(r)) continue;
-                        for (int rb = 0; rb < RB && ok; ++rb)
-                            ok = load(&tmap, rb * kBK, tile * kBM, &bmap, rb * kBK, ad * p.cout + n0);
-                    }
+            for (long long j = pair0; j < p.jobs && ok; j += pairs) {
+                const int tile = (int)(j / p.NT) * kPairRows, row = tile + rank * kBM;
+                const int n0 = (int)(j % p.NT) * p.BN + rank * (p.BN / 2);
+                for (int kb = 0; kb < KB && ok; ++kb) ok = load(&xmap, kb * kBK, row, &wmap, n0);
+                if (ok && !waited) {
+                    // t comes from the SHRINK kernel: visible from here on, to the TMA too
+                    asm volatile("griddepcontrol.wait;" ::: "memory");
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                    waited = true;
+                }
+                for (int r = req.first_ending_after(tile); ok && r < p.requests && req.at(r) < tile + kPairRows; ++r) {
+                    const int ad = req.adapter(r);
+                    if (ad < 0 || req.at(r + 1) <= req.at(r)) continue;
+                    for (int rb = 0; rb < RB && ok; ++rb)
+                        ok = load(&tmap, rb * kBK, row, &bmap, ad * p.cout + n0);
                 }
             }
-            if (!ok) raise_abort(abort_flag, p.err);
-            // the last load of every stage has landed before the CTA may exit
-            for (long long j = issued - 1; j >= 0 && j >= issued - p.stages; --j)
-                mbar_wait_bounded(full0 + 8 * (uint32_t)(j % p.stages), (uint32_t)(j / p.stages) & 1, kTcWaitNs);
+            if (!ok) raise_abort(sm.abort_flag, p.err);
+            // the last loads of every stage, of both CTAs, have landed before the pair may exit
+            if (rank == 0)
+                for (long long j = issued - 1; j >= 0 && j >= issued - p.stages; --j)
+                    mbar_wait_bounded(sm.full + 8 * (uint32_t)(j % p.stages), (uint32_t)(j / p.stages) & 1, kTcWaitNs);
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ---- one thread issues the products
-        if (lane == 0) {
-            const int fmt = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
-            const uint32_t idesc = instr_desc_f16(fmt, p.BN);
-            const uint64_t a0 = smem_desc_sw128(smem_u32(ring)), b0 = smem_desc_sw128(smem_u32(ring + kABytes));
+        // ---- one thread of the first CTA issues the products
+        if (rank == 0 && lane == 0) {
+            const uint32_t idesc = (instr_desc_f16(std::is_same<T, __nv_bfloat16>::value ? 1 : 0, p.BN) &
+                                    ~(31u << 24)) | ((uint32_t)(kPairRows >> 4) << 24);
+            const uint64_t a0 = smem_desc_sw128(smem_u32(sm.ring)), b0 = smem_desc_sw128(smem_u32(sm.ring + kABytes));
             const uint32_t sstep = (uint32_t)sbytes >> 4;
-            uint32_t s = 0, ph = 0;
+            Slot at;
             int local = 0;
             bool ok = true, issued = false;
-            uint32_t dcol = 0, acc = 0;
-            // a block of `steps` products of 16 channels each (2 descriptor units), in all rows or
-            // outside the lanes `off`
-            auto block = [&](int steps, const uint32_t *off) {
-                if (!wait_or_abort(full0 + 8 * s, ph, abort_flag)) return false;
-                tc_fence_after();
-                const uint64_t ad = a0 + s * sstep, bd = b0 + s * sstep;
-                if (off) {
-                    for (int i = 0; i < steps; ++i) mma_f16_lanes(dcol, ad + 2 * i, bd + 2 * i, idesc, off);
-                } else {
-                    mma_f16(dcol, ad, bd, idesc, acc);
-                    if (steps > 1) mma_f16(dcol, ad + 2, bd + 2, idesc, 1u);
-                    if (steps > 2) mma_f16(dcol, ad + 4, bd + 4, idesc, 1u);
-                    if (steps > 3) mma_f16(dcol, ad + 6, bd + 6, idesc, 1u);
-                }
-                acc = 1u;
-                issued = true;
-                mma_commit(empty0 + 8 * s);
-                if (++s == (uint32_t)p.stages) {
-                    s = 0;
-                    ph ^= 1u;
-                }
-                return true;
-            };
-            for (long long j = blockIdx.x; j < p.jobs && ok; j += gridDim.x) {
-                if (SHRINK && req.of_pair(j) < 0) continue;
-                const int buf = local & 1;
-                if (local >= 2 && !wait_or_abort(acce0 + 8 * buf, ((local >> 1) - 1) & 1, abort_flag)) {
+            for (long long j = pair0; j < p.jobs && ok; j += pairs, ++local) {
+                const int tile = (int)(j / p.NT) * kPairRows, buf = local & 1;
+                if (local >= 2 && !wait_or_abort(sm.acc_empty + 8 * buf, ((local >> 1) - 1) & 1, sm.abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                dcol = tmem + (uint32_t)(buf * p.BN);
-                acc = 0;
-                for (int kb = 0; kb < KB && ok; ++kb) ok = block(min(4, (p.cin - kb * kBK + 15) / 16), nullptr);
-                if (!SHRINK) {
-                    const int tile = (int)(j / p.NT);
-                    for (int r = req.first_ending_after(tile * kBM); ok && r < p.requests; ++r) {
-                        if (req.at(r) >= (tile + 1) * kBM) break;
-                        if (req.adapter(r) < 0 || req.at(r + 1) <= req.at(r)) continue;
-                        const int r0 = max(req.at(r) - tile * kBM, 0), r1 = min(req.at(r + 1) - tile * kBM, kBM);
-                        uint32_t off[4];
+                const uint32_t dcol = tmem + (uint32_t)(buf * p.BN);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait_or_abort(sm.full + 8 * at.s, at.pass & 1, sm.abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = a0 + at.s * sstep, bd = b0 + at.s * sstep;
+                    mma_pair(dcol, ad, bd, idesc, kb != 0);
+                    mma_pair(dcol, ad + 2, bd + 2, idesc, 1u);
+                    mma_pair(dcol, ad + 4, bd + 4, idesc, 1u);
+                    mma_pair(dcol, ad + 6, bd + 6, idesc, 1u);
+                    issued = true;
+                    commit_pair(sm.empty + 8 * at.s);
+                    at.next(p.stages);
+                }
+                for (int r = req.first_ending_after(tile); ok && r < p.requests && req.at(r) < tile + kPairRows; ++r) {
+                    if (req.adapter(r) < 0 || req.at(r + 1) <= req.at(r)) continue;
+                    // this request's rows of the tile
+                    const int r0 = req.at(r) - tile, r1 = req.at(r + 1) - tile;
+                    uint32_t off[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) off[i] = ~lane_bits(r0 - 32 * i, r1 - 32 * i);
-                        for (int rb = 0; rb < RB && ok; ++rb) ok = block(min(4, (p.rank - rb * kBK + 15) / 16), off);
+                    for (int i = 0; i < 8; ++i) off[i] = ~lane_bits(r0 - 32 * i, r1 - 32 * i);
+                    for (int rb = 0; rb < RB; ++rb) {
+                        if (!wait_or_abort(sm.full + 8 * at.s, at.pass & 1, sm.abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = a0 + at.s * sstep, bd = b0 + at.s * sstep;
+                        const int steps = min(4, (p.rank - rb * kBK + 15) / 16);
+                        for (int i = 0; i < steps; ++i) mma_pair_rows(dcol, ad + 2 * i, bd + 2 * i, idesc, off);
+                        commit_pair(sm.empty + 8 * at.s);
+                        at.next(p.stages);
                     }
                 }
                 if (!ok) break;
-                mma_commit(accf0 + 8 * buf);
-                ++local;
+                commit_pair(sm.acc_full + 8 * buf);
             }
-            if (!ok) raise_abort(abort_flag, p.err);
+            if (!ok) raise_abort(sm.abort_flag, p.err);
             if (issued) {
                 // every product has finished before tensor memory is freed
-                mma_commit(drain);
-                mbar_wait_bounded(drain, 0, kTcWaitNs);
+                commit_pair(sm.drain);
+                mbar_wait_bounded(sm.drain, 0, kTcWaitNs);
             }
         }
         __syncwarp();
     } else {
-        // ---- epilogue: warp w reads tensor-memory lanes 32 * (w % 4) .. +31 = rows of the tile
+        // ---- epilogue: this CTA's rows, warp w the tensor-memory lanes 32 * (w % 4) .. +31
         const int quad = warp & 3;
         const T *bias = static_cast<const T *>(p.bias);
-        const int covered0 = p.requests ? req.at(0) : 0, covered1 = p.requests ? req.at(p.requests) : 0;
+        const int covered0 = req.at(0), covered1 = req.at(p.requests);
+        const uint32_t acc_empty0 = in_first_cta(sm.acc_empty);
         int local = 0;
-        for (long long j = blockIdx.x; j < p.jobs; j += gridDim.x) {
-            int r = 0, row, n0, ncols;
-            T *dst;
-            float mul = 1.0f;
-            bool write;
-            if (SHRINK) {
-                r = req.of_pair(j);
-                if (r < 0) continue;
-                row = (int)(j - r) * kBM + quad * 32 + lane;
-                n0 = 0;
-                ncols = p.rank;
-                dst = static_cast<T *>(p.t) + (long long)row * p.rank;
-                mul = p.scale ? p.scale[req.adapter(r)] : 1.0f;
-                write = row >= req.at(r) && row < req.at(r + 1);
-            } else {
-                row = (int)(j / p.NT) * kBM + quad * 32 + lane;
-                n0 = (int)(j % p.NT) * p.BN;
-                ncols = min(p.BN, p.cout - n0);
-                dst = static_cast<T *>(p.out) + (long long)row * p.cout + n0;
-                write = row >= covered0 && row < covered1;
-            }
-            const int buf = local & 1;
-            if (!wait_or_abort(accf0 + 8 * buf, (local >> 1) & 1, abort_flag)) {
-                raise_abort(abort_flag, p.err);
+        for (long long j = pair0; j < p.jobs; j += pairs, ++local) {
+            const int row = (int)(j / p.NT) * kPairRows + rank * kBM + quad * 32 + lane;
+            const int n0 = (int)(j % p.NT) * p.BN, ncols = min(p.BN, p.cout - n0), buf = local & 1;
+            T *dst = static_cast<T *>(p.out) + (long long)row * p.cout + n0;
+            const bool write = row >= covered0 && row < covered1;
+            if (!wait_or_abort(sm.acc_full + 8 * buf, (local >> 1) & 1, sm.abort_flag)) {
+                raise_abort(sm.abort_flag, p.err);
                 break;
             }
             tc_fence_after();
             for (int c = 0; c < ncols; c += 16) {  // warp-uniform
                 float v[16];
                 tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * p.BN + c), v);
-                if (SHRINK) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] *= mul;
-                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (c + 8 * h >= ncols) continue;  // cout and rank are multiples of 8
-                    if (!SHRINK && bias) {
+                    if (c + 8 * h >= ncols) continue;  // cout is a multiple of 8
+                    if (bias) {
                         float b[8];
                         unpack16<T>(ld_nc16(bias + n0 + c + 8 * h), b);
 #pragma unroll
@@ -333,18 +528,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acce0 + 8 * buf);
-            ++local;
+            if (lane == 0) arrive_remote(acc_empty0 + 8 * buf);
         }
     }
-    // a CTA that had no tile to load t for still outlives the SHRINK kernel: the call's next user of the
-    // workspace is ordered behind this kernel
-    if (!SHRINK) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // a pair that had no t to wait for still ends after SHRINK: the next user of the workspace is ordered behind
+    // this kernel
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // neither CTA frees or leaves what the other still uses
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem_cols)
                      : "memory");
     }
 }
@@ -362,41 +557,19 @@ bool encode(CUtensorMap *m, const void *base, long long cols, long long rows, in
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-long long pairs_of(const AdapterArgs &a) { return (a.rows + kBM - 1) / kBM + a.requests; }
-
 int tmem_columns(int bn) {
     int cols = 32;
     while (cols < 2 * bn) cols <<= 1;
     return cols;
 }
 
-size_t smem_bytes(int stages, int bn, int requests) {
-    return 1024 + (size_t)stages * (kABytes + bn * kBK * 2) + (2 * kMaxStages + 5) * 8 + 8 +
-           (requests <= kReqCache ? (size_t)(2 * requests + 1) * 4 : 0);
-}
-
-template <typename T, bool SHRINK>
-cudaError_t launch_gemm(LargeParams &p, const DeviceInfo *dev, const CUtensorMap &x, const CUtensorMap &w,
-                        const CUtensorMap &t, const CUtensorMap &b, cudaStream_t stream) {
-    p.tmem_cols = tmem_columns(p.BN);
-    int stages = kMaxStages;
-    while (stages > 2 && smem_bytes(stages, p.BN, p.requests) > (size_t)dev->smem_optin) --stages;
-    p.stages = stages;
-    const size_t smem = smem_bytes(stages, p.BN, p.requests);
-    auto kern = adapters_gemm_kernel<T, SHRINK>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.jobs < dev->sms ? p.jobs : dev->sms));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = SHRINK ? 0 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, x, w, t, b, p);
+// Stages of `sbytes` that fit, and the shared memory they take.
+size_t plan_smem(LargeParams &p, size_t sbytes, size_t limit) {
+    const size_t other = 1024 + (2 * kMaxStages + 5) * 8 + 8 +
+                         (p.requests <= kReqCache ? (size_t)(2 * p.requests + 1) * 4 : 0);
+    p.stages = kMaxStages;
+    while (p.stages > 2 && other + p.stages * sbytes > limit) --p.stages;
+    return other + p.stages * sbytes;
 }
 
 template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t stream) {
@@ -409,39 +582,58 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     p.t = a.workspace;
     p.out = a.out;
     p.err = dev->err;
-    p.MT = (int)((a.rows + kBM - 1) / kBM);
-    const long long pairs = pairs_of(a);
 
-    CUtensorMap xm, am, wm, tm, bm;
-    const int rank16 = (a.rank + 15) / 16 * 16;
-    // the tile width whose rounds of tiles over the SMs cost least: a tile costs its columns, plus a
-    // constant share (the rows of x it streams and its epilogue) of 48 columns
+    // The tile width whose rounds of tiles over the CTA pairs cost least: a tile costs its columns, plus the
+    // rows of x that it streams and its epilogue, worth about 128 columns.
+    const long long mt = (a.rows + kPairRows - 1) / kPairRows, pairs = dev->sms / 2;
     int bn = 0;
     long long best = 0;
     for (int c = 256; c >= 64; c /= 2) {
-        const long long tiles = (long long)p.MT * ((a.cout + c - 1) / c);
-        const long long cost = (tiles + dev->sms - 1) / dev->sms * (c + 48);
+        const long long tiles = mt * ((a.cout + c - 1) / c);
+        const long long cost = (tiles + pairs - 1) / pairs * (c + 128);
         if (!bn || cost < best) {
             bn = c;
             best = cost;
         }
     }
-    if (!encode<T>(&xm, a.x, a.cin, a.rows, kBM) || !encode<T>(&wm, a.weight, a.cin, a.cout, bn) ||
-        !encode<T>(&tm, a.workspace, a.rank, a.rows, kBM))
-        return cudaErrorInvalidValue;
-    am = bm = wm;  // never read without adapters
+    const int rank16 = (a.rank + 15) / 16 * 16;
+    CUtensorMap xm, am, wm, tm, bm;
+    if (!encode<T>(&xm, a.x, a.cin, a.rows, kBM) || !encode<T>(&wm, a.weight, a.cin, a.cout, bn / 2)) return cudaErrorInvalidValue;
+    am = tm = bm = wm;  // never read without adapters
     if (a.adapters > 0 && (!encode<T>(&am, a.a, a.cin, (long long)a.adapters * a.rank, rank16) ||
-                           !encode<T>(&bm, a.b, a.rank, (long long)a.adapters * a.cout, bn)))
+                           !encode<T>(&tm, a.workspace, a.rank, a.rows, kBM) ||
+                           !encode<T>(&bm, a.b, a.rank, (long long)a.adapters * a.cout, bn / 2)))
         return cudaErrorInvalidValue;
+
+    static std::atomic<bool> shrink_ok[kMaxDev], expand_ok[kMaxDev];
+    cudaError_t e = allow_smem(adapters_shrink_kernel<T>, dev->smem_optin, shrink_ok);
+    if (e == cudaSuccess) e = allow_smem(adapters_expand_kernel<T>, dev->smem_optin, expand_ok);
+    if (e != cudaSuccess) return e;
     p.BN = rank16;
     p.NT = 1;
-    p.jobs = pairs;
-    cudaError_t e = launch_gemm<T, true>(p, dev, xm, am, xm, am, stream);
+    p.jobs = (a.rows + kBM - 1) / kBM + a.requests;
+    p.tmem_cols = tmem_columns(p.BN);
+    size_t smem = plan_smem(p, kABytes + p.BN * kBK * 2, (size_t)dev->smem_optin);
+    adapters_shrink_kernel<T><<<(unsigned)(p.jobs < dev->sms ? p.jobs : dev->sms), kThreads, smem, stream>>>(xm, am, p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+
     p.BN = bn;
     p.NT = (a.cout + bn - 1) / bn;
-    p.jobs = (long long)p.MT * p.NT;
-    return launch_gemm<T, false>(p, dev, xm, wm, tm, bm, stream);
+    p.jobs = mt * p.NT;
+    p.tmem_cols = tmem_columns(p.BN);
+    smem = plan_smem(p, kABytes + p.BN / 2 * kBK * 2, (size_t)dev->smem_optin);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (p.jobs < pairs ? p.jobs : pairs)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, adapters_expand_kernel<T>, xm, wm, tm, bm, p);
 }
 
 }  // namespace

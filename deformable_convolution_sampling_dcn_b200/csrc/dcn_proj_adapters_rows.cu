@@ -411,7 +411,8 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     CUtensorMap wm, xm;
     if (!encode<T>(&wm, a.weight, a.cin, a.cout, kTN) || !encode<T>(&xm, a.x, a.cin, a.rows, p.mpad))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(adapters_rows_stream<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> stream_ok[kMaxDev];
+    cudaError_t e = allow_smem(adapters_rows_stream<T>, dev->smem_optin, stream_ok);
     if (e != cudaSuccess) return e;
     const int t_ctas = ((int)a.rows * a.rank + kTWarps - 1) / kTWarps;
     const int grid = t_ctas > p.ctas ? (t_ctas < kSms ? t_ctas : kSms) : p.ctas;
