@@ -353,6 +353,14 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
         : "memory");
 }
 
+// Box of 64 columns x 32 rows from shared memory (128-byte swizzle); completes in this thread's bulk groups.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(src),
+                 "r"(c0), "r"(c1)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
 // Bits [lo, hi) of a word; bounds outside [0, 32] are cut off.
 __device__ __forceinline__ uint32_t lane_bits(int lo, int hi) {
     lo = max(lo, 0);
@@ -362,15 +370,17 @@ __device__ __forceinline__ uint32_t lane_bits(int lo, int hi) {
 }
 
 constexpr int kPairRows = 2 * kBM;
+constexpr int kOutBytes = 32 * kBK * 2;           // a warp's staged box of y
+constexpr int kOutStage = 2 * 4 * kOutBytes;      // two for each epilogue warp
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     adapters_expand_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                            const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap bmap,
-                           const LargeParams p) {
+                           const __grid_constant__ CUtensorMap ymap, const LargeParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int sbytes = kABytes + p.BN / 2 * kBK * 2;
-    const Smem sm(smem_raw, p.stages * sbytes);
+    const Smem sm(smem_raw, p.stages * sbytes + kOutStage);  // the staged boxes of y follow the ring
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cta_rank();
     const long long pair0 = blockIdx.x / 2, pairs = gridDim.x / 2;
     if (threadIdx.x == 0) sm.init(8);  // the epilogue warps of both CTAs
@@ -495,41 +505,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- epilogue: this CTA's rows, warp w the tensor-memory lanes 32 * (w % 4) .. +31
+        // ---- epilogue: this CTA's rows, warp w the tensor-memory lanes 32 * (w % 4) .. +31.  64 columns at a
+        // time go through shared memory and out by TMA in whole lines (16-byte stores by lanes that each own a row
+        // touch 32 lines an instruction); rows of no request are not to be written, so a warp that holds some
+        // stores by lanes instead.
         const int quad = warp & 3;
         const T *bias = static_cast<const T *>(p.bias);
         const int covered0 = req.at(0), covered1 = req.at(p.requests);
         const uint32_t acc_empty0 = in_first_cta(sm.acc_empty);
+        const uint32_t stage0 = smem_u32(sm.ring) + p.stages * sbytes + quad * 2 * kOutBytes;
+        uint32_t flip = 0;
         int local = 0;
         for (long long j = pair0; j < p.jobs; j += pairs, ++local) {
-            const int row = (int)(j / p.NT) * kPairRows + rank * kBM + quad * 32 + lane;
+            const int row0 = (int)(j / p.NT) * kPairRows + rank * kBM + quad * 32, row = row0 + lane;
             const int n0 = (int)(j % p.NT) * p.BN, ncols = min(p.BN, p.cout - n0), buf = local & 1;
             T *dst = static_cast<T *>(p.out) + (long long)row * p.cout + n0;
+            // the map ends at the last row: rows past it are not written either way
+            const bool boxes = row0 >= covered0 && min(row0 + 32, p.rows) <= covered1;
             const bool write = row >= covered0 && row < covered1;
             if (!wait_or_abort(sm.acc_full + 8 * buf, (local >> 1) & 1, sm.abort_flag)) {
                 raise_abort(sm.abort_flag, p.err);
                 break;
             }
             tc_fence_after();
-            for (int c = 0; c < ncols; c += 16) {  // warp-uniform
-                float v[16];
-                tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * p.BN + c), v);
+            for (int c = 0; c < ncols; c += kBK) {  // warp-uniform
+                const uint32_t stage = stage0 + flip * kOutBytes;
+                if (boxes) {
+                    // the box that was staged here two chunks ago has been read
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+                }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (c + 8 * h >= ncols) continue;  // cout is a multiple of 8
-                    if (bias) {
-                        float b[8];
-                        unpack16<T>(ld_nc16(bias + n0 + c + 8 * h), b);
+                for (int h = 0; h < 4; ++h) {
+                    float v[16];
+                    tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * p.BN + c + 16 * h), v);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[8 * h + i] += b[i];
+                    for (int i = 0; i < 2; ++i) {
+                        const int col = c + 16 * h + 8 * i;
+                        if (col >= ncols) continue;  // cout is a multiple of 8
+                        if (bias) {
+                            float b[8];
+                            unpack16<T>(ld_nc16(bias + n0 + col), b);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v[8 * i + k] += b[k];
+                        }
+                        const uint4 q = pack16<T>(v + 8 * i);
+                        if (boxes)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             stage + (uint32_t)(lane * 128 + (((2 * h + i) ^ (lane & 7)) << 4))),
+                                         "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
+                                         : "memory");
+                        else if (write)
+                            *reinterpret_cast<uint4 *>(dst + col) = q;
                     }
-                    if (write) *reinterpret_cast<uint4 *>(dst + c + 8 * h) = pack16<T>(v + 8 * h);
+                }
+                if (boxes) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store_2d(&ymap, stage, n0 + c, row0);
+                    flip ^= 1;
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_remote(acc_empty0 + 8 * buf);
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     // a pair that had no t to wait for still ends after SHRINK: the next user of the workspace is ordered behind
     // this kernel
@@ -597,8 +639,10 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
         }
     }
     const int rank16 = (a.rank + 15) / 16 * 16;
-    CUtensorMap xm, am, wm, tm, bm;
-    if (!encode<T>(&xm, a.x, a.cin, a.rows, kBM) || !encode<T>(&wm, a.weight, a.cin, a.cout, bn / 2)) return cudaErrorInvalidValue;
+    CUtensorMap xm, am, wm, tm, bm, ym;
+    if (!encode<T>(&xm, a.x, a.cin, a.rows, kBM) || !encode<T>(&wm, a.weight, a.cin, a.cout, bn / 2) ||
+        !encode<T>(&ym, a.out, a.cout, a.rows, 32))
+        return cudaErrorInvalidValue;
     am = tm = bm = wm;  // never read without adapters
     if (a.adapters > 0 && (!encode<T>(&am, a.a, a.cin, (long long)a.adapters * a.rank, rank16) ||
                            !encode<T>(&tm, a.workspace, a.rank, a.rows, kBM) ||
@@ -622,7 +666,7 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     p.NT = (a.cout + bn - 1) / bn;
     p.jobs = mt * p.NT;
     p.tmem_cols = tmem_columns(p.BN);
-    smem = plan_smem(p, kABytes + p.BN / 2 * kBK * 2, (size_t)dev->smem_optin);
+    smem = kOutStage + plan_smem(p, kABytes + p.BN / 2 * kBK * 2, (size_t)dev->smem_optin - kOutStage);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (p.jobs < pairs ? p.jobs : pairs)));
     cfg.blockDim = dim3(kThreads);
@@ -633,7 +677,7 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, adapters_expand_kernel<T>, xm, wm, tm, bm, p);
+    return cudaLaunchKernelEx(&cfg, adapters_expand_kernel<T>, xm, wm, tm, bm, ym, p);
 }
 
 }  // namespace
