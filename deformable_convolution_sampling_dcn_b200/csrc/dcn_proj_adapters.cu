@@ -130,8 +130,8 @@ struct Smem {
         Requests r;
         const bool cached = p.requests <= kReqCache;
         if (cached) {
-            for (int i = threadIdx.x; i <= p.requests; i += kThreads) cache[i] = p.start[i];
-            for (int i = threadIdx.x; i < p.requests; i += kThreads) cache[p.requests + 1 + i] = p.which[i];
+            for (int i = threadIdx.x; i <= p.requests; i += blockDim.x) cache[i] = p.start[i];
+            for (int i = threadIdx.x; i < p.requests; i += blockDim.x) cache[p.requests + 1 + i] = p.which[i];
         }
         r.start = cached ? cache : p.start;
         r.which = cached ? cache + p.requests + 1 : p.which;
@@ -371,10 +371,11 @@ __device__ __forceinline__ uint32_t lane_bits(int lo, int hi) {
 
 constexpr int kPairRows = 2 * kBM;
 constexpr int kOutBytes = 32 * kBK * 2;           // a warp's staged box of y
-constexpr int kOutStage = 2 * 4 * kOutBytes;      // two for each epilogue warp
+constexpr int kExpandThreads = 10 * 32;            // eight epilogue warps
+constexpr int kOutStage = 8 * kOutBytes + 8 * kBK * 4;  // and the bias of a chunk in fp32, for each of them
 
 template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
     adapters_expand_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                            const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap bmap,
                            const __grid_constant__ CUtensorMap ymap, const LargeParams p) {
@@ -383,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const Smem sm(smem_raw, p.stages * sbytes + kOutStage);  // the staged boxes of y follow the ring
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cta_rank();
     const long long pair0 = blockIdx.x / 2, pairs = gridDim.x / 2;
-    if (threadIdx.x == 0) sm.init(8);  // the epilogue warps of both CTAs
+    if (threadIdx.x == 0) sm.init(16);  // the epilogue warps of both CTAs
     const Requests req = sm.requests(p);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sm.tmem_slot)),
@@ -505,66 +506,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---- epilogue: this CTA's rows, warp w the tensor-memory lanes 32 * (w % 4) .. +31.  64 columns at a
-        // time go through shared memory and out by TMA in whole lines (16-byte stores by lanes that each own a row
-        // touch 32 lines an instruction); rows of no request are not to be written, so a warp that holds some
-        // stores by lanes instead.
-        const int quad = warp & 3;
+        // ---- epilogue: this CTA's rows, warp w the tensor-memory lanes 32 * (w % 4) .. +31, two warps taking the
+        // 64-column chunks in turn.  A chunk goes through shared memory and out by TMA in whole lines (16-byte
+        // stores by lanes that each own a row touch 32 lines an instruction); rows of no request are not to be
+        // written, so a warp that holds some stores by lanes instead.
+        const int quad = warp & 3, half = (warp - 2) >> 2;
         const T *bias = static_cast<const T *>(p.bias);
         const int covered0 = req.at(0), covered1 = req.at(p.requests);
         const uint32_t acc_empty0 = in_first_cta(sm.acc_empty);
-        const uint32_t stage0 = smem_u32(sm.ring) + p.stages * sbytes + quad * 2 * kOutBytes;
-        uint32_t flip = 0;
+        unsigned char *own = sm.ring + p.stages * sbytes + (warp - 2) * kOutBytes;  // box of 4 KB
+        const uint32_t stage = smem_u32(own);
+        float *bias_s = reinterpret_cast<float *>(sm.ring + p.stages * sbytes + 8 * kOutBytes) + (warp - 2) * kBK;
         int local = 0;
         for (long long j = pair0; j < p.jobs; j += pairs, ++local) {
             const int row0 = (int)(j / p.NT) * kPairRows + rank * kBM + quad * 32, row = row0 + lane;
             const int n0 = (int)(j % p.NT) * p.BN, ncols = min(p.BN, p.cout - n0), buf = local & 1;
-            T *dst = static_cast<T *>(p.out) + (long long)row * p.cout + n0;
             // the map ends at the last row: rows past it are not written either way
             const bool boxes = row0 >= covered0 && min(row0 + 32, p.rows) <= covered1;
             const bool write = row >= covered0 && row < covered1;
-            if (!wait_or_abort(sm.acc_full + 8 * buf, (local >> 1) & 1, sm.abort_flag)) {
-                raise_abort(sm.abort_flag, p.err);
-                break;
-            }
-            tc_fence_after();
-            for (int c = 0; c < ncols; c += kBK) {  // warp-uniform
-                const uint32_t stage = stage0 + flip * kOutBytes;
-                if (boxes) {
-                    // the box that was staged here two chunks ago has been read
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                    __syncwarp();
+            bool ready = false;
+            for (int c = half * kBK; c < ncols; c += 2 * kBK) {  // warp-uniform
+                __syncwarp();
+                for (int i = lane; i < kBK; i += 32)
+                    bias_s[i] = bias && c + i < ncols ? to_f32(bias[n0 + c + i]) : 0.0f;
+                // the box that was staged here before has been read
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+                if (!ready) {
+                    if (!wait_or_abort(sm.acc_full + 8 * buf, (local >> 1) & 1, sm.abort_flag)) break;
+                    tc_fence_after();
+                    ready = true;
                 }
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    float v[16];
-                    tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * p.BN + c + 16 * h), v);
+                for (int h = 0; h < 2; ++h) {
+                    float v[32];
+                    tmem_ld32(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * p.BN + c + 32 * h), v);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int col = c + 16 * h + 8 * i;
-                        if (col >= ncols) continue;  // cout is a multiple of 8
-                        if (bias) {
-                            float b[8];
-                            unpack16<T>(ld_nc16(bias + n0 + col), b);
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 b = reinterpret_cast<const float4 *>(bias_s)[8 * h + i];
+                        v[4 * i] += b.x;
+                        v[4 * i + 1] += b.y;
+                        v[4 * i + 2] += b.z;
+                        v[4 * i + 3] += b.w;
+                    }
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) v[8 * i + k] += b[k];
-                        }
+                    for (int i = 0; i < 4; ++i) {
                         const uint4 q = pack16<T>(v + 8 * i);
+                        const int col = c + 32 * h + 8 * i;
                         if (boxes)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             stage + (uint32_t)(lane * 128 + (((2 * h + i) ^ (lane & 7)) << 4))),
+                                             stage + (uint32_t)(lane * 128 + (((4 * h + i) ^ (lane & 7)) << 4))),
                                          "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w)
                                          : "memory");
-                        else if (write)
-                            *reinterpret_cast<uint4 *>(dst + col) = q;
+                        else if (write && col < ncols)  // cout is a multiple of 8
+                            *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (long long)row * p.cout + n0 + col) = q;
                     }
                 }
                 if (boxes) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) tma_store_2d(&ymap, stage, n0 + c, row0);
-                    flip ^= 1;
                 }
+            }
+            // a warp without a chunk still takes part in every accumulator's turn
+            if (!ready && !wait_or_abort(sm.acc_full + 8 * buf, (local >> 1) & 1, sm.abort_flag)) {
+                raise_abort(sm.abort_flag, p.err);
+                break;
             }
             tc_fence_before();
             __syncwarp();
@@ -669,7 +676,7 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     smem = kOutStage + plan_smem(p, kABytes + p.BN / 2 * kBK * 2, (size_t)dev->smem_optin - kOutStage);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (p.jobs < pairs ? p.jobs : pairs)));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kExpandThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
