@@ -22,8 +22,9 @@ namespace {
 
 constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126: 1 / s stays finite, an all-zero row gives q = 0
 
-// Four values to four 8-bit codes, in memory order.  A NaN becomes the e4m3
-// NaN, and 0 in int8 (its scale is NaN).
+// Four values to four 8-bit codes, in memory order.  int8 rounds by adding
+// 1.5 * 2^23 in the fused product: the low byte of the sum is the rounded value
+// (|y * inv| <= 127 * (1 + 2^-22)).
 __device__ __forceinline__ uint32_t pack8(const float *y, float inv, int quant) {
     if (quant == kQuantE4M3) {
         const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv), __NV_SATFINITE,
@@ -32,18 +33,25 @@ __device__ __forceinline__ uint32_t pack8(const float *y, float inv, int quant) 
                                                                  __NV_E4M3);
         return (uint32_t)lo | ((uint32_t)hi << 16);
     }
-    uint32_t w = 0;
+    uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int q = max(-127, min(127, __float2int_rn(y[i] * inv)));
-        w |= (uint32_t)(q & 255) << (8 * i);
-    }
-    return w;
+    for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(fmaf(y[i], inv, 12582912.0f));
+    return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
 }
 
-template <typename T, int TPR, int NV, bool AL>
-__global__ void __launch_bounds__(TPR == 0 ? 1024 : 256) norm_forward_kernel(const NormArgs a) {
+// A thread holds C = NV * VEC columns of a row: up to 16 with the loads of its
+// team's next row in flight meanwhile, or 32 without.  8-lane and warp teams
+// share a CTA of 256 threads, a CTA team has up to 512; CTAs on an SM follow
+// from the registers that leaves (48, 80 or 128).
+constexpr int kTeamThreads = 256;
+template <int TPR> constexpr int max_threads() { return TPR == 0 ? 512 : kTeamThreads; }
+constexpr int threads_per_sm(int c) { return c <= 8 ? 1280 : c <= 16 ? 768 : 512; }
+
+template <typename T, int TPR, int NV, bool AL, bool QUANT>
+__global__ void __launch_bounds__(max_threads<TPR>(), threads_per_sm(NV * Storage<T>::kVec) / max_threads<TPR>())
+    norm_forward_kernel(const NormArgs a) {
     constexpr int VEC = Storage<T>::kVec;
+    constexpr bool AHEAD = NV * VEC <= 16;
     __shared__ float red[64];
     const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
     const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
@@ -57,116 +65,106 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : 256) norm_forward_kernel(con
     for (int i = 0; i < NV; ++i)
         if (weight) w[i] = load_cols<T, AL>(weight, (t + i * tpr) * VEC, a.cols);
 
+    uint4 xn[NV], rn[NV];
+    auto fetch = [&](long long r) {
+        const long long off = r < a.rows ? r * a.cols : 0;
+        const int cols = r < a.rows ? a.cols : 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            xn[i] = load_cols<T, AL>(x + off, (t + i * tpr) * VEC, cols);
+            if (res) rn[i] = load_cols<T, AL>(res + off, (t + i * tpr) * VEC, cols);
+        }
+    };
     const long long step = (long long)gridDim.x * teams;
+    if (AHEAD) fetch((long long)blockIdx.x * teams + team);
     // every lane of a warp runs the same number of rounds: the shuffles need them all
     for (long long base = (long long)blockIdx.x * teams; base < a.rows; base += step) {
         const long long r = base + team;
         const bool live = r < a.rows;
         const long long off = live ? r * a.cols : 0;
         const int cols = live ? a.cols : 0;
-        uint4 hv[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) hv[i] = load_cols<T, AL>(x + off, (t + i * tpr) * VEC, cols);
-        if (res) {
-            uint4 rv[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) rv[i] = load_cols<T, AL>(res + off, (t + i * tpr) * VEC, cols);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float f[VEC], g[VEC];
-                unpack16<T>(hv[i], f);
-                unpack16<T>(rv[i], g);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) f[j] += g[j];
-                hv[i] = pack16<T>(f);
-                store_cols<T, AL>(static_cast<T *>(a.residual_out) + off, (t + i * tpr) * VEC, cols, hv[i]);
-            }
-        }
+        if (!AHEAD) fetch(r);
+        float y[NV][VEC];
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[VEC];
-            unpack16<T>(hv[i], f);
+            unpack16<T>(xn[i], y[i]);
+            if (res) {
+                float g[VEC];
+                unpack16<T>(rn[i], g);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) ss = fmaf(f[j], f[j], ss);
+                for (int j = 0; j < VEC; ++j) y[i][j] += g[j];
+                const uint4 h = pack16<T>(y[i]);
+                store_cols<T, AL>(static_cast<T *>(a.residual_out) + off, (t + i * tpr) * VEC, cols, h);
+                unpack16<T>(h, y[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) ss = fmaf(y[i][j], y[i][j], ss);
         }
+        if (AHEAD) fetch(r + step);
         ss = team_reduce<SumOp, TPR>(ss, red, turn);
         const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
         if (a.rstd && t == 0 && live) a.rstd[r] = rstd;
-
-        float amax = 0.0f;
-        float gmax[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float f[VEC];
-            unpack16<T>(hv[i], f);
             if (weight) {
                 float g[VEC];
                 unpack16<T>(w[i], g);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) f[j] = f[j] * rstd * g[j];
+                for (int j = 0; j < VEC; ++j) y[i][j] = y[i][j] * rstd * g[j];
             } else {
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) f[j] *= rstd;
+                for (int j = 0; j < VEC; ++j) y[i][j] *= rstd;
             }
-            if (a.out) store_cols<T, AL>(static_cast<T *>(a.out) + off, (t + i * tpr) * VEC, cols, pack16<T>(f));
-            if (a.quant) {
-                gmax[i] = 0.0f;
-                if (AL || (t + i * tpr) * VEC < cols) {
+            if (!QUANT || a.out)
+                store_cols<T, AL>(static_cast<T *>(a.out) + off, (t + i * tpr) * VEC, cols, pack16<T>(y[i]));
+        }
+        if constexpr (QUANT) {
+            float amax = 0.0f, gmax[NV];
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        const bool in = AL || (t + i * tpr) * VEC + j < cols;
-                        gmax[i] = max_nan(gmax[i], in ? fabsf(f[j]) : 0.0f);
-                    }
+            for (int i = 0; i < NV; ++i) {
+                gmax[i] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    // columns past the row hold 0 * rstd * 0, which is NaN where rstd is
+                    const bool in = (t + i * tpr) * VEC + (AL ? 0 : j) < cols;
+                    gmax[i] = max_nan(gmax[i], in ? fabsf(y[i][j]) : 0.0f);
                 }
                 amax = max_nan(amax, gmax[i]);
             }
-        }
-        if (!a.quant) continue;
-
-        const float top = a.quant == kQuantE4M3 ? 448.0f : 127.0f;
-        // lanes that share 128 columns; a team narrower than that holds rows of at most 128 columns
-        constexpr int GL = 128 / VEC;
-        const bool grouped = a.group != 0 && (TPR == 0 || TPR >= GL);
-        float s_row = 0.0f;
-        if (!grouped) {
-            s_row = max_nan(team_reduce<MaxOp, TPR>(amax, red, turn) / top, kScaleMin);
-            if (t == 0 && live) a.scale[r] = s_row;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = t + i * tpr, c = v * VEC;
-            float s = s_row;
-            if (grouped) {
-                s = max_nan(lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]) / top, kScaleMin);
-                if (v % GL == 0 && c < cols) a.scale[r * a.groups + c / 128] = s;
+            const float top = a.quant == kQuantE4M3 ? 448.0f : 127.0f;
+            // lanes that share 128 columns; a team narrower than that holds rows of at most 128 columns
+            constexpr int GL = 128 / VEC;
+            const bool grouped = a.group != 0 && (TPR == 0 || TPR >= GL);
+            float s = 0.0f, inv = 0.0f;
+            if (!grouped) {
+                s = max_nan(team_reduce<MaxOp, TPR>(amax, red, turn) / top, kScaleMin);
+                inv = 1.0f / s;
+                if (t == 0 && live) a.scale[r] = s;
             }
-            if (c < cols) {
-                const float inv = 1.0f / s;
-                float f[VEC];
-                unpack16<T>(hv[i], f);
-                if (weight) {
-                    float g[VEC];
-                    unpack16<T>(w[i], g);
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) f[j] = f[j] * rstd * g[j];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) f[j] *= rstd;
+            for (int i = 0; i < NV; ++i) {
+                const int v = t + i * tpr, c = v * VEC;
+                if (grouped) {
+                    s = max_nan(lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]) / top, kScaleMin);
+                    inv = 1.0f / s;
+                    if (v % GL == 0 && c < cols) a.scale[r * a.groups + c / 128] = s;
                 }
-                uint32_t q[VEC / 4];
+                if (c < cols) {
+                    uint32_t q[VEC / 4];
 #pragma unroll
-                for (int j = 0; j < VEC / 4; ++j) q[j] = pack8(f + 4 * j, inv, a.quant);
-                unsigned char *dst = static_cast<unsigned char *>(a.out8) + off + c;
-                if constexpr (AL) {
-                    if constexpr (VEC == 8)
-                        *reinterpret_cast<uint2 *>(dst) = make_uint2(q[0], q[1]);
-                    else
-                        *reinterpret_cast<uint32_t *>(dst) = q[0];
-                } else {
+                    for (int j = 0; j < VEC / 4; ++j) q[j] = pack8(y[i] + 4 * j, inv, a.quant);
+                    unsigned char *dst = static_cast<unsigned char *>(a.out8) + off + c;
+                    if constexpr (AL) {
+                        if constexpr (VEC == 8)
+                            *reinterpret_cast<uint2 *>(dst) = make_uint2(q[0], q[1]);
+                        else
+                            *reinterpret_cast<uint32_t *>(dst) = q[0];
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j)
-                        if (c + j < cols) dst[j] = (unsigned char)(q[j / 4] >> (8 * (j % 4)));
+                        for (int j = 0; j < VEC; ++j)
+                            if (c + j < cols) dst[j] = (unsigned char)(q[j / 4] >> (8 * (j % 4)));
+                    }
                 }
             }
         }
@@ -175,11 +173,13 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : 256) norm_forward_kernel(con
 
 template <typename T, int TPR, int NV, bool AL>
 cudaError_t launch_one(const NormArgs &a, int threads, const DeviceInfo *dev, cudaStream_t stream) {
+    constexpr int VEC = Storage<T>::kVec;
     const int teams = TPR == 0 ? 1 : threads / TPR;
     const long long need = (a.rows + teams - 1) / teams;
-    // 2048 threads an SM (the kernels stay below 64 registers, at 32 and fewer they all fit)
-    const long long most = (long long)dev->sms * (2048 / threads);
-    norm_forward_kernel<T, TPR, NV, AL><<<(unsigned)(need < most ? need : most), threads, 0, stream>>>(a);
+    const long long most = (long long)dev->sms * (threads_per_sm(NV * VEC) / threads);
+    const unsigned grid = (unsigned)(need < most ? need : most);
+    if (a.quant) norm_forward_kernel<T, TPR, NV, AL, true><<<grid, threads, 0, stream>>>(a);
+    else norm_forward_kernel<T, TPR, NV, AL, false><<<grid, threads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -188,12 +188,14 @@ template <typename T, bool AL> cudaError_t launch_al(const NormArgs &a, cudaStre
     if (!dev) return cudaErrorNotSupported;
     constexpr int VEC = Storage<T>::kVec;
     const int nvec = (a.cols + VEC - 1) / VEC;
-    if (nvec <= 8) return launch_one<T, 8, 1, AL>(a, 256, dev, stream);
-    if (nvec <= 32) return launch_one<T, 32, 1, AL>(a, 256, dev, stream);
-    if (nvec <= 64) return launch_one<T, 32, 2, AL>(a, 256, dev, stream);
-    if (nvec <= 128) return launch_one<T, 32, 4, AL>(a, 256, dev, stream);
-    const int threads = ((nvec + 3) / 4 + 31) / 32 * 32;  // at most 1024: cols <= 16384
-    return launch_one<T, 0, 4, AL>(a, threads, dev, stream);
+    if (nvec <= 8) return launch_one<T, 8, 1, AL>(a, kTeamThreads, dev, stream);
+    if (nvec <= 32) return launch_one<T, 32, 1, AL>(a, kTeamThreads, dev, stream);
+    if (nvec <= 64) return launch_one<T, 32, 2, AL>(a, kTeamThreads, dev, stream);
+    if (nvec <= 128) return launch_one<T, 32, 4, AL>(a, kTeamThreads, dev, stream);
+    // at most 512 threads: 16 columns each up to 8192, 32 up to 16384
+    const int nv = (a.cols <= 8192 ? 16 : 32) / VEC, threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+    if (nv == 16 / VEC) return launch_one<T, 0, 16 / VEC, AL>(a, threads, dev, stream);
+    return launch_one<T, 0, 32 / VEC, AL>(a, threads, dev, stream);
 }
 
 template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t stream) {

@@ -359,7 +359,8 @@ int64_t dcn_proj_adapters_workspace_bytes(const dadapt_params *p);
  * read before any of it is written), but not the same one; buffers that
  * overlap in any other way give wrong results.
  * A NaN or infinite h makes the statistics of its row NaN or rstd 0; a scale
- * over a NaN is NaN (int8 codes of NaN values are 0, e4m3 codes NaN).
+ * over a NaN is NaN, so the dequantised values are too (e4m3 codes of a NaN are
+ * NaN; int8 codes under a NaN scale mean nothing).
  * cols in [1, 16384], eps > 0.  Tensors are aligned to their element; where
  * all of them are 16-byte aligned and a row is a multiple of 16 bytes the
  * kernel moves 16-byte vectors, else elements.  rows == 0 is a no-op.
