@@ -10,6 +10,7 @@
 #pragma once
 
 #include "dcn_common.cuh"
+#include "dcn_tma.cuh"
 
 namespace dcnb {
 
@@ -78,5 +79,23 @@ template <typename T, bool AL> __device__ __forceinline__ void store_cols(T *row
             if (c + i < cols) row[c + i] = t[i];
     }
 }
+
+// ---- rows staged in shared memory
+//
+// A team's rows are contiguous in memory, so one thread copies them by bulk
+// asynchronous copies into a ring of slots, `slots` rows ahead; the team reads a
+// slot once its barrier has counted the bytes and hands it back behind the
+// barrier (or warp synchronisation) of the row's reduction.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+constexpr uint64_t kRowWaitNs = 1000000000ull;  // 1 s
+
+// Shared memory of the staged kernels: what a CTA may use when `ctas` of them share an SM (227 KB, 1 KB of it
+// taken by the system for each CTA).
+__host__ __device__ constexpr int staged_budget(int ctas) { return 227 * 1024 / ctas - 1024; }
 
 }  // namespace dcnb

@@ -39,6 +39,17 @@ __device__ __forceinline__ uint32_t pack8(const float *y, float inv, int quant) 
     return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
 }
 
+// The codes of a thread's vector at an address that is a multiple of VEC.
+template <int VEC>
+__device__ __forceinline__ void store_codes(unsigned char *dst, const float *y, float inv, int quant) {
+    if constexpr (VEC == 8)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack8(y, inv, quant), pack8(y + 4, inv, quant));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pack8(y, inv, quant);
+}
+
+constexpr int kMaxSlots = 8;
+
 // A thread holds C = NV * VEC columns of a row: up to 16 with the loads of its
 // team's next row in flight meanwhile, or 32 without.  8-lane and warp teams
 // share a CTA of 256 threads, a CTA team has up to 512; CTAs on an SM follow
@@ -151,21 +162,131 @@ __global__ void __launch_bounds__(max_threads<TPR>(), threads_per_sm(NV * Storag
                     if (v % GL == 0 && c < cols) a.scale[r * a.groups + c / 128] = s;
                 }
                 if (c < cols) {
-                    uint32_t q[VEC / 4];
-#pragma unroll
-                    for (int j = 0; j < VEC / 4; ++j) q[j] = pack8(y[i] + 4 * j, inv, a.quant);
                     unsigned char *dst = static_cast<unsigned char *>(a.out8) + off + c;
                     if constexpr (AL) {
-                        if constexpr (VEC == 8)
-                            *reinterpret_cast<uint2 *>(dst) = make_uint2(q[0], q[1]);
-                        else
-                            *reinterpret_cast<uint32_t *>(dst) = q[0];
+                        store_codes<VEC>(dst, y[i], inv, a.quant);
                     } else {
+                        uint32_t q[VEC / 4];
+#pragma unroll
+                        for (int j = 0; j < VEC / 4; ++j) q[j] = pack8(y[i] + 4 * j, inv, a.quant);
 #pragma unroll
                         for (int j = 0; j < VEC; ++j)
                             if (c + j < cols) dst[j] = (unsigned char)(q[j / 4] >> (8 * (j % 4)));
                     }
                 }
+            }
+        }
+    }
+}
+
+// Rows wider than a warp team holds, 16-byte aligned: a CTA of 16 columns a
+// thread per row, the rows staged by bulk copies (bf16 2047 x 4096 to int8: 16.8
+// us with the next row's loads in registers, 13.8 us staged).
+template <typename T, bool QUANT>
+__global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormArgs a, int slots, unsigned int *err) {
+    constexpr int VEC = Storage<T>::kVec, NV = 16 / VEC, GL = 128 / VEC;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ float red[64];
+    __shared__ __align__(8) uint64_t bars[kMaxSlots];
+    const int t = threadIdx.x, tpr = blockDim.x;
+    const uint32_t row_bytes = (uint32_t)a.cols * sizeof(T), slot_bytes = a.residual ? 2 * row_bytes : row_bytes;
+    const T *weight = static_cast<const T *>(a.weight);
+    int turn = 0;
+    if (t == 0) {
+        for (int i = 0; i < slots; ++i) mbar_init(smem_u32(bars + i), 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    auto stage = [&](long long r, int s) {  // by thread 0
+        if (r >= a.rows) return;
+        const uint32_t bar = smem_u32(bars + s), dst = smem_u32(ring) + s * slot_bytes;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load(dst, static_cast<const T *>(a.x) + r * a.cols, row_bytes, bar);
+        if (a.residual) bulk_load(dst + row_bytes, static_cast<const T *>(a.residual) + r * a.cols, row_bytes, bar);
+    };
+    const long long step = gridDim.x;
+    if (t == 0)
+        for (int i = 0; i < slots; ++i) stage(blockIdx.x + i * step, i);
+    uint4 w[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (weight) w[i] = load_cols<T, true>(weight, (t + i * tpr) * VEC, a.cols);
+
+    int s = 0;
+    uint32_t phase = 0;
+    for (long long r = blockIdx.x; r < a.rows; r += step) {
+        const long long off = r * a.cols;
+        if (!mbar_wait_bounded(smem_u32(bars + s), phase, kRowWaitNs)) {
+            atomicOr(err, kDevErrTmaTimeout);
+            return;
+        }
+        const unsigned char *slot = ring + s * slot_bytes;
+        float y[NV][VEC];
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * VEC;
+            unpack16<T>(load_cols<T, true>(reinterpret_cast<const T *>(slot), c, a.cols), y[i]);
+            if (a.residual) {
+                float g[VEC];
+                unpack16<T>(load_cols<T, true>(reinterpret_cast<const T *>(slot + row_bytes), c, a.cols), g);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[i][j] += g[j];
+                const uint4 h = pack16<T>(y[i]);
+                store_cols<T, true>(static_cast<T *>(a.residual_out) + off, c, a.cols, h);
+                unpack16<T>(h, y[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) ss = fmaf(y[i][j], y[i][j], ss);
+        }
+        ss = team_reduce<SumOp, 0>(ss, red, turn);  // behind its barrier the slot has been read
+        if (t == 0) stage(r + slots * step, s);
+        if (++s == slots) {
+            s = 0;
+            phase ^= 1;
+        }
+        const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+        if (a.rstd && t == 0) a.rstd[r] = rstd;
+        float gmax[NV], amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (t + i * tpr) * VEC;
+            if (weight) {
+                float g[VEC];
+                unpack16<T>(w[i], g);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[i][j] = y[i][j] * rstd * g[j];
+            } else {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) y[i][j] *= rstd;
+            }
+            if (!QUANT || a.out) store_cols<T, true>(static_cast<T *>(a.out) + off, c, a.cols, pack16<T>(y[i]));
+            if (QUANT) {
+                gmax[i] = 0.0f;
+                if (c < a.cols) {
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) gmax[i] = max_nan(gmax[i], fabsf(y[i][j]));
+                }
+                amax = max_nan(amax, gmax[i]);
+            }
+        }
+        if constexpr (QUANT) {
+            const float top = a.quant == kQuantE4M3 ? 448.0f : 127.0f;
+            float sc = 0.0f, inv = 0.0f;
+            if (!a.group) {
+                sc = max_nan(team_reduce<MaxOp, 0>(amax, red, turn) / top, kScaleMin);
+                inv = 1.0f / sc;
+                if (t == 0) a.scale[r] = sc;
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = t + i * tpr, c = v * VEC;
+                if (a.group) {
+                    sc = max_nan(lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]) / top, kScaleMin);
+                    inv = 1.0f / sc;
+                    if (v % GL == 0 && c < a.cols) a.scale[r * a.groups + c / 128] = sc;
+                }
+                if (c < a.cols) store_codes<VEC>(static_cast<unsigned char *>(a.out8) + off + c, y[i], inv, a.quant);
             }
         }
     }
@@ -183,6 +304,26 @@ cudaError_t launch_one(const NormArgs &a, int threads, const DeviceInfo *dev, cu
     return cudaGetLastError();
 }
 
+template <typename T> cudaError_t launch_wide(const NormArgs &a, const DeviceInfo *dev, cudaStream_t stream) {
+    const int threads = ((a.cols + 15) / 16 + 31) / 32 * 32;  // at most 1024
+    const int slot = a.cols * (int)sizeof(T) * (a.residual ? 2 : 1);
+    // as many CTAs as the registers allow (64 a thread), fewer where a slot would not fit their share
+    int per_sm = 1024 / threads;
+    if (per_sm > 8) per_sm = 8;
+    while (per_sm > 1 && 2 * slot > staged_budget(per_sm)) --per_sm;
+    int slots = staged_budget(per_sm) / slot;
+    if (slots > 4) slots = 4;
+    const int smem = slots * slot;
+    cudaError_t e = cudaFuncSetAttribute(a.quant ? norm_forward_wide_kernel<T, true> : norm_forward_wide_kernel<T, false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long most = (long long)dev->sms * per_sm;
+    const unsigned grid = (unsigned)(a.rows < most ? a.rows : most);
+    if (a.quant) norm_forward_wide_kernel<T, true><<<grid, threads, smem, stream>>>(a, slots, dev->err);
+    else norm_forward_wide_kernel<T, false><<<grid, threads, smem, stream>>>(a, slots, dev->err);
+    return cudaGetLastError();
+}
+
 template <typename T, bool AL> cudaError_t launch_al(const NormArgs &a, cudaStream_t stream) {
     const DeviceInfo *dev = device_info();
     if (!dev) return cudaErrorNotSupported;
@@ -192,10 +333,14 @@ template <typename T, bool AL> cudaError_t launch_al(const NormArgs &a, cudaStre
     if (nvec <= 32) return launch_one<T, 32, 1, AL>(a, kTeamThreads, dev, stream);
     if (nvec <= 64) return launch_one<T, 32, 2, AL>(a, kTeamThreads, dev, stream);
     if (nvec <= 128) return launch_one<T, 32, 4, AL>(a, kTeamThreads, dev, stream);
-    // at most 512 threads: 16 columns each up to 8192, 32 up to 16384
-    const int nv = (a.cols <= 8192 ? 16 : 32) / VEC, threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
-    if (nv == 16 / VEC) return launch_one<T, 0, 16 / VEC, AL>(a, threads, dev, stream);
-    return launch_one<T, 0, 32 / VEC, AL>(a, threads, dev, stream);
+    if constexpr (AL) {
+        return launch_wide<T>(a, dev, stream);
+    } else {
+        // at most 512 threads: 16 columns each up to 8192, 32 up to 16384
+        const int nv = (a.cols <= 8192 ? 16 : 32) / VEC, threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+        if (nv == 16 / VEC) return launch_one<T, 0, 16 / VEC, AL>(a, threads, dev, stream);
+        return launch_one<T, 0, 32 / VEC, AL>(a, threads, dev, stream);
+    }
 }
 
 template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t stream) {
