@@ -532,11 +532,10 @@ dcn_status dcn_add_rms_norm_backward(const dnorm_params *p, const void *grad_out
         !aligned(rstd, 4))
         return fail(DCN_ERR_ALIGN, "tensors must be aligned to their element");
     dcnb::NormArgs a = norm_args(p);
-    a.partial_rows = dcnb::norm_backward_partial_rows(p->rows, p->cols, (dcnb::DType)p->dtype);
     if (grad_weight) {
         if (!workspace) return fail(DCN_ERR_NULL, "workspace is required with a weight");
         if (!aligned(workspace, 16)) return fail(DCN_ERR_ALIGN, "workspace must be 16-byte aligned");
-        const long long need = (long long)a.partial_rows * p->cols * 4;
+        const long long need = dcn_add_rms_norm_backward_workspace_bytes(p);
         if (workspace_bytes < need)
             return fail(DCN_ERR_SHAPE, "workspace has %lld bytes, %lld needed", (long long)workspace_bytes, need);
     }

@@ -72,9 +72,9 @@ struct NormArgs {
     float *rstd;                        // [rows]: written by the forward (or nullptr), read by the backward
     const void *h, *grad_out, *grad_residual_out;  // backward; grad_residual_out may be nullptr
     void *grad_x, *grad_weight;         // backward; grad_weight may be nullptr
-    float *partial;                     // backward: [partial_rows, cols] partial weight gradients
+    float *partial;                     // backward: [norm_backward_partial_rows(), cols] partial weight gradients
     int64_t rows;
-    int cols, partial_rows;
+    int cols;
     float eps;
     int quant, group, groups;           // group: 0 or 128 columns per scale
     DType dtype;

@@ -53,6 +53,24 @@ template <typename OP, int TPR> __device__ __forceinline__ float team_reduce(flo
     }
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t f2_bits(float2 a) { return *reinterpret_cast<uint64_t *>(&a); }
+__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
 // The VEC columns starting at column c of a row, as raw storage (zeros past the end).
 template <typename T, bool AL> __device__ __forceinline__ uint4 load_cols(const T *row, int c, int cols) {
     uint4 v = make_uint4(0, 0, 0, 0);
@@ -94,8 +112,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 constexpr uint64_t kRowWaitNs = 1000000000ull;  // 1 s
 
-// Shared memory of the staged kernels: what a CTA may use when `ctas` of them share an SM (227 KB, 1 KB of it
-// taken by the system for each CTA).
-__host__ __device__ constexpr int staged_budget(int ctas) { return 227 * 1024 / ctas - 1024; }
+// A wait for slot s ran out: reports it, and waits (again with a limit) for the other slots' copies in flight.
+__device__ __forceinline__ void give_up(uint32_t bars, int s, uint32_t phase, int slots, unsigned int *err) {
+    atomicOr(err, kDevErrTmaTimeout);
+    for (int i = 1; i < slots; ++i) {
+        const int k = s + i < slots ? s + i : s + i - slots;
+        mbar_wait_bounded(bars + 8 * k, s + i < slots ? phase : phase ^ 1u, kRowWaitNs / 8);
+    }
+}
+
+// Shared memory of the staged kernels: what a CTA may use when `ctas` of them share an SM (227 KB; the system takes
+// 1 KB for each CTA, the kernels' barriers and sums another).
+__host__ __device__ constexpr int staged_budget(int ctas) { return 227 * 1024 / ctas - 2048; }
 
 }  // namespace dcnb

@@ -11,6 +11,7 @@
 // kernel adds those rows in a fixed order, so the result does not depend on
 // timing (no atomics).
 #include "dcn_device.h"
+#include "dcn_host.h"
 #include "dcn_launch.h"
 #include "dcn_norm.cuh"
 
@@ -20,11 +21,66 @@ namespace {
 constexpr int kTeamThreads = 512;  // CTA of 8-lane and warp teams
 constexpr int kSms = 148;
 
+// One row of partial sums of the weight gradient from the CTA's first WARPS warps.  Narrow teams add up pairs of
+// warps through shared memory (`sums`, kSumBytes), halving their number each time; 8-lane teams of a warp first
+// among themselves.
+template <typename T, int NV, int WARPS> constexpr int kSumFloats = (WARPS / 2) * 32 * NV * Storage<T>::kVec;
+template <typename T, int TPR, int NV, int WARPS>
+__device__ __forceinline__ void store_partial(const NormArgs &a, float2 (&gw)[NV][Storage<T>::kVec / 2], float *sums, int t,
+                                              int tpr) {
+    constexpr int VEC = Storage<T>::kVec;
+    float *part = a.partial + (long long)blockIdx.x * a.cols;
+    if constexpr (TPR != 0) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        auto sync = [] { asm volatile("bar.sync 1, %0;" ::"r"(WARPS * 32) : "memory"); };
+        if (TPR == 8) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j)
+#pragma unroll
+                    for (int o = 8; o < 32; o <<= 1) {
+                        gw[i][j].x += __shfl_xor_sync(0xffffffffu, gw[i][j].x, o);
+                        gw[i][j].y += __shfl_xor_sync(0xffffffffu, gw[i][j].y, o);
+                    }
+        }
+        // float2 k of a lane at [k][lane]: neighbouring lanes use neighbouring banks
+        float2 *slots = reinterpret_cast<float2 *>(sums);
+        constexpr int K = NV * VEC / 2;
+        sync();  // whatever was in `sums` has been read
+#pragma unroll
+        for (int n = WARPS; n > 1;) {
+            const int half = (n + 1) / 2;
+            if (warp >= half && warp < n) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) slots[((warp - half) * K + k) * 32 + lane] = gw[k / (VEC / 2)][k % (VEC / 2)];
+            }
+            sync();
+            if (warp < n - half) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    gw[k / (VEC / 2)][k % (VEC / 2)] =
+                        f2_add(gw[k / (VEC / 2)][k % (VEC / 2)], slots[(warp * K + k) * 32 + lane]);
+            }
+            sync();
+            n = half;
+        }
+        if (warp != 0 || lane >= TPR) return;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const int c = (t + i * tpr) * VEC + j;
+            if (c < a.cols) part[c] = j % 2 ? gw[i][j / 2].y : gw[i][j / 2].x;
+        }
+}
+
 template <typename T, int TPR, int NV, bool AL>
 __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 || NV * Storage<T>::kVec > 8 ? 1 : 2)
     norm_backward_kernel(const NormArgs a) {
     constexpr int VEC = Storage<T>::kVec;
-    __shared__ float red[TPR == 0 ? 64 : 32 * NV * VEC];
+    __shared__ __align__(16) float red[TPR == 0 ? 64 : kSumFloats<T, NV, kTeamThreads / 32>];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
     const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
@@ -33,21 +89,21 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 || NV
     int turn = 0;
     const T *hp = static_cast<const T *>(a.h), *gyp = static_cast<const T *>(a.grad_out);
     const T *ghp = static_cast<const T *>(a.grad_residual_out), *weight = static_cast<const T *>(a.weight);
-    uint4 w[NV];
-    float gw[NV][VEC];
+    float2 w[NV][VEC / 2], gw[NV][VEC / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (weight) w[i] = load_cols<T, AL>(weight, (t + i * tpr) * VEC, a.cols);
+        if (weight) unpack16x2<T>(load_cols<T, AL>(weight, (t + i * tpr) * VEC, a.cols), w[i]);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) gw[i][j] = 0.0f;
+        for (int j = 0; j < VEC / 2; ++j) {
+            if (!weight) w[i][j] = make_float2(1.0f, 1.0f);
+            gw[i][j] = make_float2(0.0f, 0.0f);
+        }
     }
     const float inv_cols = 1.0f / (float)a.cols;
     const long long step = (long long)gridDim.x * teams;
-    // With one or two fp32 vectors a thread, the loads of a team's next row are in flight while it works on
-    // the current one (bf16 102400 x 256: 46.1 -> 38.5 us); wider threads have no registers left for it
-    // (fp32 12800 x 512: 29.5 us without, 32.5 us with, spilling).
-    constexpr bool AHEAD = NV * VEC <= 8;
-    uint4 hn[NV], gn[NV], rn[NV];
+    // the loads of a narrow team's next row are in flight while it works on the current one
+    constexpr bool AHEAD = NV * VEC <= 8 && TPR != 0;
+    uint4 hn[NV], gn[NV];
     float sn = 0.0f;
     auto fetch = [&](long long r) {
         const bool live = r < a.rows;
@@ -58,7 +114,6 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 || NV
         for (int i = 0; i < NV; ++i) {
             hn[i] = load_cols<T, AL>(hp + off, (t + i * tpr) * VEC, cols);
             gn[i] = load_cols<T, AL>(gyp + off, (t + i * tpr) * VEC, cols);
-            if (ghp) rn[i] = load_cols<T, AL>(ghp + off, (t + i * tpr) * VEC, cols);
         }
     };
     if (AHEAD) fetch((long long)blockIdx.x * teams + team);
@@ -66,153 +121,384 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 || NV
         const long long r = base + team;
         const bool live = r < a.rows;
         if (!AHEAD) fetch(r);
-        uint4 hv[NV], gv[NV], rv[NV];
         const float rstd = sn;
+        float2 xh[NV][VEC / 2], gy[NV][VEC / 2], dot2 = make_float2(0.0f, 0.0f);
+        uint4 rv[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            hv[i] = hn[i];
-            gv[i] = gn[i];
-            rv[i] = ghp ? rn[i] : make_uint4(0, 0, 0, 0);
+            unpack16x2<T>(hn[i], xh[i]);
+            unpack16x2<T>(gn[i], gy[i]);
+            // needed only behind the reduction, so not a row ahead
+            if (ghp) rv[i] = load_cols<T, AL>(ghp + (live ? r * a.cols : 0), (t + i * tpr) * VEC, live ? a.cols : 0);
         }
         if (AHEAD) fetch(r + step);
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float h[VEC], gy[VEC], wf[VEC];
-            unpack16<T>(hv[i], h);
-            unpack16<T>(gv[i], gy);
-            if (weight) unpack16<T>(w[i], wf);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float p = gy[j] * (h[j] * rstd);
-                gw[i][j] += p;
-                dot = weight ? fmaf(p, wf[j], dot) : dot + p;
-            }
-        }
-        dot = team_reduce<SumOp, TPR>(dot, red, turn) * inv_cols;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float h[VEC], gy[VEC], wf[VEC], o[VEC];
-            unpack16<T>(hv[i], h);
-            unpack16<T>(gv[i], gy);
-            if (weight) unpack16<T>(w[i], wf);
-            unpack16<T>(rv[i], o);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float g = weight ? gy[j] * wf[j] : gy[j];
-                const float gx = rstd * (g - h[j] * rstd * dot);
-                o[j] = ghp ? gx + o[j] : gx;
-            }
-            store_cols<T, AL>(static_cast<T *>(a.grad_x) + (live ? r * a.cols : 0), (t + i * tpr) * VEC,
-                              live ? a.cols : 0, pack16<T>(o));
-        }
-    }
-    if (!a.grad_weight) return;
-    float *part = a.partial + (long long)blockIdx.x * a.cols;
-    if constexpr (TPR == 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < VEC; ++j)
-                if ((t + i * tpr) * VEC + j < a.cols) part[(t + i * tpr) * VEC + j] = gw[i][j];
-    } else {
-        // one warp after the other adds its columns to the CTA's sums; 8-lane teams of a warp first
-        // among themselves
-        constexpr int W = TPR * NV * VEC;
-        for (int k = 0; k < kTeamThreads / 32; ++k) {
-            if ((int)threadIdx.x / 32 == k) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) {
-                        float v = gw[i][j];
-                        if (TPR == 8) {
-                            v += __shfl_xor_sync(0xffffffffu, v, 8);
-                            v += __shfl_xor_sync(0xffffffffu, v, 16);
-                        }
-                        // lane-major, so neighbouring lanes use neighbouring banks
-                        float *s = red + (i * VEC + j) * TPR + t;
-                        if (TPR == 32 || (threadIdx.x & 31) < TPR) *s = k ? *s + v : v;
-                    }
+            for (int j = 0; j < VEC / 2; ++j) {
+                xh[i][j] = f2_mul(xh[i][j], make_float2(rstd, rstd));
+                const float2 p = f2_mul(gy[i][j], xh[i][j]);
+                gw[i][j] = f2_add(gw[i][j], p);
+                dot2 = f2_fma(p, w[i][j], dot2);
             }
-            __syncthreads();
+        const float dot = -team_reduce<SumOp, TPR>(dot2.x + dot2.y, red, turn) * inv_cols;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float2 o[VEC / 2];
+            if (ghp) unpack16x2<T>(rv[i], o);
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) {
+                // rstd * (g - xh * mean(g * xh)) + grad_residual_out
+                const float2 d = f2_fma(xh[i][j], make_float2(dot, dot), f2_mul(gy[i][j], w[i][j]));
+                o[j] = ghp ? f2_fma(d, make_float2(rstd, rstd), o[j]) : f2_mul(d, make_float2(rstd, rstd));
+            }
+            store_cols<T, AL>(static_cast<T *>(a.grad_x) + (live ? r * a.cols : 0), (t + i * tpr) * VEC,
+                              live ? a.cols : 0, pack16<T>(reinterpret_cast<const float *>(o)));
         }
-        for (int c = threadIdx.x; c < W && c < a.cols; c += kTeamThreads) {
-            const int v = c / VEC;
-            part[c] = red[(v / TPR * VEC + c % VEC) * TPR + v % TPR];
+    }
+    if (!a.grad_weight) return;
+    store_partial<T, TPR, NV, kTeamThreads / 32>(a, gw, red, t, tpr);
+}
+
+// A row's products from its staged tensors: xh and grad_out in registers, the weight gradient, and this thread's part
+// of sum(g * xh).
+template <typename T, int NV>
+__device__ __forceinline__ float staged_row(const unsigned char *h, const unsigned char *g, int t, int tpr, int cols,
+                                            float rstd, const float2 (&w)[NV][Storage<T>::kVec / 2],
+                                            float2 (&xh)[NV][Storage<T>::kVec / 2], float2 (&gy)[NV][Storage<T>::kVec / 2],
+                                            float2 (&gw)[NV][Storage<T>::kVec / 2]) {
+    constexpr int VEC = Storage<T>::kVec;
+    float2 dot = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * tpr) * VEC;
+        unpack16x2<T>(load_cols<T, true>(reinterpret_cast<const T *>(h), c, cols), xh[i]);
+        unpack16x2<T>(load_cols<T, true>(reinterpret_cast<const T *>(g), c, cols), gy[i]);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+            xh[i][j] = f2_mul(xh[i][j], make_float2(rstd, rstd));
+            const float2 p = f2_mul(gy[i][j], xh[i][j]);
+            gw[i][j] = f2_add(gw[i][j], p);
+            dot = f2_fma(p, w[i][j], dot);
+        }
+    }
+    return dot.x + dot.y;
+}
+
+// grad_x of the row; `r` the staged gradient of the new residual, or nullptr.
+template <typename T, int NV>
+__device__ __forceinline__ void staged_output(T *out, const unsigned char *r, int t, int tpr, int cols, float rstd,
+                                              float mean, const float2 (&w)[NV][Storage<T>::kVec / 2],
+                                              const float2 (&xh)[NV][Storage<T>::kVec / 2],
+                                              const float2 (&gy)[NV][Storage<T>::kVec / 2]) {
+    constexpr int VEC = Storage<T>::kVec;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * tpr) * VEC;
+        float2 o[VEC / 2];
+        if (r) unpack16x2<T>(load_cols<T, true>(reinterpret_cast<const T *>(r), c, cols), o);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+            const float2 d = f2_fma(xh[i][j], make_float2(-mean, -mean), f2_mul(gy[i][j], w[i][j]));
+            o[j] = r ? f2_fma(d, make_float2(rstd, rstd), o[j]) : f2_mul(d, make_float2(rstd, rstd));
+        }
+        store_cols<T, true>(out, c, cols, pack16<T>(reinterpret_cast<const float *>(o)));
+    }
+}
+
+template <typename T, int NV>
+__device__ __forceinline__ void load_weight(const NormArgs &a, int t, int tpr, float2 (&w)[NV][Storage<T>::kVec / 2],
+                                            float2 (&gw)[NV][Storage<T>::kVec / 2]) {
+    constexpr int VEC = Storage<T>::kVec;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (a.weight)
+            unpack16x2<T>(load_cols<T, true>(static_cast<const T *>(a.weight), (t + i * tpr) * VEC, a.cols), w[i]);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+            if (!a.weight) w[i][j] = make_float2(1.0f, 1.0f);
+            gw[i][j] = make_float2(0.0f, 0.0f);
         }
     }
 }
 
-// grad_weight[c] = sum over the CTAs of the first kernel, in a fixed order.  8
-// columns (one 32-byte sector of a row of partial sums) and 128 threads along
-// the rows: a few loads per thread, all in flight at once.
-constexpr int kRedX = 8, kRedY = 128;
+constexpr int kMaxSlots = 8;
+
+// Rows of up to 128 vectors, 16-byte aligned: WARPS rows at a time, one per warp, are contiguous in memory, and a
+// further warp copies such tiles of the two or three tensors into a ring in shared memory, one bulk copy each
+// (copies of single rows measured 51 us where tiles take XX: bf16 102400 x 256).
+template <typename T, int NV, int WARPS, int CTAS>
+__global__ void __launch_bounds__((WARPS + 1) * 32, CTAS)
+    norm_backward_tiles_kernel(const NormArgs a, int slots, unsigned int *err) {
+    constexpr int VEC = Storage<T>::kVec;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxSlots];  // full, empty
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int warp = threadIdx.x >> 5, t = threadIdx.x & 31;
+    const uint32_t row_bytes = (uint32_t)a.cols * sizeof(T), tile_bytes = WARPS * row_bytes;
+    const uint32_t slot_bytes = (a.grad_residual_out ? 3 : 2) * tile_bytes;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kMaxSlots;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < slots; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, WARPS);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const long long tiles = (a.rows + WARPS - 1) / WARPS;
+    int s = 0;
+    uint32_t phase = 0;
+    if (warp == WARPS) {
+        if (t == 0) {
+            for (long long i = blockIdx.x; i < tiles; i += gridDim.x) {
+                // (the first pass over the ring waits for the phase before the first, which counts as complete)
+                if (!mbar_wait_bounded(empty + 8 * s, phase ^ 1u, kRowWaitNs)) {
+                    atomicOr(err, kDevErrTmaTimeout);
+                    break;
+                }
+                const long long r = i * WARPS, off = r * a.cols, left = a.rows - r;
+                const uint32_t bytes = (uint32_t)(left < WARPS ? left : WARPS) * row_bytes;
+                const uint32_t bar = full + 8 * s, dst = smem_u32(ring) + s * slot_bytes;
+                mbar_arrive_expect_tx(bar, (a.grad_residual_out ? 3 : 2) * bytes);
+                bulk_load(dst, static_cast<const T *>(a.h) + off, bytes, bar);
+                bulk_load(dst + tile_bytes, static_cast<const T *>(a.grad_out) + off, bytes, bar);
+                if (a.grad_residual_out)
+                    bulk_load(dst + 2 * tile_bytes, static_cast<const T *>(a.grad_residual_out) + off, bytes, bar);
+                if (++s == slots) {
+                    s = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        return;
+    }
+    float2 w[NV][VEC / 2], gw[NV][VEC / 2];
+    load_weight<T, NV>(a, t, 32, w, gw);
+    const float inv_cols = 1.0f / (float)a.cols;
+    const long long step = (long long)gridDim.x * WARPS;
+    long long r = (long long)blockIdx.x * WARPS + warp;
+    float next_rstd = r < a.rows ? __ldg(a.rstd + r) : 0.0f;
+    for (long long i = blockIdx.x; i < tiles; i += gridDim.x, r += step) {
+        const float rstd = next_rstd;
+        next_rstd = r + step < a.rows ? __ldg(a.rstd + r + step) : 0.0f;
+        if (!mbar_wait_bounded(full + 8 * s, phase, kRowWaitNs)) {
+            if (t == 0) atomicOr(err, kDevErrTmaTimeout);
+            break;
+        }
+        if (r < a.rows) {
+            const unsigned char *base = ring + s * slot_bytes + warp * row_bytes;
+            float2 xh[NV][VEC / 2], gy[NV][VEC / 2];
+            float dot = staged_row<T, NV>(base, base + tile_bytes, t, 32, a.cols, rstd, w, xh, gy, gw);
+            dot = lanes_reduce<SumOp, 32>(dot) * inv_cols;
+            staged_output<T, NV>(static_cast<T *>(a.grad_x) + r * a.cols,
+                                 a.grad_residual_out ? base + 2 * tile_bytes : nullptr, t, 32, a.cols, rstd, dot, w, xh, gy);
+        }
+        __syncwarp();
+        if (t == 0) mbar_arrive(empty + 8 * s);
+        if (++s == slots) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    if (!a.grad_weight) return;
+    // every tile has been read: the ring is free (two slots of WARPS rows hold more than the sums of WARPS / 2)
+    store_partial<T, 32, NV, WARPS>(a, gw, reinterpret_cast<float *>(ring), t, 32);
+}
+
+// Wider rows, 16-byte aligned, of up to 8192 columns: a CTA of 16 columns a thread per row, each row of the tensors
+// copied into the ring by one bulk copy.  The slot of a row is handed back behind the barrier of the next row's
+// reduction, when the whole CTA is past its output.
 template <typename T>
-__global__ void __launch_bounds__(kRedX *kRedY) norm_grad_weight_kernel(const float *partial, int n, int cols, T *out) {
-    __shared__ float s[kRedY][kRedX];
+__global__ void __launch_bounds__(512, 1) norm_backward_wide_kernel(const NormArgs a, int slots, unsigned int *err) {
+    constexpr int VEC = Storage<T>::kVec, NV = 16 / VEC;
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ float red[64];
+    __shared__ __align__(8) uint64_t bars_s[kMaxSlots];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int t = threadIdx.x, tpr = blockDim.x;
+    const uint32_t row_bytes = (uint32_t)a.cols * sizeof(T), slot_bytes = (a.grad_residual_out ? 3 : 2) * row_bytes;
+    const uint32_t bars = smem_u32(bars_s);
+    int turn = 0;
+    if (t == 0) {
+        for (int i = 0; i < slots; ++i) mbar_init(bars + 8 * i, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    auto stage = [&](long long r, int s) {  // by thread 0
+        if (r >= a.rows) return;
+        const uint32_t bar = bars + 8 * s, dst = smem_u32(ring) + s * slot_bytes;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load(dst, static_cast<const T *>(a.h) + r * a.cols, row_bytes, bar);
+        bulk_load(dst + row_bytes, static_cast<const T *>(a.grad_out) + r * a.cols, row_bytes, bar);
+        if (a.grad_residual_out)
+            bulk_load(dst + 2 * row_bytes, static_cast<const T *>(a.grad_residual_out) + r * a.cols, row_bytes, bar);
+    };
+    const long long step = gridDim.x, first = blockIdx.x;
+    if (t == 0)
+        for (int i = 0; i < slots; ++i) stage(first + i * step, i);
+    float2 w[NV][VEC / 2], gw[NV][VEC / 2];
+    load_weight<T, NV>(a, t, tpr, w, gw);
+    const float inv_cols = 1.0f / (float)a.cols;
+    float next_rstd = first < a.rows ? __ldg(a.rstd + first) : 0.0f;
+    int s = 0;
+    uint32_t phase = 0;
+    for (long long r = first; r < a.rows; r += step) {
+        const float rstd = next_rstd;
+        next_rstd = r + step < a.rows ? __ldg(a.rstd + r + step) : 0.0f;
+        if (!mbar_wait_bounded(bars + 8 * s, phase, kRowWaitNs)) {
+            give_up(bars, s, phase, slots, err);
+            return;
+        }
+        const unsigned char *base = ring + s * slot_bytes;
+        float2 xh[NV][VEC / 2], gy[NV][VEC / 2];
+        float dot = staged_row<T, NV>(base, base + row_bytes, t, tpr, a.cols, rstd, w, xh, gy, gw);
+        dot = team_reduce<SumOp, 0>(dot, red, turn) * inv_cols;
+        if (t == 0 && r != first) stage(r + (slots - 1) * step, s ? s - 1 : slots - 1);
+        staged_output<T, NV>(static_cast<T *>(a.grad_x) + r * a.cols, a.grad_residual_out ? base + 2 * row_bytes : nullptr,
+                             t, tpr, a.cols, rstd, dot, w, xh, gy);
+        if (++s == slots) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    if (!a.grad_weight) return;
+    store_partial<T, 0, NV, 0>(a, gw, red, t, tpr);
+}
+
+// grad_weight[c] = sum over the CTAs of the first kernel, in a fixed order: 8
+// columns (one 32-byte sector of a row of partial sums) and Y threads along the
+// rows, so that a thread has a few loads and all of them in flight at once.
+constexpr int kRedX = 8;
+template <typename T, int Y>
+__global__ void __launch_bounds__(kRedX *Y) norm_grad_weight_kernel(const float *partial, int n, int cols, T *out) {
+    __shared__ float s[Y / 4][kRedX];
     const int x = threadIdx.x % kRedX, y = threadIdx.x / kRedX, c = blockIdx.x * kRedX + x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float v = 0.0f;
     if (c < cols) {
-#pragma unroll 4
-        for (int k = y; k < n; k += kRedY) v += __ldcg(partial + (long long)k * cols + c);
+#pragma unroll 8
+        for (int k = y; k < n; k += Y) v += __ldcg(partial + (long long)k * cols + c);
     }
-    s[y][x] = v;
+    // the 4 threads of a warp that share a column, then the warps
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    s[y / 4][x] = v;
     __syncthreads();
+    if (y == 0 && c < cols) {
 #pragma unroll
-    for (int h = kRedY / 2; h > 0; h >>= 1) {
-        if (y < h) s[y][x] += s[y + h][x];
-        __syncthreads();
+        for (int k = 1; k < Y / 4; ++k) v += s[k][x];
+        out[c] = from_f32<T>(v);
     }
-    if (y == 0 && c < cols) out[c] = from_f32<T>(s[0][x]);
 }
 
-// Team, CTA size and CTAs on an SM for a row of nvec vectors (16-byte vectors
-// of 4 or 8 columns).  A warp holds up to 128 vectors in registers; wider rows
-// take a CTA with 16 columns a thread.
+// How a row is worked on: teams of 8 lanes, a warp or a CTA (tpr = 0), nv vectors a thread, `rows` of them in a
+// CTA at a time, `per_sm` CTAs on an SM; staged through shared memory or not.
 struct Config {
-    int tpr, nv, threads, per_sm;
+    int tpr, nv, threads, rows, per_sm;
+    bool staged;
 };
-Config config_of(int cols, int vec) {
-    const int nvec = (cols + vec - 1) / vec;
-    if (nvec <= 8) return {8, 1, kTeamThreads, 2};
-    if (nvec <= 32) return {32, 1, kTeamThreads, 2};
-    if (nvec <= 64) return {32, 2, kTeamThreads, vec == 4 ? 2 : 1};
-    if (nvec <= 128) return {32, 4, kTeamThreads, 1};
-    const int nv = 16 / vec, threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;  // at most 1024: cols <= 16384
-    const int fit = 1024 / threads;
-    return {0, nv, threads, fit < 8 ? fit : 8};
+Config config_of(int cols, int vec, bool aligned) {
+    const int nvec = (cols + vec - 1) / vec, nv16 = 16 / vec;
+    if (nvec <= 8) return {8, 1, kTeamThreads, kTeamThreads / 8, 2, false};
+    if (nvec <= 128) {
+        const int nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, c = nv * vec;
+        if (!aligned) return {32, nv, kTeamThreads, kTeamThreads / 32, c <= 8 ? 2 : 1, false};
+        // columns a thread -> registers -> consumer warps: 72 registers for two CTAs of 13 warps, 112 for one of 17
+        if (c <= 8) return {32, nv, 13 * 32, 12, 2, true};
+        if (c <= 16) return {32, nv, 17 * 32, 16, 1, true};
+        return {32, nv, 13 * 32, 12, 1, true};
+    }
+    const int threads = ((nvec + nv16 - 1) / nv16 + 31) / 32 * 32;  // at most 1024: cols <= 16384
+    if (!aligned || cols > 8192) {
+        const int fit = 1024 / threads;
+        return {0, nv16, threads, 1, fit < 8 ? fit : 8, false};
+    }
+    int per_sm = 512 / threads < 4 ? 512 / threads : 4;
+    // fewer CTAs where two staged rows of three tensors would not fit their share of the shared memory
+    while (per_sm > 1 && 2 * 3 * cols * (16 / vec) > staged_budget(per_sm)) --per_sm;
+    return {0, nv16, threads, 1, per_sm, true};
 }
 
-template <typename T, int TPR, int NV, bool AL>
-cudaError_t launch_one(const NormArgs &a, int threads, cudaStream_t stream) {
-    const int teams = TPR == 0 ? 1 : threads / TPR;
-    const long long need = (a.rows + teams - 1) / teams;
-    const int grid = (int)(need < a.partial_rows ? need : a.partial_rows);
-    norm_backward_kernel<T, TPR, NV, AL><<<grid, threads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.grad_weight) return e;
+int grid_of(int64_t rows, const Config &c) {
+    const int64_t need = (rows + c.rows - 1) / c.rows, most = (int64_t)kSms * c.per_sm;
+    return (int)(need < most ? need : most);
+}
+
+template <typename T> cudaError_t launch_grad_weight(const NormArgs &a, int n, cudaStream_t stream) {
+    if (!a.grad_weight) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.cols + kRedX - 1) / kRedX));
-    cfg.blockDim = dim3(kRedX * kRedY);
+    const bool many = n > 32;  // rows of partial sums
+    cfg.blockDim = dim3(kRedX * (many ? 64 : 8));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_grad_weight_kernel<T>, (const float *)a.partial, grid, a.cols,
-                              static_cast<T *>(a.grad_weight));
+    return cudaLaunchKernelEx(&cfg, many ? norm_grad_weight_kernel<T, 64> : norm_grad_weight_kernel<T, 8>,
+                              (const float *)a.partial, n, a.cols, static_cast<T *>(a.grad_weight));
+}
+
+template <typename T, int TPR, int NV, bool AL>
+cudaError_t launch_plain(const NormArgs &a, const Config &c, cudaStream_t stream) {
+    norm_backward_kernel<T, TPR, NV, AL><<<grid_of(a.rows, c), c.threads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+// Staged launch: as many slots as fit, at least two.
+template <typename K>
+cudaError_t launch_staged(K kern, const NormArgs &a, const Config &c, int budget, int es, std::atomic<bool> (&ok)[kMaxDev],
+                          const DeviceInfo *dev, cudaStream_t stream) {
+    const int slot = a.cols * es * (a.grad_residual_out ? 3 : 2) * c.rows;
+    int slots = budget / slot;
+    if (slots > kMaxSlots) slots = kMaxSlots;
+    const cudaError_t e = allow_smem(kern, staged_budget(1), ok);
+    if (e != cudaSuccess) return e;
+    kern<<<grid_of(a.rows, c), c.threads, slots * slot, stream>>>(a, slots, dev->err);
+    return cudaGetLastError();
+}
+
+template <typename T, int NV, int WARPS, int CTAS>
+cudaError_t launch_tiles(const NormArgs &a, const Config &c, const DeviceInfo *dev, cudaStream_t stream) {
+    static std::atomic<bool> ok[kMaxDev];
+    return launch_staged(norm_backward_tiles_kernel<T, NV, WARPS, CTAS>, a, c, staged_budget(CTAS),
+                         (int)sizeof(T), ok, dev, stream);
+}
+
+template <typename T, bool AL> cudaError_t launch_first(const NormArgs &a, const Config &c, cudaStream_t stream) {
+    constexpr int VEC = Storage<T>::kVec, NVC = 16 / VEC;
+    if (c.tpr == 8) return launch_plain<T, 8, 1, AL>(a, c, stream);
+    if constexpr (AL) {
+        const DeviceInfo *dev = device_info();
+        if (!dev) return cudaErrorNotSupported;
+        if (c.tpr == 32 && c.nv == 1) return launch_tiles<T, 1, 12, 2>(a, c, dev, stream);
+        if (c.tpr == 32 && c.nv == 2) {
+            if constexpr (VEC == 4) return launch_tiles<T, 2, 12, 2>(a, c, dev, stream);
+            else return launch_tiles<T, 2, 16, 1>(a, c, dev, stream);
+        }
+        if (c.tpr == 32) {
+            if constexpr (VEC == 4) return launch_tiles<T, 4, 16, 1>(a, c, dev, stream);
+            else return launch_tiles<T, 4, 12, 1>(a, c, dev, stream);
+        }
+        if (c.staged) {
+            static std::atomic<bool> ok[kMaxDev];
+            return launch_staged(norm_backward_wide_kernel<T>, a, c, staged_budget(c.per_sm), (int)sizeof(T), ok, dev,
+                                 stream);
+        }
+    } else {
+        if (c.tpr == 32 && c.nv == 1) return launch_plain<T, 32, 1, AL>(a, c, stream);
+        if (c.tpr == 32 && c.nv == 2) return launch_plain<T, 32, 2, AL>(a, c, stream);
+        if (c.tpr == 32) return launch_plain<T, 32, 4, AL>(a, c, stream);
+    }
+    return launch_plain<T, 0, NVC, AL>(a, c, stream);
 }
 
 template <typename T, bool AL> cudaError_t launch_al(const NormArgs &a, cudaStream_t stream) {
-    const Config c = config_of(a.cols, Storage<T>::kVec);
-    if (c.tpr == 8) return launch_one<T, 8, 1, AL>(a, c.threads, stream);
-    if (c.tpr == 32 && c.nv == 1) return launch_one<T, 32, 1, AL>(a, c.threads, stream);
-    if (c.tpr == 32 && c.nv == 2) return launch_one<T, 32, 2, AL>(a, c.threads, stream);
-    if (c.tpr == 32) return launch_one<T, 32, 4, AL>(a, c.threads, stream);
-    return launch_one<T, 0, 16 / Storage<T>::kVec, AL>(a, c.threads, stream);
+    const Config c = config_of(a.cols, Storage<T>::kVec, AL);
+    const cudaError_t e = launch_first<T, AL>(a, c, stream);
+    return e != cudaSuccess ? e : launch_grad_weight<T>(a, grid_of(a.rows, c), stream);
 }
 
 template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t stream) {
@@ -225,10 +511,10 @@ template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t strea
 }  // namespace
 
 int norm_backward_partial_rows(int64_t rows, int cols, DType dtype) {
-    const Config c = config_of(cols, dtype == DType::F32 ? 4 : 8);
-    const int teams = c.tpr ? c.threads / c.tpr : 1;
-    const int64_t need = (rows + teams - 1) / teams, most = (int64_t)kSms * c.per_sm;
-    return (int)(need < most ? need : most);
+    // whether the tensors are aligned is not known yet
+    const int vec = dtype == DType::F32 ? 4 : 8;
+    const int x = grid_of(rows, config_of(cols, vec, true)), y = grid_of(rows, config_of(cols, vec, false));
+    return x > y ? x : y;
 }
 
 cudaError_t launch_norm_backward(const NormArgs &a, cudaStream_t stream) {

@@ -14,6 +14,7 @@
 #include <cuda_fp8.h>
 
 #include "dcn_device.h"
+#include "dcn_host.h"
 #include "dcn_launch.h"
 #include "dcn_norm.cuh"
 
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
     for (long long r = blockIdx.x; r < a.rows; r += step) {
         const long long off = r * a.cols;
         if (!mbar_wait_bounded(smem_u32(bars + s), phase, kRowWaitNs)) {
-            atomicOr(err, kDevErrTmaTimeout);
+            give_up(smem_u32(bars), s, phase, slots, err);
             return;
         }
         const unsigned char *slot = ring + s * slot_bytes;
@@ -314,8 +315,9 @@ template <typename T> cudaError_t launch_wide(const NormArgs &a, const DeviceInf
     int slots = staged_budget(per_sm) / slot;
     if (slots > 4) slots = 4;
     const int smem = slots * slot;
-    cudaError_t e = cudaFuncSetAttribute(a.quant ? norm_forward_wide_kernel<T, true> : norm_forward_wide_kernel<T, false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<bool> plain_ok[kMaxDev], quant_ok[kMaxDev];
+    const cudaError_t e = a.quant ? allow_smem(norm_forward_wide_kernel<T, true>, staged_budget(1), quant_ok)
+                                  : allow_smem(norm_forward_wide_kernel<T, false>, staged_budget(1), plain_ok);
     if (e != cudaSuccess) return e;
     const long long most = (long long)dev->sms * per_sm;
     const unsigned grid = (unsigned)(a.rows < most ? a.rows : most);

@@ -3,9 +3,8 @@
 // routes (many rows: dcn_proj_adapters.cu, few rows: dcn_proj_adapters_rows.cu).
 #pragma once
 
-#include <atomic>
-
 #include "dcn_common.cuh"
+#include "dcn_host.h"
 #include "dcn_launch.h"
 
 namespace dcnb {
@@ -23,18 +22,6 @@ __device__ __forceinline__ int adapter_of(const int32_t *which, int s, int num_a
 
 __device__ __forceinline__ void report_bad_adapter(int a, int num_adapters, unsigned int *err) {
     if (a < -1 || a >= num_adapters) atomicOr(err, kDevErrBadAdapter);
-}
-
-// Lets `kern` use `bytes` of shared memory, once per device; `done` is the kernel's own array of flags.
-constexpr int kMaxDev = 64;
-template <typename K> cudaError_t allow_smem(K kern, int bytes, std::atomic<bool> (&done)[kMaxDev]) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < kMaxDev && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev >= 0 && dev < kMaxDev) done[dev].store(true, std::memory_order_release);
-    return e;
 }
 
 size_t adapters_small_workspace(const AdapterArgs &a);
