@@ -5,8 +5,10 @@
 // columns sit in 16 (16-bit storage) or 32 (fp32) neighbouring lanes.
 //
 // A team is 8 lanes, a warp, or the whole CTA (TPR = 0).  Rows whose byte
-// length or base address is not a multiple of 16 take the same mapping with
-// element-wise accesses (AL = false).
+// length or base address is not a multiple of 16 go by elements: thread t holds
+// the columns t, t + TPR, t + 2*TPR, ..., so a warp's accesses are 64 or 128
+// neighbouring bytes (the vector mapping with accesses by elements measured
+// three times slower: its warps touch 16 sectors an access).
 #pragma once
 
 #include "dcn_common.cuh"
@@ -72,30 +74,23 @@ __device__ __forceinline__ float2 f2_add(float2 a, float2 b) {
 }
 
 // The VEC columns starting at column c of a row, as raw storage (zeros past the end).
-template <typename T, bool AL> __device__ __forceinline__ uint4 load_cols(const T *row, int c, int cols) {
+template <typename T> __device__ __forceinline__ uint4 load_cols(const T *row, int c, int cols) {
     uint4 v = make_uint4(0, 0, 0, 0);
-    if constexpr (AL) {
-        if (c < cols) v = *reinterpret_cast<const uint4 *>(row + c);
-    } else {
-        constexpr int VEC = Storage<T>::kVec;
-        T t[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) t[i] = c + i < cols ? row[c + i] : from_f32<T>(0.0f);
-        v = *reinterpret_cast<uint4 *>(t);
-    }
+    if (c < cols) v = *reinterpret_cast<const uint4 *>(row + c);
     return v;
 }
 
-template <typename T, bool AL> __device__ __forceinline__ void store_cols(T *row, int c, int cols, const uint4 &v) {
-    if constexpr (AL) {
-        if (c < cols) *reinterpret_cast<uint4 *>(row + c) = v;
-    } else {
-        constexpr int VEC = Storage<T>::kVec;
-        const T *t = reinterpret_cast<const T *>(&v);
+template <typename T> __device__ __forceinline__ void store_cols(T *row, int c, int cols, const uint4 &v) {
+    if (c < cols) *reinterpret_cast<uint4 *>(row + c) = v;
+}
+
+// By elements: value k of a thread is column k * tpr + t.
+template <typename T, int C> __device__ __forceinline__ void load_elems(const T *row, int t, int tpr, int cols, float *f) {
+    T v[C];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if (c + i < cols) row[c + i] = t[i];
-    }
+    for (int k = 0; k < C; ++k) v[k] = k * tpr + t < cols ? row[k * tpr + t] : from_f32<T>(0.0f);
+#pragma unroll
+    for (int k = 0; k < C; ++k) f[k] = to_f32(v[k]);
 }
 
 // ---- rows staged in shared memory

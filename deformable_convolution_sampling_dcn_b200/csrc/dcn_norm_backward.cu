@@ -25,7 +25,7 @@ constexpr int kSms = 148;
 // warps through shared memory (`sums`, kSumBytes), halving their number each time; 8-lane teams of a warp first
 // among themselves.
 template <typename T, int NV, int WARPS> constexpr int kSumFloats = (WARPS / 2) * 32 * NV * Storage<T>::kVec;
-template <typename T, int TPR, int NV, int WARPS>
+template <typename T, int TPR, int NV, int WARPS, bool ELEMS = false>
 __device__ __forceinline__ void store_partial(const NormArgs &a, float2 (&gw)[NV][Storage<T>::kVec / 2], float *sums, int t,
                                               int tpr) {
     constexpr int VEC = Storage<T>::kVec;
@@ -71,93 +71,127 @@ __device__ __forceinline__ void store_partial(const NormArgs &a, float2 (&gw)[NV
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            const int c = (t + i * tpr) * VEC + j;
+            const int c = ELEMS ? (i * VEC + j) * tpr + t : (t + i * tpr) * VEC + j;
             if (c < a.cols) part[c] = j % 2 ? gw[i][j / 2].y : gw[i][j / 2].x;
         }
 }
 
-template <typename T, int TPR, int NV, bool AL>
-__global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 || NV * Storage<T>::kVec > 8 ? 1 : 2)
-    norm_backward_kernel(const NormArgs a) {
+template <typename T, int NV>
+__device__ __forceinline__ void load_weight(const NormArgs &a, int t, int tpr, float2 (&w)[NV][Storage<T>::kVec / 2],
+                                            float2 (&gw)[NV][Storage<T>::kVec / 2]) {
     constexpr int VEC = Storage<T>::kVec;
-    __shared__ __align__(16) float red[TPR == 0 ? 64 : kSumFloats<T, NV, kTeamThreads / 32>];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
-    const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
-    const int teams = TPR == 0 ? 1 : (int)blockDim.x / TPR;
-    const int team = TPR == 0 ? 0 : (int)threadIdx.x / TPR;
-    int turn = 0;
-    const T *hp = static_cast<const T *>(a.h), *gyp = static_cast<const T *>(a.grad_out);
-    const T *ghp = static_cast<const T *>(a.grad_residual_out), *weight = static_cast<const T *>(a.weight);
-    float2 w[NV][VEC / 2], gw[NV][VEC / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (weight) unpack16x2<T>(load_cols<T, AL>(weight, (t + i * tpr) * VEC, a.cols), w[i]);
+        if (a.weight)
+            unpack16x2<T>(load_cols<T>(static_cast<const T *>(a.weight), (t + i * tpr) * VEC, a.cols), w[i]);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
-            if (!weight) w[i][j] = make_float2(1.0f, 1.0f);
+            if (!a.weight) w[i][j] = make_float2(1.0f, 1.0f);
             gw[i][j] = make_float2(0.0f, 0.0f);
         }
     }
+}
+
+// The narrowest rows, 16-byte aligned: a vector each for 8 lanes.  The loads of a team's next row are in flight
+// while it works on the current one.
+template <typename T> __global__ void __launch_bounds__(kTeamThreads, 2) norm_backward_narrow_kernel(const NormArgs a) {
+    constexpr int VEC = Storage<T>::kVec, TPR = 8, TEAMS = kTeamThreads / TPR;
+    __shared__ __align__(16) float sums[kSumFloats<T, 1, kTeamThreads / 32>];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
+    const T *hp = static_cast<const T *>(a.h), *gyp = static_cast<const T *>(a.grad_out);
+    const T *ghp = static_cast<const T *>(a.grad_residual_out);
+    float2 w[1][VEC / 2], gw[1][VEC / 2];
+    load_weight<T, 1>(a, t, TPR, w, gw);
     const float inv_cols = 1.0f / (float)a.cols;
-    const long long step = (long long)gridDim.x * teams;
-    // the loads of a narrow team's next row are in flight while it works on the current one
-    constexpr bool AHEAD = NV * VEC <= 8 && TPR != 0;
-    uint4 hn[NV], gn[NV];
+    const long long step = (long long)gridDim.x * TEAMS;
+    uint4 hn, gn, rn;
     float sn = 0.0f;
     auto fetch = [&](long long r) {
-        const bool live = r < a.rows;
-        const long long off = live ? r * a.cols : 0;
-        const int cols = live ? a.cols : 0;
-        sn = live ? a.rstd[r] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            hn[i] = load_cols<T, AL>(hp + off, (t + i * tpr) * VEC, cols);
-            gn[i] = load_cols<T, AL>(gyp + off, (t + i * tpr) * VEC, cols);
-        }
+        const long long off = r < a.rows ? r * a.cols : 0;
+        const int cols = r < a.rows ? a.cols : 0;
+        sn = r < a.rows ? a.rstd[r] : 0.0f;
+        hn = load_cols<T>(hp + off, t * VEC, cols);
+        gn = load_cols<T>(gyp + off, t * VEC, cols);
+        if (ghp) rn = load_cols<T>(ghp + off, t * VEC, cols);
     };
-    if (AHEAD) fetch((long long)blockIdx.x * teams + team);
-    for (long long base = (long long)blockIdx.x * teams; base < a.rows; base += step) {
+    fetch((long long)blockIdx.x * TEAMS + team);
+    // every lane of a warp runs the same number of rounds: the shuffles need them all
+    for (long long base = (long long)blockIdx.x * TEAMS; base < a.rows; base += step) {
         const long long r = base + team;
-        const bool live = r < a.rows;
-        if (!AHEAD) fetch(r);
         const float rstd = sn;
-        float2 xh[NV][VEC / 2], gy[NV][VEC / 2], dot2 = make_float2(0.0f, 0.0f);
-        uint4 rv[NV];
+        float2 xh[VEC / 2], gy[VEC / 2], o[VEC / 2], dot2 = make_float2(0.0f, 0.0f);
+        unpack16x2<T>(hn, xh);
+        unpack16x2<T>(gn, gy);
+        if (ghp) unpack16x2<T>(rn, o);
+        fetch(r + step);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            unpack16x2<T>(hn[i], xh[i]);
-            unpack16x2<T>(gn[i], gy[i]);
-            // needed only behind the reduction, so not a row ahead
-            if (ghp) rv[i] = load_cols<T, AL>(ghp + (live ? r * a.cols : 0), (t + i * tpr) * VEC, live ? a.cols : 0);
+        for (int j = 0; j < VEC / 2; ++j) {
+            xh[j] = f2_mul(xh[j], make_float2(rstd, rstd));
+            const float2 p = f2_mul(gy[j], xh[j]);
+            gw[0][j] = f2_add(gw[0][j], p);
+            dot2 = f2_fma(p, w[0][j], dot2);
         }
-        if (AHEAD) fetch(r + step);
+        const float dot = -lanes_reduce<SumOp, TPR>(dot2.x + dot2.y) * inv_cols;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int j = 0; j < VEC / 2; ++j) {
+            const float2 d = f2_fma(xh[j], make_float2(dot, dot), f2_mul(gy[j], w[0][j]));
+            o[j] = ghp ? f2_fma(d, make_float2(rstd, rstd), o[j]) : f2_mul(d, make_float2(rstd, rstd));
+        }
+        if (r < a.rows)
+            store_cols<T>(static_cast<T *>(a.grad_x) + r * a.cols, t * VEC, a.cols,
+                          pack16<T>(reinterpret_cast<const float *>(o)));
+    }
+    if (!a.grad_weight) return;
+    store_partial<T, TPR, 1, kTeamThreads / 32>(a, gw, sums, t, TPR);
+}
+
+// Rows at any alignment, by elements: warp or CTA teams of NV * VEC columns a thread.  Also the widest aligned fp32
+// rows, of which two do not fit the shared memory.
+template <typename T, int TPR, int NV>
+__global__ void __launch_bounds__(TPR == 0 ? 1024 : 256, TPR == 0 ? 1 : 2) norm_backward_elems_kernel(const NormArgs a) {
+    constexpr int VEC = Storage<T>::kVec, C = NV * VEC, WARPS = 8;
+    __shared__ __align__(16) float sums[TPR == 0 ? 64 : kSumFloats<T, NV, WARPS>];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
+    const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % 32;
+    const int teams = TPR == 0 ? 1 : WARPS, team = TPR == 0 ? 0 : (int)threadIdx.x / 32;
+    int turn = 0;
+    float w[C];
+    float2 gw[NV][VEC / 2];
+    if (a.weight) load_elems<T, C>(static_cast<const T *>(a.weight), t, tpr, a.cols, w);
 #pragma unroll
-            for (int j = 0; j < VEC / 2; ++j) {
-                xh[i][j] = f2_mul(xh[i][j], make_float2(rstd, rstd));
-                const float2 p = f2_mul(gy[i][j], xh[i][j]);
-                gw[i][j] = f2_add(gw[i][j], p);
-                dot2 = f2_fma(p, w[i][j], dot2);
-            }
-        const float dot = -team_reduce<SumOp, TPR>(dot2.x + dot2.y, red, turn) * inv_cols;
+    for (int k = 0; k < C; ++k) {
+        if (!a.weight) w[k] = 1.0f;
+        if (k % 2 == 0) gw[k / VEC][k % VEC / 2] = make_float2(0.0f, 0.0f);
+    }
+    const float inv_cols = 1.0f / (float)a.cols;
+    const long long step = (long long)gridDim.x * teams;
+    for (long long r = (long long)blockIdx.x * teams + team; r < a.rows; r += step) {  // the same in the whole team
+        const long long off = r * a.cols;
+        const float rstd = a.rstd[r];
+        float xh[C], gy[C], o[C], dot = 0.0f;
+        load_elems<T, C>(static_cast<const T *>(a.h) + off, t, tpr, a.cols, xh);
+        load_elems<T, C>(static_cast<const T *>(a.grad_out) + off, t, tpr, a.cols, gy);
+        if (a.grad_residual_out) load_elems<T, C>(static_cast<const T *>(a.grad_residual_out) + off, t, tpr, a.cols, o);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float2 o[VEC / 2];
-            if (ghp) unpack16x2<T>(rv[i], o);
+        for (int k = 0; k < C; ++k) {
+            xh[k] *= rstd;
+            const float p = gy[k] * xh[k];
+            if (k % 2) gw[k / VEC][k % VEC / 2].y += p;
+            else gw[k / VEC][k % VEC / 2].x += p;
+            dot = fmaf(p, w[k], dot);
+        }
+        dot = -team_reduce<SumOp, TPR>(dot, sums, turn) * inv_cols;
 #pragma unroll
-            for (int j = 0; j < VEC / 2; ++j) {
-                // rstd * (g - xh * mean(g * xh)) + grad_residual_out
-                const float2 d = f2_fma(xh[i][j], make_float2(dot, dot), f2_mul(gy[i][j], w[i][j]));
-                o[j] = ghp ? f2_fma(d, make_float2(rstd, rstd), o[j]) : f2_mul(d, make_float2(rstd, rstd));
-            }
-            store_cols<T, AL>(static_cast<T *>(a.grad_x) + (live ? r * a.cols : 0), (t + i * tpr) * VEC,
-                              live ? a.cols : 0, pack16<T>(reinterpret_cast<const float *>(o)));
+        for (int k = 0; k < C; ++k) {
+            const float d = fmaf(xh[k], dot, gy[k] * w[k]);
+            const float gx = a.grad_residual_out ? fmaf(d, rstd, o[k]) : d * rstd;
+            if (k * tpr + t < a.cols) static_cast<T *>(a.grad_x)[off + k * tpr + t] = from_f32<T>(gx);
         }
     }
     if (!a.grad_weight) return;
-    store_partial<T, TPR, NV, kTeamThreads / 32>(a, gw, red, t, tpr);
+    store_partial<T, TPR, NV, WARPS, true>(a, gw, sums, t, tpr);
 }
 
 // A row's products from its staged tensors: xh and grad_out in registers, the weight gradient, and this thread's part
@@ -172,8 +206,8 @@ __device__ __forceinline__ float staged_row(const unsigned char *h, const unsign
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * tpr) * VEC;
-        unpack16x2<T>(load_cols<T, true>(reinterpret_cast<const T *>(h), c, cols), xh[i]);
-        unpack16x2<T>(load_cols<T, true>(reinterpret_cast<const T *>(g), c, cols), gy[i]);
+        unpack16x2<T>(load_cols<T>(reinterpret_cast<const T *>(h), c, cols), xh[i]);
+        unpack16x2<T>(load_cols<T>(reinterpret_cast<const T *>(g), c, cols), gy[i]);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
             xh[i][j] = f2_mul(xh[i][j], make_float2(rstd, rstd));
@@ -196,29 +230,13 @@ __device__ __forceinline__ void staged_output(T *out, const unsigned char *r, in
     for (int i = 0; i < NV; ++i) {
         const int c = (t + i * tpr) * VEC;
         float2 o[VEC / 2];
-        if (r) unpack16x2<T>(load_cols<T, true>(reinterpret_cast<const T *>(r), c, cols), o);
+        if (r) unpack16x2<T>(load_cols<T>(reinterpret_cast<const T *>(r), c, cols), o);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
             const float2 d = f2_fma(xh[i][j], make_float2(-mean, -mean), f2_mul(gy[i][j], w[i][j]));
             o[j] = r ? f2_fma(d, make_float2(rstd, rstd), o[j]) : f2_mul(d, make_float2(rstd, rstd));
         }
-        store_cols<T, true>(out, c, cols, pack16<T>(reinterpret_cast<const float *>(o)));
-    }
-}
-
-template <typename T, int NV>
-__device__ __forceinline__ void load_weight(const NormArgs &a, int t, int tpr, float2 (&w)[NV][Storage<T>::kVec / 2],
-                                            float2 (&gw)[NV][Storage<T>::kVec / 2]) {
-    constexpr int VEC = Storage<T>::kVec;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (a.weight)
-            unpack16x2<T>(load_cols<T, true>(static_cast<const T *>(a.weight), (t + i * tpr) * VEC, a.cols), w[i]);
-#pragma unroll
-        for (int j = 0; j < VEC / 2; ++j) {
-            if (!a.weight) w[i][j] = make_float2(1.0f, 1.0f);
-            gw[i][j] = make_float2(0.0f, 0.0f);
-        }
+        store_cols<T>(out, c, cols, pack16<T>(reinterpret_cast<const float *>(o)));
     }
 }
 
@@ -392,32 +410,33 @@ __global__ void __launch_bounds__(kRedX *Y) norm_grad_weight_kernel(const float 
     }
 }
 
-// How a row is worked on: teams of 8 lanes, a warp or a CTA (tpr = 0), nv vectors a thread, `rows` of them in a
-// CTA at a time, `per_sm` CTAs on an SM; staged through shared memory or not.
+// How rows are worked on: `threads` of a CTA, `rows` at a time, `per_sm` CTAs on an SM.
+enum Route { kNarrow, kTiles, kWide, kElems };
 struct Config {
-    int tpr, nv, threads, rows, per_sm;
-    bool staged;
+    Route route;
+    int nv, threads, rows, per_sm;  // nv vectors (kElems: groups of VEC columns) a thread
 };
 Config config_of(int cols, int vec, bool aligned) {
     const int nvec = (cols + vec - 1) / vec, nv16 = 16 / vec;
-    if (nvec <= 8) return {8, 1, kTeamThreads, kTeamThreads / 8, 2, false};
-    if (nvec <= 128) {
+    const int wide = ((cols + 15) / 16 + 31) / 32 * 32;  // threads of a CTA for a row, 16 columns each
+    if (aligned && nvec <= 8) return {kNarrow, 1, kTeamThreads, kTeamThreads / 8, 2};
+    if (aligned && nvec <= 128) {
+        // columns a thread -> registers -> warps: 72 registers for two CTAs of 13 warps, 112 for one of 17
         const int nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, c = nv * vec;
-        if (!aligned) return {32, nv, kTeamThreads, kTeamThreads / 32, c <= 8 ? 2 : 1, false};
-        // columns a thread -> registers -> consumer warps: 72 registers for two CTAs of 13 warps, 112 for one of 17
-        if (c <= 8) return {32, nv, 13 * 32, 12, 2, true};
-        if (c <= 16) return {32, nv, 17 * 32, 16, 1, true};
-        return {32, nv, 13 * 32, 12, 1, true};
+        if (c <= 8) return {kTiles, nv, 13 * 32, 12, 2};
+        if (c <= 16) return {kTiles, nv, 17 * 32, 16, 1};
+        return {kTiles, nv, 13 * 32, 12, 1};
     }
-    const int threads = ((nvec + nv16 - 1) / nv16 + 31) / 32 * 32;  // at most 1024: cols <= 16384
-    if (!aligned || cols > 8192) {
-        const int fit = 1024 / threads;
-        return {0, nv16, threads, 1, fit < 8 ? fit : 8, false};
+    if (aligned && cols <= 8192) {
+        int per_sm = 512 / wide < 4 ? 512 / wide : 4;
+        // fewer CTAs where two staged rows of three tensors would not fit their share of the shared memory
+        while (per_sm > 1 && 2 * 3 * cols * (16 / vec) > staged_budget(per_sm)) --per_sm;
+        return {kWide, nv16, wide, 1, per_sm};
     }
-    int per_sm = 512 / threads < 4 ? 512 / threads : 4;
-    // fewer CTAs where two staged rows of three tensors would not fit their share of the shared memory
-    while (per_sm > 1 && 2 * 3 * cols * (16 / vec) > staged_budget(per_sm)) --per_sm;
-    return {0, nv16, threads, 1, per_sm, true};
+    if (cols <= 32 * vec) return {kElems, 1, 256, 8, 2};
+    if (cols <= 512) return {kElems, nv16, 256, 8, 2};
+    const int c = cols <= 8192 ? 8 : 16, threads = ((cols + c - 1) / c + 31) / 32 * 32;  // at most 1024
+    return {kElems, c / vec, threads, 1, 1024 / threads < 8 ? 1024 / threads : 8};
 }
 
 int grid_of(int64_t rows, const Config &c) {
@@ -441,9 +460,8 @@ template <typename T> cudaError_t launch_grad_weight(const NormArgs &a, int n, c
                               (const float *)a.partial, n, a.cols, static_cast<T *>(a.grad_weight));
 }
 
-template <typename T, int TPR, int NV, bool AL>
-cudaError_t launch_plain(const NormArgs &a, const Config &c, cudaStream_t stream) {
-    norm_backward_kernel<T, TPR, NV, AL><<<grid_of(a.rows, c), c.threads, 0, stream>>>(a);
+template <typename K> cudaError_t launch_plain(K kern, const NormArgs &a, const Config &c, cudaStream_t stream) {
+    kern<<<grid_of(a.rows, c), c.threads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -467,45 +485,43 @@ cudaError_t launch_tiles(const NormArgs &a, const Config &c, const DeviceInfo *d
                          (int)sizeof(T), ok, dev, stream);
 }
 
-template <typename T, bool AL> cudaError_t launch_first(const NormArgs &a, const Config &c, cudaStream_t stream) {
+template <typename T> cudaError_t launch_rows(const NormArgs &a, const Config &c, cudaStream_t stream) {
     constexpr int VEC = Storage<T>::kVec, NVC = 16 / VEC;
-    if (c.tpr == 8) return launch_plain<T, 8, 1, AL>(a, c, stream);
-    if constexpr (AL) {
-        const DeviceInfo *dev = device_info();
-        if (!dev) return cudaErrorNotSupported;
-        if (c.tpr == 32 && c.nv == 1) return launch_tiles<T, 1, 12, 2>(a, c, dev, stream);
-        if (c.tpr == 32 && c.nv == 2) {
-            if constexpr (VEC == 4) return launch_tiles<T, 2, 12, 2>(a, c, dev, stream);
-            else return launch_tiles<T, 2, 16, 1>(a, c, dev, stream);
-        }
-        if (c.tpr == 32) {
-            if constexpr (VEC == 4) return launch_tiles<T, 4, 16, 1>(a, c, dev, stream);
-            else return launch_tiles<T, 4, 12, 1>(a, c, dev, stream);
-        }
-        if (c.staged) {
+    const DeviceInfo *dev = device_info();
+    if (!dev) return cudaErrorNotSupported;
+    switch (c.route) {
+        case kNarrow: return launch_plain(norm_backward_narrow_kernel<T>, a, c, stream);
+        case kTiles:
+            if (c.nv == 1) return launch_tiles<T, 1, 12, 2>(a, c, dev, stream);
+            if constexpr (VEC == 4) {
+                if (c.nv == 2) return launch_tiles<T, 2, 12, 2>(a, c, dev, stream);
+                return launch_tiles<T, 4, 16, 1>(a, c, dev, stream);
+            } else {
+                if (c.nv == 2) return launch_tiles<T, 2, 16, 1>(a, c, dev, stream);
+                return launch_tiles<T, 4, 12, 1>(a, c, dev, stream);
+            }
+        case kWide: {
             static std::atomic<bool> ok[kMaxDev];
             return launch_staged(norm_backward_wide_kernel<T>, a, c, staged_budget(c.per_sm), (int)sizeof(T), ok, dev,
                                  stream);
         }
-    } else {
-        if (c.tpr == 32 && c.nv == 1) return launch_plain<T, 32, 1, AL>(a, c, stream);
-        if (c.tpr == 32 && c.nv == 2) return launch_plain<T, 32, 2, AL>(a, c, stream);
-        if (c.tpr == 32) return launch_plain<T, 32, 4, AL>(a, c, stream);
+        case kElems:
+            if (c.rows > 1)
+                return c.nv == 1 ? launch_plain(norm_backward_elems_kernel<T, 32, 1>, a, c, stream)
+                                 : launch_plain(norm_backward_elems_kernel<T, 32, NVC>, a, c, stream);
+            return c.nv == NVC ? launch_plain(norm_backward_elems_kernel<T, 0, NVC>, a, c, stream)
+                               : launch_plain(norm_backward_elems_kernel<T, 0, NVC / 2>, a, c, stream);
     }
-    return launch_plain<T, 0, NVC, AL>(a, c, stream);
-}
-
-template <typename T, bool AL> cudaError_t launch_al(const NormArgs &a, cudaStream_t stream) {
-    const Config c = config_of(a.cols, Storage<T>::kVec, AL);
-    const cudaError_t e = launch_first<T, AL>(a, c, stream);
-    return e != cudaSuccess ? e : launch_grad_weight<T>(a, grid_of(a.rows, c), stream);
+    return cudaErrorInvalidValue;
 }
 
 template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t stream) {
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.h) | reinterpret_cast<uintptr_t>(a.grad_out) |
                            reinterpret_cast<uintptr_t>(a.grad_residual_out) | reinterpret_cast<uintptr_t>(a.weight) |
                            reinterpret_cast<uintptr_t>(a.grad_x) | (uintptr_t)((size_t)a.cols * sizeof(T));
-    return bits % 16 == 0 ? launch_al<T, true>(a, stream) : launch_al<T, false>(a, stream);
+    const Config c = config_of(a.cols, Storage<T>::kVec, bits % 16 == 0);
+    const cudaError_t e = launch_rows<T>(a, c, stream);
+    return e != cudaSuccess ? e : launch_grad_weight<T>(a, grid_of(a.rows, c), stream);
 }
 
 }  // namespace

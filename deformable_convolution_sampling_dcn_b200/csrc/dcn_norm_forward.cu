@@ -51,31 +51,26 @@ __device__ __forceinline__ void store_codes(unsigned char *dst, const float *y, 
 
 constexpr int kMaxSlots = 8;
 
-// A thread holds C = NV * VEC columns of a row: up to 16 with the loads of its
-// team's next row in flight meanwhile, or 32 without.  8-lane and warp teams
-// share a CTA of 256 threads, a CTA team has up to 512; CTAs on an SM follow
-// from the registers that leaves (48, 80 or 128).
+// 8-lane and warp teams in CTAs of 256 threads.  A thread holds C = NV * VEC
+// columns of a row: up to 16 with the loads of its team's next row in flight
+// meanwhile, or 32 without; CTAs on an SM follow from the registers that leaves
+// (64, 80 or 128).
 constexpr int kTeamThreads = 256;
-template <int TPR> constexpr int max_threads() { return TPR == 0 ? 512 : kTeamThreads; }
-constexpr int threads_per_sm(int c) { return c <= 8 ? 1280 : c <= 16 ? 768 : 512; }
+constexpr int ctas_per_sm(int c) { return c <= 8 ? 4 : c <= 16 ? 3 : 2; }
 
-template <typename T, int TPR, int NV, bool AL, bool QUANT>
-__global__ void __launch_bounds__(max_threads<TPR>(), threads_per_sm(NV * Storage<T>::kVec) / max_threads<TPR>())
+template <typename T, int TPR, int NV, bool QUANT>
+__global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVec))
     norm_forward_kernel(const NormArgs a) {
     constexpr int VEC = Storage<T>::kVec;
     constexpr bool AHEAD = NV * VEC <= 16;
-    __shared__ float red[64];
-    const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
-    const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
-    const int teams = TPR == 0 ? 1 : (int)blockDim.x / TPR;
-    const int team = TPR == 0 ? 0 : (int)threadIdx.x / TPR;
-    int turn = 0;
+    constexpr int tpr = TPR, teams = kTeamThreads / TPR;
+    const int t = (int)threadIdx.x % TPR, team = (int)threadIdx.x / TPR;
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
     const T *weight = static_cast<const T *>(a.weight);
     uint4 w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (weight) w[i] = load_cols<T, AL>(weight, (t + i * tpr) * VEC, a.cols);
+        if (weight) w[i] = load_cols<T>(weight, (t + i * tpr) * VEC, a.cols);
 
     uint4 xn[NV], rn[NV];
     auto fetch = [&](long long r) {
@@ -83,8 +78,8 @@ __global__ void __launch_bounds__(max_threads<TPR>(), threads_per_sm(NV * Storag
         const int cols = r < a.rows ? a.cols : 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            xn[i] = load_cols<T, AL>(x + off, (t + i * tpr) * VEC, cols);
-            if (res) rn[i] = load_cols<T, AL>(res + off, (t + i * tpr) * VEC, cols);
+            xn[i] = load_cols<T>(x + off, (t + i * tpr) * VEC, cols);
+            if (res) rn[i] = load_cols<T>(res + off, (t + i * tpr) * VEC, cols);
         }
     };
     const long long step = (long long)gridDim.x * teams;
@@ -107,14 +102,14 @@ __global__ void __launch_bounds__(max_threads<TPR>(), threads_per_sm(NV * Storag
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) y[i][j] += g[j];
                 const uint4 h = pack16<T>(y[i]);
-                store_cols<T, AL>(static_cast<T *>(a.residual_out) + off, (t + i * tpr) * VEC, cols, h);
+                store_cols<T>(static_cast<T *>(a.residual_out) + off, (t + i * tpr) * VEC, cols, h);
                 unpack16<T>(h, y[i]);
             }
 #pragma unroll
             for (int j = 0; j < VEC; ++j) ss = fmaf(y[i][j], y[i][j], ss);
         }
         if (AHEAD) fetch(r + step);
-        ss = team_reduce<SumOp, TPR>(ss, red, turn);
+        ss = lanes_reduce<SumOp, TPR>(ss);
         const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
         if (a.rstd && t == 0 && live) a.rstd[r] = rstd;
 #pragma unroll
@@ -129,7 +124,7 @@ __global__ void __launch_bounds__(max_threads<TPR>(), threads_per_sm(NV * Storag
                 for (int j = 0; j < VEC; ++j) y[i][j] *= rstd;
             }
             if (!QUANT || a.out)
-                store_cols<T, AL>(static_cast<T *>(a.out) + off, (t + i * tpr) * VEC, cols, pack16<T>(y[i]));
+                store_cols<T>(static_cast<T *>(a.out) + off, (t + i * tpr) * VEC, cols, pack16<T>(y[i]));
         }
         if constexpr (QUANT) {
             float amax = 0.0f, gmax[NV];
@@ -139,18 +134,17 @@ __global__ void __launch_bounds__(max_threads<TPR>(), threads_per_sm(NV * Storag
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     // columns past the row hold 0 * rstd * 0, which is NaN where rstd is
-                    const bool in = (t + i * tpr) * VEC + (AL ? 0 : j) < cols;
-                    gmax[i] = max_nan(gmax[i], in ? fabsf(y[i][j]) : 0.0f);
+                    gmax[i] = max_nan(gmax[i], (t + i * tpr) * VEC < cols ? fabsf(y[i][j]) : 0.0f);
                 }
                 amax = max_nan(amax, gmax[i]);
             }
             const float top = a.quant == kQuantE4M3 ? 448.0f : 127.0f;
             // lanes that share 128 columns; a team narrower than that holds rows of at most 128 columns
             constexpr int GL = 128 / VEC;
-            const bool grouped = a.group != 0 && (TPR == 0 || TPR >= GL);
+            const bool grouped = a.group != 0 && TPR >= GL;
             float s = 0.0f, inv = 0.0f;
             if (!grouped) {
-                s = max_nan(team_reduce<MaxOp, TPR>(amax, red, turn) / top, kScaleMin);
+                s = max_nan(lanes_reduce<MaxOp, TPR>(amax) / top, kScaleMin);
                 inv = 1.0f / s;
                 if (t == 0 && live) a.scale[r] = s;
             }
@@ -163,17 +157,7 @@ __global__ void __launch_bounds__(max_threads<TPR>(), threads_per_sm(NV * Storag
                     if (v % GL == 0 && c < cols) a.scale[r * a.groups + c / 128] = s;
                 }
                 if (c < cols) {
-                    unsigned char *dst = static_cast<unsigned char *>(a.out8) + off + c;
-                    if constexpr (AL) {
-                        store_codes<VEC>(dst, y[i], inv, a.quant);
-                    } else {
-                        uint32_t q[VEC / 4];
-#pragma unroll
-                        for (int j = 0; j < VEC / 4; ++j) q[j] = pack8(y[i] + 4 * j, inv, a.quant);
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j)
-                            if (c + j < cols) dst[j] = (unsigned char)(q[j / 4] >> (8 * (j % 4)));
-                    }
+                    store_codes<VEC>(static_cast<unsigned char *>(a.out8) + off + c, y[i], inv, a.quant);
                 }
             }
         }
@@ -211,7 +195,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
     uint4 w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (weight) w[i] = load_cols<T, true>(weight, (t + i * tpr) * VEC, a.cols);
+        if (weight) w[i] = load_cols<T>(weight, (t + i * tpr) * VEC, a.cols);
 
     int s = 0;
     uint32_t phase = 0;
@@ -227,14 +211,14 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (t + i * tpr) * VEC;
-            unpack16<T>(load_cols<T, true>(reinterpret_cast<const T *>(slot), c, a.cols), y[i]);
+            unpack16<T>(load_cols<T>(reinterpret_cast<const T *>(slot), c, a.cols), y[i]);
             if (a.residual) {
                 float g[VEC];
-                unpack16<T>(load_cols<T, true>(reinterpret_cast<const T *>(slot + row_bytes), c, a.cols), g);
+                unpack16<T>(load_cols<T>(reinterpret_cast<const T *>(slot + row_bytes), c, a.cols), g);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) y[i][j] += g[j];
                 const uint4 h = pack16<T>(y[i]);
-                store_cols<T, true>(static_cast<T *>(a.residual_out) + off, c, a.cols, h);
+                store_cols<T>(static_cast<T *>(a.residual_out) + off, c, a.cols, h);
                 unpack16<T>(h, y[i]);
             }
 #pragma unroll
@@ -261,7 +245,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) y[i][j] *= rstd;
             }
-            if (!QUANT || a.out) store_cols<T, true>(static_cast<T *>(a.out) + off, c, a.cols, pack16<T>(y[i]));
+            if (!QUANT || a.out) store_cols<T>(static_cast<T *>(a.out) + off, c, a.cols, pack16<T>(y[i]));
             if (QUANT) {
                 gmax[i] = 0.0f;
                 if (c < a.cols) {
@@ -293,15 +277,125 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
     }
 }
 
-template <typename T, int TPR, int NV, bool AL>
-cudaError_t launch_one(const NormArgs &a, int threads, const DeviceInfo *dev, cudaStream_t stream) {
-    constexpr int VEC = Storage<T>::kVec;
-    const int teams = TPR == 0 ? 1 : threads / TPR;
+// Rows at any alignment, by elements; warp or CTA teams of C columns a thread.
+template <typename T, int TPR, int C, bool QUANT>
+__global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 ? 1 : ctas_per_sm(C))
+    norm_forward_elems_kernel(const NormArgs a) {
+    __shared__ float red[64];
+    // maxima of the groups (bits of values >= 0, two rows' sets) and the factors that follow from them
+    __shared__ int gmax_s[2][TPR == 0 && QUANT ? 128 : 1];
+    __shared__ float inv_s[TPR == 0 && QUANT ? 128 : 1];
+    const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
+    const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % 32;
+    const int teams = TPR == 0 ? 1 : kTeamThreads / 32, team = TPR == 0 ? 0 : (int)threadIdx.x / 32;
+    int turn = 0, set = 0;
+    float w[C];
+    if (a.weight) load_elems<T, C>(static_cast<const T *>(a.weight), t, tpr, a.cols, w);
+    if (TPR == 0 && QUANT) {
+        for (int i = t; i < 256; i += tpr) gmax_s[i / 128][i % 128] = 0;
+        __syncthreads();
+    }
+    const long long step = (long long)gridDim.x * teams;
+    for (long long r = (long long)blockIdx.x * teams + team; r < a.rows; r += step) {  // the same in the whole team
+        const long long off = r * a.cols;
+        float y[C], ss = 0.0f;
+        load_elems<T, C>(static_cast<const T *>(a.x) + off, t, tpr, a.cols, y);
+        if (a.residual) {
+            float g[C];
+            load_elems<T, C>(static_cast<const T *>(a.residual) + off, t, tpr, a.cols, g);
+            T *dst = static_cast<T *>(a.residual_out) + off;
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                const T h = from_f32<T>(y[k] + g[k]);
+                if (k * tpr + t < a.cols) dst[k * tpr + t] = h;
+                y[k] = to_f32(h);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < C; ++k) ss = fmaf(y[k], y[k], ss);
+        ss = team_reduce<SumOp, TPR>(ss, red, turn);
+        const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+        if (a.rstd && t == 0) a.rstd[r] = rstd;
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            y[k] *= rstd;
+            if (a.weight) y[k] *= w[k];
+            const bool in = k * tpr + t < a.cols;
+            if (in && (!QUANT || a.out)) static_cast<T *>(a.out)[off + k * tpr + t] = from_f32<T>(y[k]);
+            if (QUANT) {
+                if (!in) y[k] = 0.0f;
+                amax = max_nan(amax, fabsf(y[k]));
+            }
+        }
+        if constexpr (QUANT) {
+            const float top = a.quant == kQuantE4M3 ? 448.0f : 127.0f;
+            float s = 0.0f, inv = 0.0f;
+            if (!a.group) {
+                s = max_nan(team_reduce<MaxOp, TPR>(amax, red, turn) / top, kScaleMin);
+                inv = 1.0f / s;
+                if (t == 0) a.scale[r] = s;
+            } else if (TPR == 0) {
+                // 32 columns of a warp lie in one group
+#pragma unroll
+                for (int k = 0; k < C; ++k) {
+                    const float m = lanes_reduce<MaxOp, 32>(fabsf(y[k]));
+                    const int c = k * tpr + t - t % 32;
+                    if (t % 32 == 0 && c < a.cols) atomicMax(&gmax_s[set][c / 128], __float_as_int(m));
+                }
+                __syncthreads();
+                for (int i = t; i < a.groups; i += tpr) {
+                    s = max_nan(__int_as_float(gmax_s[set][i]) / top, kScaleMin);
+                    inv_s[i] = 1.0f / s;
+                    a.scale[r * a.groups + i] = s;
+                    gmax_s[set ^ 1][i] = 0;  // the next row's, last read two barriers ago
+                }
+                __syncthreads();
+                set ^= 1;
+            }
+            unsigned char *dst = static_cast<unsigned char *>(a.out8) + off;
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                const int c = k * tpr + t;
+                if (a.group && TPR == 0) {
+                    inv = inv_s[c < a.cols ? c / 128 : 0];
+                } else if (a.group && k % 4 == 0) {
+                    // a warp's values k .. k + 3 are 128 columns
+                    float m = fabsf(y[k]);
+#pragma unroll
+                    for (int q = 1; q < 4; ++q)
+                        if (k + q < C) m = max_nan(m, fabsf(y[k + q]));
+                    s = max_nan(lanes_reduce<MaxOp, 32>(m) / top, kScaleMin);
+                    inv = 1.0f / s;
+                    if (t == 0 && c < a.cols) a.scale[r * a.groups + k / 4] = s;
+                }
+                if (c < a.cols) {
+                    const float q4[4] = {y[k], 0.0f, 0.0f, 0.0f};
+                    dst[c] = (unsigned char)pack8(q4, inv, a.quant);
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int TPR, int C>
+cudaError_t launch_elems(const NormArgs &a, int threads, const DeviceInfo *dev, cudaStream_t stream) {
+    const int teams = TPR == 0 ? 1 : threads / 32;
     const long long need = (a.rows + teams - 1) / teams;
-    const long long most = (long long)dev->sms * (threads_per_sm(NV * VEC) / threads);
+    const long long most = (long long)dev->sms * (TPR == 0 ? 1024 / threads : ctas_per_sm(C));
     const unsigned grid = (unsigned)(need < most ? need : most);
-    if (a.quant) norm_forward_kernel<T, TPR, NV, AL, true><<<grid, threads, 0, stream>>>(a);
-    else norm_forward_kernel<T, TPR, NV, AL, false><<<grid, threads, 0, stream>>>(a);
+    if (a.quant) norm_forward_elems_kernel<T, TPR, C, true><<<grid, threads, 0, stream>>>(a);
+    else norm_forward_elems_kernel<T, TPR, C, false><<<grid, threads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int TPR, int NV>
+cudaError_t launch_one(const NormArgs &a, const DeviceInfo *dev, cudaStream_t stream) {
+    constexpr int teams = kTeamThreads / TPR;
+    const long long need = (a.rows + teams - 1) / teams, most = (long long)dev->sms * ctas_per_sm(NV * Storage<T>::kVec);
+    const unsigned grid = (unsigned)(need < most ? need : most);
+    if (a.quant) norm_forward_kernel<T, TPR, NV, true><<<grid, kTeamThreads, 0, stream>>>(a);
+    else norm_forward_kernel<T, TPR, NV, false><<<grid, kTeamThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -326,31 +420,24 @@ template <typename T> cudaError_t launch_wide(const NormArgs &a, const DeviceInf
     return cudaGetLastError();
 }
 
-template <typename T, bool AL> cudaError_t launch_al(const NormArgs &a, cudaStream_t stream) {
+template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t stream) {
     const DeviceInfo *dev = device_info();
     if (!dev) return cudaErrorNotSupported;
-    constexpr int VEC = Storage<T>::kVec;
-    const int nvec = (a.cols + VEC - 1) / VEC;
-    if (nvec <= 8) return launch_one<T, 8, 1, AL>(a, kTeamThreads, dev, stream);
-    if (nvec <= 32) return launch_one<T, 32, 1, AL>(a, kTeamThreads, dev, stream);
-    if (nvec <= 64) return launch_one<T, 32, 2, AL>(a, kTeamThreads, dev, stream);
-    if (nvec <= 128) return launch_one<T, 32, 4, AL>(a, kTeamThreads, dev, stream);
-    if constexpr (AL) {
-        return launch_wide<T>(a, dev, stream);
-    } else {
-        // at most 512 threads: 16 columns each up to 8192, 32 up to 16384
-        const int nv = (a.cols <= 8192 ? 16 : 32) / VEC, threads = ((nvec + nv - 1) / nv + 31) / 32 * 32;
-        if (nv == 16 / VEC) return launch_one<T, 0, 16 / VEC, AL>(a, threads, dev, stream);
-        return launch_one<T, 0, 32 / VEC, AL>(a, threads, dev, stream);
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
+                           reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.residual_out) |
+                           reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.out8) |
+                           (uintptr_t)((size_t)a.cols * sizeof(T));
+    if (bits % 16) {
+        if (a.cols <= 128) return launch_elems<T, 32, 4>(a, kTeamThreads, dev, stream);
+        if (a.cols <= 512) return launch_elems<T, 32, 16>(a, kTeamThreads, dev, stream);
+        return launch_elems<T, 0, 16>(a, ((a.cols + 15) / 16 + 31) / 32 * 32, dev, stream);  // at most 1024 threads
     }
-}
-
-template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t stream) {
-    uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
-                     reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.residual_out) |
-                     reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.out8) |
-                     (uintptr_t)((size_t)a.cols * sizeof(T));
-    return bits % 16 == 0 ? launch_al<T, true>(a, stream) : launch_al<T, false>(a, stream);
+    const int nvec = a.cols / Storage<T>::kVec;
+    if (nvec <= 8) return launch_one<T, 8, 1>(a, dev, stream);
+    if (nvec <= 32) return launch_one<T, 32, 1>(a, dev, stream);
+    if (nvec <= 64) return launch_one<T, 32, 2>(a, dev, stream);
+    if (nvec <= 128) return launch_one<T, 32, 4>(a, dev, stream);
+    return launch_wide<T>(a, dev, stream);
 }
 
 }  // namespace

@@ -148,21 +148,38 @@ def test_large_values_and_tiny_values(cuda_dev):
     assert ((o.out.double().cpu() - y).abs() <= y.abs() * (32 * U + half_step(torch.float16)) + tiny(torch.float16)).all()
 
 
-def test_unaligned_views_match_aligned(cuda_dev):
-    """Tensors that start off 16-byte boundaries take element-wise accesses and give the same numbers."""
-    for dtype, quant in (("bf16", None), ("f32", "e4m3"), ("f16", "int8")):
-        x, r, w = inputs(11, 264, DT[dtype], 21)
+def off(t):
+    """The tensor at an address that is a multiple of its element only."""
+    return torch.empty(t.numel() + 3, dtype=t.dtype, device="cuda")[1:1 + t.numel()].view(t.shape).copy_(t)
 
-        def off(t):
-            b = torch.empty(t.numel() + 3, dtype=t.dtype, device="cuda")[1:1 + t.numel()].view(t.shape)
-            return b.copy_(t)
 
-        a = d.dcn_add_rms_norm_forward(*gpu(x, r, w), eps=EPS, quant=quant)
-        b = d.dcn_add_rms_norm_forward(off(x), off(r), off(w), eps=EPS, quant=quant)
-        for p, q in zip(a, b):
-            assert (p is None) == (q is None)
-            if p is not None:
-                assert torch.equal(p.float(), q.float())
+@pytest.mark.parametrize("cols", [8, 120, 264, 512, 1032, 8192, 8200])
+def test_unaligned_views(cols, cuda_dev):
+    """Tensors that start off 16-byte boundaries, at widths that are aligned otherwise: the accesses go by
+    elements and the order of the sums is another one, within the same tolerances."""
+    for dtype, quant, group in (("bf16", None, 0), ("f32", "e4m3", 0), ("f16", "int8", 128), ("bf16", "e4m3", 128)):
+        x, r, w = inputs(11, cols, DT[dtype], 21)
+        o = d.dcn_add_rms_norm_forward(off(x), off(r), off(w), eps=EPS, quant=quant, group=group, keep_out=True)
+        h, y, _ = definition(x, r, w)
+        assert torch.equal(o.residual_out.cpu(), h)
+        err = (o.out.double().cpu() - y).abs()
+        assert (err <= y.abs() * (32 * U + half_step(DT[dtype])) + tiny(DT[dtype])).all()
+        if quant:
+            check_quant(o, y, quant, group)
+        check_backward(11, cols, dtype, 22, place=off)
+
+
+def test_outputs_end_with_the_row(cuda_dev):
+    """Unaligned outputs inside larger buffers: nothing around them is written."""
+    for rows, cols in ((5, 13), (3, 300), (2, 1001)):
+        x, r, w = gpu(*inputs(rows, cols, torch.bfloat16, 23))
+        bufs = [torch.full((rows * cols + 9,), 5, dtype=dt, device="cuda")
+                for dt in (torch.bfloat16, torch.bfloat16, torch.int8)]
+        views = [b[3:3 + rows * cols].view(rows, cols) for b in bufs]
+        d.dcn_add_rms_norm_forward(x, r, w, out=views[0], residual_out=views[1], out8=views[2], quant="int8")
+        d.dcn_add_rms_norm_backward(x, r, torch.ones(rows, device="cuda"), w, grad_x=views[0])
+        for b in bufs:
+            assert (b[:3] == 5).all() and (b[3 + rows * cols:] == 5).all()
 
 
 def test_in_place_and_given_buffers(cuda_dev):
@@ -219,12 +236,13 @@ def rows_in_a_chain(rows):
     return -(-rows // 148) + 64 + 2 + 16 + 10 + 7 + 4
 
 
-def check_backward(rows, cols, dtype, seed, weight=True, residual=True):
+def check_backward(rows, cols, dtype, seed, weight=True, residual=True, place=torch.Tensor.cuda):
     dt = DT[dtype]
     h, gh, w = inputs(rows, cols, dt, seed, residual, weight)
     gy = torch.randn(rows, cols, generator=torch.Generator().manual_seed(seed + 1)).to(dt)
     rstd = definition(h, None, None)[2].float()
-    gx, gw = d.dcn_add_rms_norm_backward(*gpu(gy, h, rstd, w), grad_residual_out=None if gh is None else gh.cuda())
+    gx, gw = d.dcn_add_rms_norm_backward(place(gy), place(h), rstd.cuda(), None if w is None else place(w),
+                                         grad_residual_out=None if gh is None else place(gh))
     want, bound, want_w, abs_w = backward_definition(gy, h, rstd, w, gh)
     err = (gx.double().cpu() - want).abs()
     assert (err <= bound + want.abs() * (half_step(dt) + 2 * U) + tiny(dt)).all(), float(err.max())
@@ -258,7 +276,7 @@ def test_backward_repeats_bit_for_bit(cuda_dev):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_backward_in_place_and_unaligned(cuda_dev):
+def test_backward_in_place(cuda_dev):
     h, gh, w = inputs(17, 264, torch.bfloat16, 6)
     gy = torch.randn(17, 264).to(torch.bfloat16)
     rstd = definition(h, None, None)[2].float().cuda()
@@ -268,12 +286,6 @@ def test_backward_in_place_and_unaligned(cuda_dev):
         got = d.dcn_add_rms_norm_backward(gyg, hg, rstd, wg, grad_residual_out=ghg,
                                           grad_x=gyg if which == "grad_out" else ghg)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
-
-    def off(t):
-        return torch.empty(t.numel() + 3, dtype=t.dtype, device="cuda")[1:1 + t.numel()].view(t.shape).copy_(t)
-
-    got = d.dcn_add_rms_norm_backward(off(gy), off(h), rstd, off(w), grad_residual_out=off(gh))
-    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_gradients_against_differences(cuda_dev):
