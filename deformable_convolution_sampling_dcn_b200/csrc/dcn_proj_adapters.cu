@@ -22,6 +22,11 @@
 // programmatic dependent of SHRINK and waits for it only before its first load
 // of t.
 //
+// Where the tiles are fewer than the SMs, a cluster of CTAs (SHRINK) or of pairs
+// (EXPAND) splits the contraction of one tile; the parts meet in distributed
+// shared memory and are added in the order of the splits, each CTA finishing a
+// share of the columns.
+//
 // Both are persistent and warp-specialised: warp 0 streams the 64-wide blocks
 // of both operands by TMA (128-byte swizzle, zero fill past every edge) through
 // a ring, one thread of warp 1 (of the pair's first CTA) issues tcgen05.mma into
@@ -44,6 +49,9 @@ constexpr int kBK = 64;
 constexpr int kABytes = kBM * kBK * 2;
 constexpr int kThreads = 6 * 32;
 constexpr int kMaxStages = 8;
+// CTA pairs in clusters of up to eight CTAs that run at the same time: a cluster lies within one of the GPU's
+// processing clusters of 16 to 20 SMs, so 128 of the 148 SMs can be counted on.
+constexpr int kClusterPairs = 64;
 constexpr int kReqCache = 1024;  // requests whose table is kept in shared memory
 
 struct LargeParams {
@@ -56,6 +64,7 @@ struct LargeParams {
     int NT;                // EXPAND: tiles of output channels
     int BN;                // EXPAND: output channels of a tile; SHRINK: rank rounded up to 16
     int stages, tmem_cols;
+    int splits;            // of the contraction; a cluster has one job where this is not 1
     long long jobs;        // EXPAND: tiles of y; SHRINK: pairs of a tile and a request
     unsigned int *err;
 };
@@ -153,6 +162,49 @@ struct Slot {
     }
 };
 
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of CTA `rank`'s variable that is at `addr` in this one.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float load_remote(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr));
+    return v;
+}
+
+// A split's accumulator, 128 rows (this warp's 32, one a lane) x `cols`, into its shared memory, column by column.
+__device__ __forceinline__ void dump_accumulator(uint32_t taddr, float *dst, int cols, int first, int step) {
+    for (int c = first; c < cols; c += step) {
+        float v[16];
+        tmem_ld16(taddr + (uint32_t)c, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dst[(c + i) * 128] = v[i];
+    }
+}
+// Sum of the splits' values of 8 columns from c on, in the order of the splits; their CTAs are `stride` ranks apart.
+__device__ __forceinline__ void add_splits(uint32_t addr, int c, int splits, int first_rank, int stride, float *v) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    for (int s = 0; s < splits; ++s) {
+        const uint32_t base = in_cta(addr + (uint32_t)(c * 128 * 4), first_rank + s * stride);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += load_remote(base + (uint32_t)(i * 128 * 4));
+    }
+}
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     adapters_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
@@ -176,7 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *sm.tmem_slot;
     if (blockIdx.x == 0 && warp >= 2)
         for (int i = threadIdx.x - 64; i < p.requests; i += 128) report_bad_adapter(req.which[i], p.adapters, p.err);
-    const int KB = (p.cin + kBK - 1) / kBK;
+    const int blocks = (p.cin + kBK - 1) / kBK;
+    // this CTA's part of the contraction and its cluster's job
+    const int split = p.splits > 1 ? (int)cta_rank() : 0;
+    const int kb0 = blocks * split / p.splits, kb1 = blocks * (split + 1) / p.splits;
+    const long long job0 = blockIdx.x / p.splits, jobs_step = gridDim.x / p.splits;
 
     if (warp == 0) {
         // ---- producer
@@ -184,11 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             Slot at;
             long long issued = 0;
             bool ok = true;
-            for (long long j = blockIdx.x; j < p.jobs && ok; j += gridDim.x) {
+            for (long long j = job0; j < p.jobs && ok; j += jobs_step) {
                 const int r = req.of_pair(j);
                 if (r < 0) continue;
                 const int row = (int)(j - r) * kBM, arow = req.adapter(r) * p.rank;
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     const uint32_t full = sm.full + 8 * at.s;
                     if (at.pass >= 1 && !wait_or_abort(sm.empty + 8 * at.s, (at.pass - 1) & 1, sm.abort_flag)) {
                         ok = false;
@@ -217,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Slot at;
             int local = 0;
             bool ok = true, issued = false;
-            for (long long j = blockIdx.x; j < p.jobs && ok; j += gridDim.x) {
+            for (long long j = job0; j < p.jobs && ok; j += jobs_step) {
                 if (req.of_pair(j) < 0) continue;
                 const int buf = local & 1;
                 if (local >= 2 && !wait_or_abort(sm.acc_empty + 8 * buf, ((local >> 1) - 1) & 1, sm.abort_flag)) {
@@ -226,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t dcol = tmem + (uint32_t)(buf * p.BN);
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_or_abort(sm.full + 8 * at.s, at.pass & 1, sm.abort_flag)) {
                         ok = false;
                         break;
@@ -234,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const uint64_t ad = a0 + at.s * sstep, bd = b0 + at.s * sstep;
                     // steps of 16 elements = 2 descriptor units; columns past cin are zeros
-                    mma_f16(dcol, ad, bd, idesc, kb != 0);
+                    mma_f16(dcol, ad, bd, idesc, kb != kb0);
                     mma_f16(dcol, ad + 2, bd + 2, idesc, 1u);
                     mma_f16(dcol, ad + 4, bd + 4, idesc, 1u);
                     mma_f16(dcol, ad + 6, bd + 6, idesc, 1u);
@@ -258,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- epilogue: warp w reads tensor-memory lanes 32 * (w % 4) .. +31 = rows of the tile
         const int quad = warp & 3;
         int local = 0;
-        for (long long j = blockIdx.x; j < p.jobs; j += gridDim.x) {
+        for (long long j = job0; j < p.jobs; j += jobs_step) {
             const int r = req.of_pair(j);
             if (r < 0) continue;
             const int row = (int)(j - r) * kBM + quad * 32 + lane, buf = local & 1;
@@ -270,6 +326,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
+            if (p.splits > 1) {
+                // the products have read the ring
+                dump_accumulator(tmem + ((uint32_t)(32 * quad) << 16), reinterpret_cast<float *>(sm.ring) + quad * 32 + lane,
+                                 p.BN, 0, 16);
+                break;
+            }
             for (int c = 0; c < p.rank; c += 16) {  // warp-uniform
                 float v[16];
                 tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * p.BN + c), v);
@@ -286,6 +348,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++local;
         }
     }
+    if (p.splits > 1) {
+        __syncwarp();
+        cluster_sync();
+        const int r = req.of_pair(job0), quad = warp & 3;
+        if (r >= 0 && warp >= 2) {
+            const int row = (int)(job0 - r) * kBM + quad * 32 + lane;
+            const float mul = p.scale ? p.scale[req.adapter(r)] : 1.0f;
+            const uint32_t addr = smem_u32(sm.ring) + (uint32_t)(quad * 32 + lane) * 4;
+            for (int c = 8 * split; c < p.rank; c += 8 * p.splits) {
+                float v[8];
+                add_splits(addr, c, p.splits, 0, 1, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= mul;
+                if (row >= req.at(r) && row < req.at(r + 1))
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(p.t) + (long long)row * p.rank + c) = pack16<T>(v);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // the other CTAs may still read this one's sums
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -297,23 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- CTA pairs
 
-__device__ __forceinline__ uint32_t cta_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// Address of the pair's first CTA's variable that is at `addr` in this one.
-__device__ __forceinline__ uint32_t in_first_cta(uint32_t addr) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-    return r;
-}
-__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Fetches a tensor map ahead of its first use.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 // Load into this CTA's shared memory that completes on a barrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
@@ -322,6 +390,11 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
+}
+// Brings a box to L2.
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *map, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(c0), "r"(c1)
+                 : "memory");
 }
 // 256 rows: the first CTA's 128 and the second's; N columns, half of the operand in each CTA.
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -345,11 +418,12 @@ __device__ __forceinline__ void mma_pair_rows(uint32_t d_tmem, uint64_t adesc, u
         "r"(off[5]), "r"(off[6]), "r"(off[7])
         : "memory");
 }
-// Arrive on `bar` of both CTAs once every product this thread issued so far is complete.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
+// Arrive on `bar` of both CTAs of the pair (ranks `leader` and the next) once every product this thread issued so far
+// is complete.
+__device__ __forceinline__ void commit_pair(uint32_t bar, int leader) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3 << leader))
         : "memory");
 }
 
@@ -375,16 +449,24 @@ constexpr int kExpandThreads = 10 * 32;            // eight epilogue warps
 constexpr int kOutStage = 8 * kOutBytes + 8 * kBK * 4;  // and the bias of a chunk in fp32, for each of them
 
 template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
+__global__ void __launch_bounds__(kExpandThreads, 1)
     adapters_expand_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap wmap,
                            const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap bmap,
                            const __grid_constant__ CUtensorMap ymap, const LargeParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const int sbytes = kABytes + p.BN / 2 * kBK * 2;
     const Smem sm(smem_raw, p.stages * sbytes + kOutStage);  // the staged boxes of y follow the ring
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = (int)cta_rank();
-    const long long pair0 = blockIdx.x / 2, pairs = gridDim.x / 2;
-    if (threadIdx.x == 0) sm.init(16);  // the epilogue warps of both CTAs
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int crank = (int)cta_rank(), rank = crank & 1, split = crank >> 1, leader = crank & ~1;
+    const long long pair0 = blockIdx.x / (2 * p.splits), pairs = gridDim.x / (2 * p.splits);
+    if (threadIdx.x == 0) {
+        sm.init(16);  // the epilogue warps of both CTAs
+        prefetch_map(&xmap);
+        prefetch_map(&wmap);
+        prefetch_map(&tmap);
+        prefetch_map(&bmap);
+        prefetch_map(&ymap);
+    }
     const Requests req = sm.requests(p);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sm.tmem_slot)),
@@ -397,7 +479,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
     cluster_sync();  // the other CTA's barriers and tensor memory are ready
     tc_fence_after();
     const uint32_t tmem = *sm.tmem_slot;
-    const int KB = (p.cin + kBK - 1) / kBK, RB = (p.rank + kBK - 1) / kBK;
+    const int blocks = (p.cin + kBK - 1) / kBK, RB = (p.rank + kBK - 1) / kBK;
+    // this pair's part of the contraction; the adapters' blocks belong to the last one
+    const int kb0 = blocks * split / p.splits, kb1 = blocks * (split + 1) / p.splits;
+    const bool adapters = split == p.splits - 1;
 
     if (warp == 0) {
         // ---- producer: this CTA's rows and half of the channels; both CTAs' loads complete on the first one's
@@ -406,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
             Slot at;
             long long issued = 0;
             bool ok = true, waited = false;
-            const uint32_t full0 = in_first_cta(sm.full);
+            const uint32_t full0 = in_cta(sm.full, leader);
             auto load = [&](const CUtensorMap *am, int k, int row, const CUtensorMap *bm, int brow) {
                 if (at.pass >= 1 && !wait_or_abort(sm.empty + 8 * at.s, (at.pass - 1) & 1, sm.abort_flag)) return false;
                 if (rank == 0) mbar_arrive_expect_tx(sm.full + 8 * at.s, (uint32_t)(2 * sbytes));
@@ -420,8 +505,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
             for (long long j = pair0; j < p.jobs && ok; j += pairs) {
                 const int tile = (int)(j / p.NT) * kPairRows, row = tile + rank * kBM;
                 const int n0 = (int)(j % p.NT) * p.BN + rank * (p.BN / 2);
-                for (int kb = 0; kb < KB && ok; ++kb) ok = load(&xmap, kb * kBK, row, &wmap, n0);
+                for (int kb = kb0; kb < kb1 && ok; ++kb) ok = load(&xmap, kb * kBK, row, &wmap, n0);
+                if (!adapters) continue;
                 if (ok && !waited) {
+                    // the first tile's B, which does not depend on SHRINK, comes to L2 meanwhile
+                    for (int r = req.first_ending_after(tile); r < p.requests && req.at(r) < tile + kPairRows; ++r)
+                        if (req.adapter(r) >= 0 && req.at(r + 1) > req.at(r))
+                            for (int rb = 0; rb < RB; ++rb) prefetch_2d(&bmap, rb * kBK, req.adapter(r) * p.cout + n0);
                     // t comes from the SHRINK kernel: visible from here on, to the TMA too
                     asm volatile("griddepcontrol.wait;" ::: "memory");
                     asm volatile("fence.proxy.async;" ::: "memory");
@@ -459,22 +549,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t dcol = tmem + (uint32_t)(buf * p.BN);
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_or_abort(sm.full + 8 * at.s, at.pass & 1, sm.abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t ad = a0 + at.s * sstep, bd = b0 + at.s * sstep;
-                    mma_pair(dcol, ad, bd, idesc, kb != 0);
+                    mma_pair(dcol, ad, bd, idesc, kb != kb0);
                     mma_pair(dcol, ad + 2, bd + 2, idesc, 1u);
                     mma_pair(dcol, ad + 4, bd + 4, idesc, 1u);
                     mma_pair(dcol, ad + 6, bd + 6, idesc, 1u);
                     issued = true;
-                    commit_pair(sm.empty + 8 * at.s);
+                    commit_pair(sm.empty + 8 * at.s, leader);
                     at.next(p.stages);
                 }
-                for (int r = req.first_ending_after(tile); ok && r < p.requests && req.at(r) < tile + kPairRows; ++r) {
+                for (int r = req.first_ending_after(tile);
+                     adapters && ok && r < p.requests && req.at(r) < tile + kPairRows; ++r) {
                     if (req.adapter(r) < 0 || req.at(r + 1) <= req.at(r)) continue;
                     // this request's rows of the tile
                     const int r0 = req.at(r) - tile, r1 = req.at(r + 1) - tile;
@@ -490,17 +581,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
                         const uint64_t ad = a0 + at.s * sstep, bd = b0 + at.s * sstep;
                         const int steps = min(4, (p.rank - rb * kBK + 15) / 16);
                         for (int i = 0; i < steps; ++i) mma_pair_rows(dcol, ad + 2 * i, bd + 2 * i, idesc, off);
-                        commit_pair(sm.empty + 8 * at.s);
+                        commit_pair(sm.empty + 8 * at.s, leader);
                         at.next(p.stages);
                     }
                 }
                 if (!ok) break;
-                commit_pair(sm.acc_full + 8 * buf);
+                commit_pair(sm.acc_full + 8 * buf, leader);
             }
             if (!ok) raise_abort(sm.abort_flag, p.err);
             if (issued) {
                 // every product has finished before tensor memory is freed
-                commit_pair(sm.drain);
+                commit_pair(sm.drain, leader);
                 mbar_wait_bounded(sm.drain, 0, kTcWaitNs);
             }
         }
@@ -513,7 +604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
         const int quad = warp & 3, half = (warp - 2) >> 2;
         const T *bias = static_cast<const T *>(p.bias);
         const int covered0 = req.at(0), covered1 = req.at(p.requests);
-        const uint32_t acc_empty0 = in_first_cta(sm.acc_empty);
+        const uint32_t acc_empty0 = in_cta(sm.acc_empty, leader);
         unsigned char *own = sm.ring + p.stages * sbytes + (warp - 2) * kOutBytes;  // box of 4 KB
         const uint32_t stage = smem_u32(own);
         float *bias_s = reinterpret_cast<float *>(sm.ring + p.stages * sbytes + 8 * kOutBytes) + (warp - 2) * kBK;
@@ -525,6 +616,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
             const bool boxes = row0 >= covered0 && min(row0 + 32, p.rows) <= covered1;
             const bool write = row >= covered0 && row < covered1;
             bool ready = false;
+            if (p.splits > 1) {
+                if (!wait_or_abort(sm.acc_full, 0, sm.abort_flag)) {
+                    raise_abort(sm.abort_flag, p.err);
+                    break;
+                }
+                tc_fence_after();
+                // the products have read the ring
+                dump_accumulator(tmem + ((uint32_t)(32 * quad) << 16), reinterpret_cast<float *>(sm.ring) + quad * 32 + lane,
+                                 p.BN, 16 * half, 32);
+                break;
+            }
             for (int c = half * kBK; c < ncols; c += 2 * kBK) {  // warp-uniform
                 __syncwarp();
                 for (int i = lane; i < kBK; i += 32)
@@ -577,7 +679,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
             __syncwarp();
             if (lane == 0) arrive_remote(acc_empty0 + 8 * buf);
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        // the boxes have left shared memory; the end of the kernel completes their writes
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+    }
+    if (p.splits > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 2 && pair0 < p.jobs) {
+            // this split's share of the columns, 8 at a time; the row is the lane's
+            const int quad = warp & 3, half = (warp - 2) >> 2;
+            const int row = (int)(pair0 / p.NT) * kPairRows + rank * kBM + quad * 32 + lane;
+            const int n0 = (int)(pair0 % p.NT) * p.BN, ncols = min(p.BN, p.cout - n0);
+            const bool write = row >= req.at(0) && row < req.at(p.requests);
+            const uint32_t addr = smem_u32(sm.ring) + (uint32_t)(quad * 32 + lane) * 4;
+            for (int c = 8 * (split * 2 + half); c < ncols; c += 16 * p.splits) {
+                float v[8], b[8] = {};
+                if (p.bias) unpack16<T>(ld_nc16(static_cast<const T *>(p.bias) + n0 + c), b);
+                add_splits(addr, c, p.splits, rank, 2, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += b[i];
+                if (write)
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (long long)row * p.cout + n0 + c) = pack16<T>(v);
+            }
+        }
         __syncwarp();
     }
     // a pair that had no t to wait for still ends after SHRINK: the next user of the workspace is ordered behind
@@ -612,12 +737,15 @@ int tmem_columns(int bn) {
     return cols;
 }
 
-// Stages of `sbytes` that fit, and the shared memory they take.
-size_t plan_smem(LargeParams &p, size_t sbytes, size_t limit) {
+// Stages of `sbytes` that fit and that a CTA's `use` blocks can fill (a short ring leaves EXPAND room beside SHRINK's
+// last CTAs), and the shared memory they take; the accumulator of a split, `sums` bytes, takes the ring's place.
+size_t plan_smem(LargeParams &p, size_t sbytes, size_t sums, size_t limit, long long use) {
     const size_t other = 1024 + (2 * kMaxStages + 5) * 8 + 8 +
                          (p.requests <= kReqCache ? (size_t)(2 * p.requests + 1) * 4 : 0);
-    p.stages = kMaxStages;
+    p.stages = use < 2 ? 2 : use < kMaxStages ? (int)use : kMaxStages;
     while (p.stages > 2 && other + p.stages * sbytes > limit) --p.stages;
+    if (p.splits > 1)
+        while (p.stages * sbytes < sums && p.stages < kMaxStages) ++p.stages;
     return other + p.stages * sbytes;
 }
 
@@ -632,19 +760,25 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     p.out = a.out;
     p.err = dev->err;
 
-    // The tile width whose rounds of tiles over the CTA pairs cost least: a tile costs its columns, plus the
-    // rows of x that it streams and its epilogue, worth about 128 columns.
+    // Tile width and splits of the contraction by their cost in clocks of an SM, as measured: 2.6 for each 64-wide
+    // row that it fetches (128 of x, half a tile of W, a block of the contraction), 12 for each column of the
+    // epilogue, 1500 for a round of tiles, 4000 for the exchange between splits.  Clusters that split have one tile.
     const long long mt = (a.rows + kPairRows - 1) / kPairRows, pairs = dev->sms / 2;
-    int bn = 0;
-    long long best = 0;
-    for (int c = 256; c >= 64; c /= 2) {
-        const long long tiles = mt * ((a.cout + c - 1) / c);
-        const long long cost = (tiles + pairs - 1) / pairs * (c + 128);
-        if (!bn || cost < best) {
-            bn = c;
-            best = cost;
+    const int blocks = (a.cin + kBK - 1) / kBK;
+    int bn = 0, splits = 1;
+    double best = 0.0;
+    for (int c = 256; c >= 64; c /= 2)
+        for (int s = 1; s <= 4 && s <= blocks; s *= 2) {
+            const long long tiles = mt * ((a.cout + c - 1) / c);
+            if (s > 1 && tiles * s > kClusterPairs) break;
+            const double rounds = s > 1 ? 1.0 : (double)((tiles + pairs - 1) / pairs);
+            const double cost = rounds * (1500.0 + 2.6 * ((blocks + s - 1) / s) * (128 + c / 2) + 12.0 * c) + (s > 1 ? 4000.0 : 0.0);
+            if (!bn || cost < best) {
+                bn = c;
+                splits = s;
+                best = cost;
+            }
         }
-    }
     const int rank16 = (a.rank + 15) / 16 * 16;
     CUtensorMap xm, am, wm, tm, bm, ym;
     if (!encode<T>(&xm, a.x, a.cin, a.rows, kBM) || !encode<T>(&wm, a.weight, a.cin, a.cout, bn / 2) ||
@@ -663,27 +797,40 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     p.BN = rank16;
     p.NT = 1;
     p.jobs = (a.rows + kBM - 1) / kBM + a.requests;
+    p.splits = 1;
+    // the exchange costs 2 us, what 8 blocks take: halve runs of 16 blocks and more
+    while (p.splits < 8 && 2 * p.splits * p.jobs <= 2 * kClusterPairs && blocks >= 16 * p.splits) p.splits *= 2;
     p.tmem_cols = tmem_columns(p.BN);
-    size_t smem = plan_smem(p, kABytes + p.BN * kBK * 2, (size_t)dev->smem_optin);
-    adapters_shrink_kernel<T><<<(unsigned)(p.jobs < dev->sms ? p.jobs : dev->sms), kThreads, smem, stream>>>(xm, am, p);
-    e = cudaGetLastError();
+    size_t smem = plan_smem(p, kABytes + p.BN * kBK * 2, (size_t)p.BN * kBM * 4, (size_t)dev->smem_optin,
+                            (blocks + p.splits - 1) / p.splits * ((p.jobs + dev->sms - 1) / dev->sms));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.stream = stream;
+    cfg.gridDim = dim3((unsigned)(p.splits > 1 ? p.jobs * p.splits : p.jobs < dev->sms ? p.jobs : dev->sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, adapters_shrink_kernel<T>, xm, am, p);
     if (e != cudaSuccess) return e;
 
     p.BN = bn;
     p.NT = (a.cout + bn - 1) / bn;
     p.jobs = mt * p.NT;
+    p.splits = splits;
     p.tmem_cols = tmem_columns(p.BN);
-    smem = kOutStage + plan_smem(p, kABytes + p.BN / 2 * kBK * 2, (size_t)dev->smem_optin - kOutStage);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (p.jobs < pairs ? p.jobs : pairs)));
+    smem = kOutStage + plan_smem(p, kABytes + p.BN / 2 * kBK * 2, (size_t)p.BN * kBM * 4, (size_t)dev->smem_optin - kOutStage,
+                                 ((blocks + splits - 1) / splits + 2) * ((p.jobs + pairs - 1) / pairs));
+    attr[0].val.clusterDim.x = (unsigned)(2 * splits);
+    cfg.gridDim = dim3((unsigned)(2 * splits * (p.jobs < pairs ? p.jobs : pairs)));
     cfg.blockDim = dim3(kExpandThreads);
     cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, adapters_expand_kernel<T>, xm, wm, tm, bm, ym, p);
 }
 

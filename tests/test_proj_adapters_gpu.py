@@ -110,6 +110,13 @@ LARGE = [
     ([700], [0], 520, 264, 128, 1),                                          # two blocks of rank
     ([90, 40, 200], [1, 0, 1], 72, 1032, 72, 2),                             # a ragged second block of rank
     ([20000, 13, 5000], [0, 1, 1], 64, 256, 8, 2),                           # several tiles per CTA
+    # few tiles and a long contraction: clusters split it, in 2, 4 and 8 parts
+    ([70, 0, 30], [1, 0, 0], 4096, 64, 128, 2),
+    ([200, 57], [0, 1], 2056, 136, 24, 2),
+    ([900, 1, 99, 500], [0, -1, 2, 1], 1000, 104, 16, 3),
+    ([66], [0], 192, 64, 8, 1),                                               # as few blocks as splits
+    ([3, 300, 700], [2, 1, 0], 3768, 72, 64, 3),
+    ([2000, 700], [0, 1], 520, 328, 40, 2),
 ]
 
 
