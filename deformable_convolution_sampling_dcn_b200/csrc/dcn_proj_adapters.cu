@@ -738,15 +738,20 @@ int tmem_columns(int bn) {
 }
 
 // Stages of `sbytes` that fit and that a CTA's `use` blocks can fill (a short ring leaves EXPAND room beside SHRINK's
-// last CTAs), and the shared memory they take; the accumulator of a split, `sums` bytes, takes the ring's place.
-size_t plan_smem(LargeParams &p, size_t sbytes, size_t sums, size_t limit, long long use) {
-    const size_t other = 1024 + (2 * kMaxStages + 5) * 8 + 8 +
+// last CTAs), and the shared memory they take with `extra`; the accumulator of a split, `sums` bytes, takes the ring's
+// place.
+// CTAs of a pair or a cluster wait for one another while they hold tensor memory.  Two calls on two streams must not
+// block each other's other halves, so a CTA takes at least the same share of the shared memory as of the tensor
+// memory: CTAs that fit an SM together then find tensor memory together.
+size_t plan_smem(LargeParams &p, size_t sbytes, size_t sums, size_t extra, size_t limit, long long use) {
+    const size_t other = extra + 1024 + (2 * kMaxStages + 5) * 8 + 8 +
                          (p.requests <= kReqCache ? (size_t)(2 * p.requests + 1) * 4 : 0);
     p.stages = use < 2 ? 2 : use < kMaxStages ? (int)use : kMaxStages;
     while (p.stages > 2 && other + p.stages * sbytes > limit) --p.stages;
     if (p.splits > 1)
         while (p.stages * sbytes < sums && p.stages < kMaxStages) ++p.stages;
-    return other + p.stages * sbytes;
+    const size_t need = other + p.stages * sbytes, share = limit * p.tmem_cols / 512;
+    return need > share ? need : share;
 }
 
 template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t stream) {
@@ -801,7 +806,7 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     // the exchange costs 2 us, what 8 blocks take: halve runs of 16 blocks and more
     while (p.splits < 8 && 2 * p.splits * p.jobs <= 2 * kClusterPairs && blocks >= 16 * p.splits) p.splits *= 2;
     p.tmem_cols = tmem_columns(p.BN);
-    size_t smem = plan_smem(p, kABytes + p.BN * kBK * 2, (size_t)p.BN * kBM * 4, (size_t)dev->smem_optin,
+    size_t smem = plan_smem(p, kABytes + p.BN * kBK * 2, (size_t)p.BN * kBM * 4, 0, (size_t)dev->smem_optin,
                             (blocks + p.splits - 1) / p.splits * ((p.jobs + dev->sms - 1) / dev->sms));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -824,8 +829,8 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     p.jobs = mt * p.NT;
     p.splits = splits;
     p.tmem_cols = tmem_columns(p.BN);
-    smem = kOutStage + plan_smem(p, kABytes + p.BN / 2 * kBK * 2, (size_t)p.BN * kBM * 4, (size_t)dev->smem_optin - kOutStage,
-                                 ((blocks + splits - 1) / splits + 2) * ((p.jobs + pairs - 1) / pairs));
+    smem = plan_smem(p, kABytes + p.BN / 2 * kBK * 2, (size_t)p.BN * kBM * 4, kOutStage, (size_t)dev->smem_optin,
+                     ((blocks + splits - 1) / splits + 2) * ((p.jobs + pairs - 1) / pairs));
     attr[0].val.clusterDim.x = (unsigned)(2 * splits);
     cfg.gridDim = dim3((unsigned)(2 * splits * (p.jobs < pairs ? p.jobs : pairs)));
     cfg.blockDim = dim3(kExpandThreads);
