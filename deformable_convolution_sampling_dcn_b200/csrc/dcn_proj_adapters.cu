@@ -49,9 +49,9 @@ constexpr int kBK = 64;
 constexpr int kABytes = kBM * kBK * 2;
 constexpr int kThreads = 6 * 32;
 constexpr int kMaxStages = 8;
-// CTA pairs in clusters of up to eight CTAs that run at the same time: a cluster lies within one of the GPU's
-// processing clusters of 16 to 20 SMs, so 128 of the 148 SMs can be counted on.
-constexpr int kClusterPairs = 64;
+// CTA pairs of split tiles.  A cluster lies within one of the GPU's processing clusters, and some of 64 pairs in
+// clusters of eight CTAs waited for the others to end (80 rows 1024 -> 1024: 30 us against 17 without splits).
+constexpr int kClusterPairs = 32;
 constexpr int kReqCache = 1024;  // requests whose table is kept in shared memory
 
 struct LargeParams {
@@ -851,13 +851,25 @@ cudaError_t launch_adapters_large(const AdapterArgs &a, cudaStream_t stream) {
     }
 }
 
-// Few rows are bound by the weight's bytes and take the row-wise kernels.
+// The route by its time in microseconds, as measured (one B200; cin and cout of 256 to 4096, ranks 16 and 64).  The
+// row-wise route (dcn_proj_adapters_rows.cu): 6.5, the weight at 5 TB/s, 0.02 a row for the partial sums, and 2.4
+// million products a microsecond for t and the adapter term, which do not use the tensor cores.  The tiles of this
+// file: 12, and 0.36 for each block of the contraction and round of tiles.  Up to 64 rows it is always the first.
+static bool few_rows(const AdapterArgs &a) {
+    if (a.rows <= 64) return true;
+    if (a.rows > kMaxSmallRows) return false;
+    const double rows = 6.5 + 2.0 * a.cin * a.cout / 5.0e6 + 0.02 * (double)a.rows +
+                        (double)a.rows * a.rank * ((double)a.cin + a.cout) / 2.4e6;
+    const int blocks = (a.cin + kBK - 1) / kBK, tiles = (a.cout + 63) / 64, rounds = (tiles + 73) / 74;
+    return rows <= 12.0 + 0.36 * blocks * rounds;
+}
+
 size_t proj_adapters_workspace(const AdapterArgs &a) {
-    return a.rows <= kMaxSmallRows ? adapters_small_workspace(a) : adapters_large_workspace(a);
+    return few_rows(a) ? adapters_small_workspace(a) : adapters_large_workspace(a);
 }
 
 cudaError_t launch_proj_adapters(const AdapterArgs &a, cudaStream_t stream) {
-    return a.rows <= kMaxSmallRows ? launch_adapters_small(a, stream) : launch_adapters_large(a, stream);
+    return few_rows(a) ? launch_adapters_small(a, stream) : launch_adapters_large(a, stream);
 }
 
 }  // namespace dcnb

@@ -12,7 +12,7 @@ namespace dcnb {
 // Bit of the device error word: a request named an adapter outside [-1, num_adapters).
 enum : unsigned { kDevErrBadAdapter = 2u };
 
-constexpr int kMaxSmallRows = 64;
+constexpr int kMaxSmallRows = 256;  // columns of a tcgen05 product
 
 // Adapter of request s: -1 for none.  An index out of range counts as none.
 __device__ __forceinline__ int adapter_of(const int32_t *which, int s, int num_adapters) {

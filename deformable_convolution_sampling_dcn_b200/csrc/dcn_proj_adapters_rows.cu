@@ -1,4 +1,5 @@
-// Projection with low-rank adapters, few rows: single tokens of many requests.
+// Projection with low-rank adapters, few rows (at most 256): single tokens of
+// many requests, short prompts.
 //   t[m, :] = scale[a] * A[a] x[m]             a = adapter of row m's request
 //   y[m, n] = bias[n] + sum_k W[n, k] x[m, k] + sum_j B[a][n, j] t[m, j]
 //
@@ -405,9 +406,12 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     p.err = dev->err;
     p.tmem_cols = 32;
     while (p.tmem_cols < 2 * p.mpad) p.tmem_cols <<= 1;
+    // as many stages as fit and as a run has blocks
     const int run = (p.kb * p.tiles + p.ctas - 1) / p.ctas;
-    p.stages = run < kMaxStages ? (run < 2 ? 2 : run) : kMaxStages;
-    const size_t smem = 1024 + (size_t)p.stages * (kWBytes + p.mpad * kBK * 2) + (2 * kMaxStages + 5) * 8 + 8;
+    const size_t sbytes = kWBytes + (size_t)p.mpad * kBK * 2, other = 1024 + (2 * kMaxStages + 5) * 8 + 8;
+    p.stages = run < 2 ? 2 : run < kMaxStages ? run : kMaxStages;
+    while (other + p.stages * sbytes > (size_t)dev->smem_optin) --p.stages;
+    const size_t smem = other + p.stages * sbytes;
     CUtensorMap wm, xm;
     if (!encode<T>(&wm, a.weight, a.cin, a.cout, kTN) || !encode<T>(&xm, a.x, a.cin, a.rows, p.mpad))
         return cudaErrorInvalidValue;

@@ -307,9 +307,10 @@ dcn_status deform_roi_pool_forward(const droi_params *p, const void *x, const fl
  * [0, rows]; an order that is not ascending gives wrong values but no access
  * out of range.  An adapter outside [-1, num_adapters) counts as none and sets
  * bit 1 of the device error word (dcn_take_device_error).
- * Sums are fp32.  With at most 64 rows A[a] x stays in fp32; with more it is
- * scaled and rounded once to the storage dtype, as an operand of the second
- * tensor-core product.  Values of one row do not depend on other requests'.
+ * Sums are fp32.  With at most 64 rows A[a] x stays in fp32; with more it may be
+ * (and above 256 rows is) scaled and rounded once to the storage dtype, as an
+ * operand of the second tensor-core product.  Values of one row do not depend
+ * on other requests'.
  * cin, cout and rank are multiples of 8, cin and cout up to 65536, rank up to
  * 128; rows up to 2^30; num_requests and num_adapters up to 2^20, with
  * num_adapters * cout and num_adapters * rank up to 2^30.  x, weight, bias, a, b

@@ -138,7 +138,7 @@ def test_adapter_params(lib, kw, status):
 def test_adapter_pointers(lib):
     p = adapt()
     need = lib.dcn_proj_adapters_workspace_bytes(ctypes.byref(p))
-    assert need == 100 * 16 * 2  # many rows: t in the storage type
+    assert lib.dcn_proj_adapters_workspace_bytes(ctypes.byref(adapt(rows=1000))) == 1000 * 16 * 2  # t in the storage type
     # few rows: t in fp32, and fp32 partial sums of 16 rows for one block of the weight
     assert lib.dcn_proj_adapters_workspace_bytes(ctypes.byref(adapt(rows=10))) == (10 * 16 + 2 * 16 * 128) * 4
     for name in ("x", "w", "start", "which", "out", "ws", "a", "b"):

@@ -3,7 +3,7 @@
 Tolerance per element (u = 2^-24, uT = finfo(T).eps / 2): the contraction has
 cin + rank products, exact in fp32, and every addition loses at most one step,
 2u of the running sum, which the sum of magnitudes bounds; with more than 64
-rows t = scale * A x is rounded once (uT, and tiny(T) below its normals); the
+rows t = scale * A x may be rounded once (uT, and tiny(T) below its normals); the
 result is rounded once.
 """
 import pytest
@@ -89,6 +89,15 @@ SMALL = [
     ([3, 0, 5, 0, 0, 20, 4], [1, 0, -1, 2, 1, 0, 1], 256, 128, 128, 3),   # short requests, empty ones
     ([64], [0], 4096, 256, 32, 1),
     ([33, 31], [1, 1], 96, 72, 40, 2),
+    ([65], [0], 64, 64, 16, 1),
+    ([128], [0], 8, 8, 8, 1),
+    ([100, 28, 1], [0, 1, 0], 64, 72, 8, 2),
+    ([1] * 130, [i % 5 - 1 for i in range(130)], 128, 64, 16, 4),
+    ([1] * 256, [i % 33 - 1 for i in range(256)], 1000, 136, 16, 32),       # 32 tiles of adapters
+    ([70, 0, 30, 100], [1, 0, 0, -1], 4096, 64, 128, 2),
+    ([2] * 100, [i % 3 for i in range(100)], 328, 1032, 48, 3),              # two slots a tile, 96 of its rows
+    ([0] * 300 + [5] * 50, [i % 4 - 1 for i in range(350)], 200, 264, 24, 3),  # more requests than rows: a slot a row
+    ([66, 190], [0, 1], 2056, 520, 64, 2),
 ]
 
 
@@ -100,10 +109,10 @@ def test_few_rows(i, dtype, cuda_dev):
 
 
 LARGE = [
-    ([65], [0], 64, 64, 16, 1),
-    ([128], [0], 8, 8, 8, 1),
-    ([100, 28, 1], [0, 1, 0], 64, 72, 8, 2),
-    ([1] * 130, [i % 5 - 1 for i in range(130)], 128, 64, 16, 4),           # 128 requests in one tile
+    ([257], [0], 64, 64, 16, 1),
+    ([384], [0], 8, 8, 8, 1),
+    ([200, 56, 1], [0, 1, 0], 64, 72, 8, 2),
+    ([1] * 300, [i % 5 - 1 for i in range(300)], 128, 64, 16, 4),           # 256 requests in one tile
     ([127, 1, 128, 0, 2, 0, 254], [0, -1, 1, 1, 2, 0, 1], 200, 136, 24, 3),  # at, before and behind tile borders
     ([1600, 1600, 7], [2, -1, 0], 512, 512, 16, 3),
     ([300, 0, 0, 500, 33], [1, 0, 0, 0, 1], 1000, 520, 64, 2),
@@ -111,10 +120,10 @@ LARGE = [
     ([90, 40, 200], [1, 0, 1], 72, 1032, 72, 2),                             # a ragged second block of rank
     ([20000, 13, 5000], [0, 1, 1], 64, 256, 8, 2),                           # several tiles per CTA
     # few tiles and a long contraction: clusters split it, in 2, 4 and 8 parts
-    ([70, 0, 30], [1, 0, 0], 4096, 64, 128, 2),
+    ([270, 0, 30], [1, 0, 0], 4096, 64, 128, 2),
     ([200, 57], [0, 1], 2056, 136, 24, 2),
     ([900, 1, 99, 500], [0, -1, 2, 1], 1000, 104, 16, 3),
-    ([66], [0], 192, 64, 8, 1),                                               # as few blocks as splits
+    ([266], [0], 192, 64, 8, 1),                                              # as few blocks as splits
     ([3, 300, 700], [2, 1, 0], 3768, 72, 64, 3),
     ([2000, 700], [0, 1], 520, 328, 40, 2),
 ]
@@ -127,14 +136,15 @@ def test_many_rows(i, dtype, cuda_dev):
     check(s, call(s))
 
 
-@pytest.mark.parametrize("lens,which", [([5, 6], [0, 1]), ([100, 33], [1, 0])])
+@pytest.mark.parametrize("lens,which", [([5, 6], [0, 1]), ([300, 33], [1, 0])])
 def test_without_bias_or_scale(lens, which, cuda_dev):
     s = make(lens, which, 136, 80, 16, 2, "f16", 50, bias=False, scale=False)
     check(s, call(s))
 
 
 @pytest.mark.parametrize("rows,first,lens", [(40, 0, [7, 12]), (40, 5, [7, 12]), (300, 0, [100, 60]),
-                                             (300, 9, [150, 100]), (64, 0, [0, 0]), (500, 0, [0, 0])])
+                                             (300, 9, [150, 100]), (64, 0, [0, 0]), (500, 0, [0, 0]),
+                                             (200, 3, [90, 40])])
 def test_rows_of_no_request_stay(rows, first, lens, cuda_dev):
     """Padding before the first and behind the last request is left as it was, whatever x holds there."""
     s = make(lens, [1, 0], 64, 96, 16, 2, "bf16", 60, rows=rows, first=first)
@@ -148,7 +158,7 @@ def test_rows_of_no_request_stay(rows, first, lens, cuda_dev):
     check(s, y, slice(first, end))
 
 
-@pytest.mark.parametrize("lens", [[4, 4, 4], [60, 40, 100]])
+@pytest.mark.parametrize("lens", [[4, 4, 4], [60, 40, 100], [60, 40, 200]])
 def test_one_requests_infinities_stay_its_own(lens, cuda_dev):
     """NaN and infinities in one request's rows or adapter reach no other request in the same tile."""
     s = make(lens, [0, 1, 2], 64, 64, 16, 3, "f16", 70)
@@ -165,7 +175,7 @@ def test_one_requests_infinities_stay_its_own(lens, cuda_dev):
 
 
 def test_bad_adapter_index_is_reported(cuda_dev):
-    for lens in ([3, 4], [100, 90]):
+    for lens in ([3, 4], [100, 90], [300, 90]):
         s = make(lens, [7, 1], 64, 64, 16, 2, "bf16", 80)
         y = call(s)
         torch.cuda.synchronize()
@@ -196,12 +206,12 @@ def test_many_requests(n, cuda_dev):
     check(s, call(s))
     lens = [1 if i % (n // 40) == 0 else 0 for i in range(n)]  # few rows, many empty requests
     s = make(lens, [i % 4 - 1 for i in range(n)], 64, 64, 8, 3, "f16", n)
-    assert s["x"].shape[0] <= 64
+    assert s["x"].shape[0] <= 256
     check(s, call(s))
 
 
 def test_no_adapters_and_empty(cuda_dev):
-    for rows in (5, 200):
+    for rows in (5, 200, 400):
         s = make([rows], [-1], 64, 64, 16, 1, "f16", 90)
         s["a"], s["b"], s["scale"] = s["a"][:0], s["b"][:0], s["scale"][:0]
         check(s, call(s))
@@ -222,7 +232,7 @@ def test_leading_dimensions(cuda_dev):
     assert y.shape == (4, 5, 6, 72) and torch.equal(y.view(120, 72), flat)
 
 
-@pytest.mark.parametrize("lens", [[1] * 20, [200, 100]])
+@pytest.mark.parametrize("lens", [[1] * 20, [50, 100], [200, 100]])
 def test_streams_graphs_and_repeats(lens, cuda_dev):
     n = len(lens)
     s = make(lens, [i % 3 - 1 for i in range(n)], 512, 256, 16, 2, "bf16", 94)
