@@ -167,7 +167,7 @@ def _pair(v) -> Tuple[int, int]:
 def _cuda_tensor(name, t: torch.Tensor, dtype=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -607,7 +607,7 @@ class GradList:
                 raise TypeError("gradients and out buffers must be torch.Tensors")
             if t.dtype not in _DTYPE_CODE:
                 raise TypeError(f"unsupported dtype {t.dtype}")
-            if t.device.type != "cuda":
+            if not t.is_cuda:
                 raise ValueError("gradients must be CUDA tensors (the library has no CPU path)")
             if not t.is_contiguous():
                 raise ValueError("gradients and out buffers must be contiguous")

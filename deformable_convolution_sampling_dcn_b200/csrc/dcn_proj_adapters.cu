@@ -64,6 +64,7 @@ struct LargeParams {
     int NT;                // EXPAND: tiles of output channels
     int BN;                // EXPAND: output channels of a tile; SHRINK: rank rounded up to 16
     int stages, tmem_cols;
+    int aw;                // bytes of a row of an adapter block: 32, 64 or 128, its swizzle too
     int splits;            // of the contraction; a cluster has one job where this is not 1
     long long jobs;        // EXPAND: tiles of y; SHRINK: pairs of a tile and a request
     unsigned int *err;
@@ -443,6 +444,14 @@ __device__ __forceinline__ uint32_t lane_bits(int lo, int hi) {
     return (hi == 32 ? 0xffffffffu : (1u << hi) - 1u) & ~((1u << lo) - 1u);
 }
 
+// The descriptor of a 128-byte-swizzled operand for one of 32- or 64-byte rows in the swizzle of that width: 8-row
+// groups 256 or 512 bytes apart.
+__device__ __forceinline__ uint64_t narrow_desc(uint64_t d, int row_bytes) {
+    if (row_bytes == 128) return d;
+    d &= ~((7ull << 61) | (0x3fffull << 32));
+    return d | (uint64_t)(row_bytes == 64 ? 4 : 6) << 61 | (uint64_t)(8 * row_bytes >> 4) << 32;
+}
+
 constexpr int kPairRows = 2 * kBM;
 constexpr int kOutBytes = 32 * kBK * 2;           // a warp's staged box of y
 constexpr int kExpandThreads = 10 * 32;            // eight epilogue warps
@@ -492,9 +501,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             long long issued = 0;
             bool ok = true, waited = false;
             const uint32_t full0 = in_cta(sm.full, leader);
-            auto load = [&](const CUtensorMap *am, int k, int row, const CUtensorMap *bm, int brow) {
+            auto load = [&](const CUtensorMap *am, int k, int row, const CUtensorMap *bm, int brow, uint32_t bytes) {
                 if (at.pass >= 1 && !wait_or_abort(sm.empty + 8 * at.s, (at.pass - 1) & 1, sm.abort_flag)) return false;
-                if (rank == 0) mbar_arrive_expect_tx(sm.full + 8 * at.s, (uint32_t)(2 * sbytes));
+                if (rank == 0) mbar_arrive_expect_tx(sm.full + 8 * at.s, 2 * bytes);
                 const uint32_t st = smem_u32(sm.ring) + at.s * sbytes;
                 tma_load_2d_pair(st, am, full0 + 8 * at.s, k, row);
                 tma_load_2d_pair(st + kABytes, bm, full0 + 8 * at.s, k, brow);
@@ -505,7 +514,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             for (long long j = pair0; j < p.jobs && ok; j += pairs) {
                 const int tile = (int)(j / p.NT) * kPairRows, row = tile + rank * kBM;
                 const int n0 = (int)(j % p.NT) * p.BN + rank * (p.BN / 2);
-                for (int kb = kb0; kb < kb1 && ok; ++kb) ok = load(&xmap, kb * kBK, row, &wmap, n0);
+                for (int kb = kb0; kb < kb1 && ok; ++kb) ok = load(&xmap, kb * kBK, row, &wmap, n0, sbytes);
                 if (!adapters) continue;
                 if (ok && !waited) {
                     // the first tile's B, which does not depend on SHRINK, comes to L2 meanwhile
@@ -521,7 +530,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                     const int ad = req.adapter(r);
                     if (ad < 0 || req.at(r + 1) <= req.at(r)) continue;
                     for (int rb = 0; rb < RB && ok; ++rb)
-                        ok = load(&tmap, rb * kBK, row, &bmap, ad * p.cout + n0);
+                        ok = load(&tmap, rb * kBK, row, &bmap, ad * p.cout + n0, (kBM + p.BN / 2) * p.aw);
                 }
             }
             if (!ok) raise_abort(sm.abort_flag, p.err);
@@ -537,6 +546,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             const uint32_t idesc = (instr_desc_f16(std::is_same<T, __nv_bfloat16>::value ? 1 : 0, p.BN) &
                                     ~(31u << 24)) | ((uint32_t)(kPairRows >> 4) << 24);
             const uint64_t a0 = smem_desc_sw128(smem_u32(sm.ring)), b0 = smem_desc_sw128(smem_u32(sm.ring + kABytes));
+            const uint64_t a1 = narrow_desc(a0, p.aw), b1 = narrow_desc(b0, p.aw);
             const uint32_t sstep = (uint32_t)sbytes >> 4;
             Slot at;
             int local = 0;
@@ -578,7 +588,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t ad = a0 + at.s * sstep, bd = b0 + at.s * sstep;
+                        const uint64_t ad = a1 + at.s * sstep, bd = b1 + at.s * sstep;
                         const int steps = min(4, (p.rank - rb * kBK + 15) / 16);
                         for (int i = 0; i < steps; ++i) mma_pair_rows(dcol, ad + 2 * i, bd + 2 * i, idesc, off);
                         commit_pair(sm.empty + 8 * at.s, leader);
@@ -718,16 +728,19 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     }
 }
 
-// 64-column boxes of `box` rows over a [rows, cols] matrix of T.
+// Boxes of `box` rows and `width` bytes over a [rows, cols] matrix of T, in the swizzle of that width.
 template <typename T>
-bool encode(CUtensorMap *m, const void *base, long long cols, long long rows, int box) {
+bool encode(CUtensorMap *m, const void *base, long long cols, long long rows, int box, int width = 128) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t str[1] = {(cuuint64_t)cols * 2};
-    const cuuint32_t bx[2] = {(cuuint32_t)kBK, (cuuint32_t)box}, es[2] = {1, 1};
+    const cuuint32_t bx[2] = {(cuuint32_t)(width / 2), (cuuint32_t)box}, es[2] = {1, 1};
+    const CUtensorMapSwizzle sw = width == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                : CU_TENSOR_MAP_SWIZZLE_32B;
     const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     return encode_fn()(m, dt, 2, const_cast<void *>(base), dims, str, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -767,7 +780,7 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
 
     // Tile width and splits of the contraction by their cost in clocks of an SM, as measured: 2.6 for each 64-wide
     // row that it fetches (128 of x, half a tile of W, a block of the contraction), 12 for each column of the
-    // epilogue, 1500 for a round of tiles, 4000 for the exchange between splits.  Clusters that split have one tile.
+    // epilogue, 1500 for a round of tiles, 10000 for the exchange between splits.  Clusters that split have one tile.
     const long long mt = (a.rows + kPairRows - 1) / kPairRows, pairs = dev->sms / 2;
     const int blocks = (a.cin + kBK - 1) / kBK;
     int bn = 0, splits = 1;
@@ -777,7 +790,7 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
             const long long tiles = mt * ((a.cout + c - 1) / c);
             if (s > 1 && tiles * s > kClusterPairs) break;
             const double rounds = s > 1 ? 1.0 : (double)((tiles + pairs - 1) / pairs);
-            const double cost = rounds * (1500.0 + 2.6 * ((blocks + s - 1) / s) * (128 + c / 2) + 12.0 * c) + (s > 1 ? 4000.0 : 0.0);
+            const double cost = rounds * (1500.0 + 2.6 * ((blocks + s - 1) / s) * (128 + c / 2) + 12.0 * c) + (s > 1 ? 10000.0 : 0.0);
             if (!bn || cost < best) {
                 bn = c;
                 splits = s;
@@ -785,14 +798,17 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
             }
         }
     const int rank16 = (a.rank + 15) / 16 * 16;
+    // low ranks in rows of their own width: boxes of 128 bytes that are mostly fill cost as much as full ones
+    // (256 -> 4096, 80 rows: 23 us at rank 16 against 16 at rank 64)
+    p.aw = a.rank <= 16 ? 32 : a.rank <= 32 ? 64 : 128;
     CUtensorMap xm, am, wm, tm, bm, ym;
     if (!encode<T>(&xm, a.x, a.cin, a.rows, kBM) || !encode<T>(&wm, a.weight, a.cin, a.cout, bn / 2) ||
         !encode<T>(&ym, a.out, a.cout, a.rows, 32))
         return cudaErrorInvalidValue;
     am = tm = bm = wm;  // never read without adapters
     if (a.adapters > 0 && (!encode<T>(&am, a.a, a.cin, (long long)a.adapters * a.rank, rank16) ||
-                           !encode<T>(&tm, a.workspace, a.rank, a.rows, kBM) ||
-                           !encode<T>(&bm, a.b, a.rank, (long long)a.adapters * a.cout, bn / 2)))
+                           !encode<T>(&tm, a.workspace, a.rank, a.rows, kBM, p.aw) ||
+                           !encode<T>(&bm, a.b, a.rank, (long long)a.adapters * a.cout, bn / 2, p.aw)))
         return cudaErrorInvalidValue;
 
     static std::atomic<bool> shrink_ok[kMaxDev], expand_ok[kMaxDev];
@@ -803,8 +819,10 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     p.NT = 1;
     p.jobs = (a.rows + kBM - 1) / kBM + a.requests;
     p.splits = 1;
-    // the exchange costs 2 us, what 8 blocks take: halve runs of 16 blocks and more
-    while (p.splits < 8 && 2 * p.splits * p.jobs <= 2 * kClusterPairs && blocks >= 16 * p.splits) p.splits *= 2;
+    // the exchange costs 2 us, what 8 blocks take: halve runs of 16 blocks and more, where EXPAND's CTAs still find
+    // SMs beside SHRINK's (128 rows 4096 -> 4096, rank 64: 33 us beside it, 42 behind it)
+    const long long expand_ctas = 2 * splits * mt * ((a.cout + bn - 1) / bn);
+    while (p.splits < 8 && 2 * p.splits * p.jobs + expand_ctas <= dev->sms && blocks >= 16 * p.splits) p.splits *= 2;
     p.tmem_cols = tmem_columns(p.BN);
     size_t smem = plan_smem(p, kABytes + p.BN * kBK * 2, (size_t)p.BN * kBM * 4, 0, (size_t)dev->smem_optin,
                             (blocks + p.splits - 1) / p.splits * ((p.jobs + dev->sms - 1) / dev->sms));
