@@ -13,7 +13,9 @@
 //
 // Bound: device memory, the gradients being read twice.  The second pass walks
 // the runs backwards and starts with what the first pass read last, which L2
-// still holds.
+// still holds.  Measured (one B200): 301 bf16 tensors of 97 M elements into fp32
+// 142 us, 34 us (5.7 TB/s) of it the norm; 13 fp32 tensors of 1.1 M elements 6.5
+// us, two dependent launches.
 //
 // The squares of a vector (4 fp32, exact 8 of 16 bits) are added in fp32, the
 // vectors in fp64.  Where that sum leaves [2^-90, 2^125) the squares are formed

@@ -33,6 +33,11 @@
 // one of two tensor-memory accumulators, warps 2..5 read the finished one back,
 // finish it and store.  Every wait is bounded and gives up when another role of
 // the CTA has aborted.
+//
+// Measured (one B200): fp16 12800 rows 512 -> 512, rank 16 21 us (338 TFLOP/s,
+// bound by the chain of latencies of the two launches and by fetches from L2);
+// bf16 16111 rows 2048 -> 2048, rank 64 120 us (1.2 PFLOP/s), 97 us of it the
+// products with W.
 #include <cudaTypedefs.h>
 
 #include <type_traits>

