@@ -545,6 +545,12 @@ def dcn_add_rms_norm_forward(x: torch.Tensor, residual: Optional[torch.Tensor] =
     return AddRmsNorm(out, residual_out, out8, scale, rstd)
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_backward_workspace_bytes(rows: int, cols: int, eps: float, code: int) -> int:
+    """Workspace of a problem of these sizes (a function of them alone); 16 where they are refused."""
+    return max(16, lib().dcn_add_rms_norm_backward_workspace_bytes(ctypes.byref(DnormParams(rows, cols, eps, code, 0, 0))))
+
+
 def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
                               weight: Optional[torch.Tensor] = None, *,
                               grad_residual_out: Optional[torch.Tensor] = None, eps: float = 1e-6, grad_x=None,
@@ -571,8 +577,7 @@ def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: tor
         grad_weight = torch.empty_like(weight) if grad_weight is None else \
             _like("grad_weight", grad_weight, (cols,), dt, dev)
         if workspace is None:
-            need = lib().dcn_add_rms_norm_backward_workspace_bytes(ctypes.byref(p))
-            workspace = h.new_empty(max(need, 16), dtype=torch.uint8)
+            workspace = h.new_empty(_norm_backward_workspace_bytes(rows, cols, eps, _DTYPE_CODE[dt]), dtype=torch.uint8)
         else:
             _cuda_tensor("workspace", workspace)
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()

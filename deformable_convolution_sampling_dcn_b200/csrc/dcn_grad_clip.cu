@@ -32,8 +32,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;         // vectors of a thread in a chunk, all in flight at once
 constexpr int kChunkVecs = kThreads * kUnroll;
-constexpr int kMaxCtas = 1184;     // of the norm: 8 on each of 148 SMs, all resident
-constexpr int kScaleCtas = 888;    // of the scaling: 6 (its registers allow no more)
+// 6 CTAs on each of 148 SMs (the scaling's registers allow no more), in both passes: the second then starts where
+// the first ended in every run.
+constexpr int kMaxCtas = 888;
 
 struct Entry {
     const void *g;
@@ -279,9 +280,9 @@ template <int CAP> int fill(const ClipArgs &a, int first, Table<CAP> &t) {
     return i;
 }
 
-template <int CAP> int grid_of(const Table<CAP> &t, int most) {
+template <int CAP> int grid_of(const Table<CAP> &t) {
     const uint32_t c = t.e[t.count - 1].end_chunk;
-    return (int)(c < (uint32_t)most ? c : (uint32_t)most);
+    return (int)(c < (uint32_t)kMaxCtas ? c : (uint32_t)kMaxCtas);
 }
 
 template <int CAP> cudaError_t run(const ClipArgs &a, cudaStream_t stream) {
@@ -291,7 +292,7 @@ template <int CAP> cudaError_t run(const ClipArgs &a, cudaStream_t stream) {
     for (int i = 0; i < a.num_tensors;) {
         i = fill(a, i, t);
         if (!t.count) break;
-        const int grid = grid_of(t, kMaxCtas);
+        const int grid = grid_of(t);
         if (a.inf) grad_norm_kernel<CAP, true><<<grid, kThreads, 0, stream>>>(t, a.partial + n_partial);
         else grad_norm_kernel<CAP, false><<<grid, kThreads, 0, stream>>>(t, a.partial + n_partial);
         const cudaError_t e = cudaGetLastError();
@@ -311,7 +312,7 @@ template <int CAP> cudaError_t run(const ClipArgs &a, cudaStream_t stream) {
         // a programmatic dependent: it reads nothing that the norm kernel writes before its wait, and writes
         // nothing before it either
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)grid_of(t, kScaleCtas));
+        cfg.gridDim = dim3((unsigned)grid_of(t));
         cfg.blockDim = dim3(kThreads);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
