@@ -260,14 +260,16 @@ uint32_t chunks_of(const ClipArgs &a, int i) {
     return (uint32_t)((bytes + kChunkVecs * 16 - 1) / (kChunkVecs * 16));
 }
 
-// Fills a table with the non-empty tensors from `first` on; returns the next tensor.
+// Fills a table with the non-empty tensors from `first` on; returns the next non-empty tensor (a table is empty only
+// where there is none at all), num_tensors behind the last.
 template <int CAP> int fill(const ClipArgs &a, int first, Table<CAP> &t) {
     t.count = 0;
     uint32_t end = 0;
     int i = first;
-    for (; i < a.num_tensors && t.count < CAP; ++i) {
+    for (; i < a.num_tensors; ++i) {
         const uint32_t c = chunks_of(a, i);
         if (!c) continue;
+        if (t.count == CAP) break;
         Entry &e = t.e[t.count++];
         e.g = a.grads[i];
         e.out = a.outs ? a.outs[i] : const_cast<void *>(a.grads[i]);

@@ -101,6 +101,17 @@ def test_table_sizes(n, cuda_dev):
     check_clip(ts, gs, norm, 0.1, 1e-6, torch.float32, 5 * U)
 
 
+@pytest.mark.parametrize("n", [64, 960, 1920])
+def test_empty_tensors_behind_a_full_table(n, cuda_dev):
+    ts = tensors([(j % 7 + 1,) for j in range(n)] + [(0,)] * 5, torch.float32, 13)
+    for max_norm in (0.1, 1e6):
+        gs = [t.cuda() for t in ts]
+        norm = torch.full((), -1.0, device="cuda")
+        d.dcn_clip_grads(gs, max_norm, norm=norm)
+        check_clip(ts, gs, norm, max_norm, 1e-6, torch.float32, norm_tol(torch.float32))
+    assert abs(float(d.dcn_grad_norm([t.cuda() for t in ts])) - norm64(ts)) <= norm64(ts) * norm_tol(torch.float32)
+
+
 def test_mixed_types(cuda_dev):
     ts = [torch.randn(1000).to(dt) for dt in (torch.float32, torch.bfloat16, torch.float16) for _ in range(2)]
     gs = [t.cuda() for t in ts]
