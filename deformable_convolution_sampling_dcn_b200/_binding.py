@@ -442,6 +442,9 @@ def deform_roi_pool_forward(x, rois, offset, *, pooled=(7, 7), sampling: int = 2
     return out
 
 
+_INT32_MAX = 2 ** 31 - 1  # sizes go to the library in 32 bits
+
+
 def _launch(index: int, fn, *args) -> None:
     """fn(*args, stream) on CUDA device `index` and its current stream; raises on a non-OK status.
 
@@ -472,7 +475,17 @@ def _rows(x: torch.Tensor) -> Tuple[int, int]:
     shape = x.shape
     if not shape or shape[-1] < 1:
         raise ValueError("x must be [..., cols] with at least one column")
+    if shape[-1] > _INT32_MAX:
+        raise ValueError(f"{shape[-1]} columns exceed 32 bits")
     return x.numel() // shape[-1], shape[-1]
+
+
+def _workspace(t: torch.Tensor, index: int) -> Tuple[int, int]:
+    """Address and bytes of a caller's workspace, which has to be on CUDA device `index`."""
+    _cuda_tensor("workspace", t)
+    if t.get_device() != index:
+        raise ValueError(f"workspace is on {t.device}, expected cuda:{index}")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 class AddRmsNorm(NamedTuple):
@@ -578,9 +591,7 @@ def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: tor
             _like("grad_weight", grad_weight, (cols,), dt, dev)
         if workspace is None:
             workspace = h.new_empty(_norm_backward_workspace_bytes(rows, cols, eps, _DTYPE_CODE[dt]), dtype=torch.uint8)
-        else:
-            _cuda_tensor("workspace", workspace)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = _workspace(workspace, dev)
     elif grad_weight is not None:
         raise ValueError("grad_weight without a weight")
     _launch(dev, lib().dcn_add_rms_norm_backward, ctypes.byref(p), grad_out.data_ptr(), h.data_ptr(),
@@ -642,6 +653,8 @@ class GradList:
             self._o = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in self.out])
             self._od = (ctypes.c_int32 * max(n, 1))(*[_DTYPE_CODE[t.dtype] for t in self.out])
         self._ws = int(lib().dcn_grad_norm_workspace_bytes(n))
+        if self._ws < 0:
+            raise ValueError(f"{n} gradients are too many")
         self._protos = None
 
     def _new(self, index: int):
@@ -667,24 +680,23 @@ def _grad_call(grads, out, norm_type, norm, workspace):
     if dev is None:
         if norm is None:
             raise ValueError("no gradients: pass norm, which gives the device")
+        _cuda_tensor("norm", norm)
         dev = norm.get_device()
     if norm is not None:
         _like("norm", norm, (), torch.float32, dev)
-    if workspace is not None:
-        _cuda_tensor("workspace", workspace)
     if norm is None or workspace is None:
         n, w = grads._new(dev)
         norm, workspace = n if norm is None else norm, w if workspace is None else workspace
-    return grads, dev, norm, workspace, workspace.numel() * workspace.element_size()
+    return (grads, dev, norm) + _workspace(workspace, dev)
 
 
 def dcn_grad_norm(grads, *, norm_type: float = 2.0, norm=None, workspace=None) -> torch.Tensor:
     """The 2-norm (or largest magnitude, norm_type inf) of all gradients together, an fp32 scalar on the
     device; grads is a GradList or a sequence of tensors.  See dcn_b200.h."""
-    grads, dev, norm, workspace, nbytes = _grad_call(grads, None, norm_type, norm, workspace)
+    grads, dev, norm, ws_ptr, ws_bytes = _grad_call(grads, None, norm_type, norm, workspace)
     p = DclipParams(grads.count, _NORM_KIND[norm_type], 0.0, 1.0)
     _launch(dev, lib().dcn_grad_norm, ctypes.byref(p), grads._g, grads._n, grads._d, norm.data_ptr(),
-            workspace.data_ptr(), nbytes)
+            ws_ptr, ws_bytes)
     return norm
 
 
@@ -692,10 +704,10 @@ def dcn_clip_grads(grads, max_norm: float, *, norm_type: float = 2.0, eps: float
                    workspace=None) -> torch.Tensor:
     """Scales all gradients by min(1, max_norm / (norm + eps)), in place or into `out`, and returns the norm
     before that (fp32 scalar on the device; nothing synchronises).  See dcn_b200.h."""
-    grads, dev, norm, workspace, nbytes = _grad_call(grads, out, norm_type, norm, workspace)
+    grads, dev, norm, ws_ptr, ws_bytes = _grad_call(grads, out, norm_type, norm, workspace)
     p = DclipParams(grads.count, _NORM_KIND[norm_type], max_norm, eps)
     _launch(dev, lib().dcn_clip_grads, ctypes.byref(p), grads._g, grads._n, grads._d, grads._o, grads._od,
-            norm.data_ptr(), workspace.data_ptr(), nbytes)
+            norm.data_ptr(), ws_ptr, ws_bytes)
     return norm
 
 
@@ -726,6 +738,8 @@ def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optio
     if len(ws) != 2 or len(sa) != 3 or len(sr) != 1:
         raise ValueError("weight must be [cout, cin], a [adapters, rank, cin], request_adapter [requests]")
     cout, na, rank, nr = ws[0], sa[0], sa[1], sr[0]
+    if max(cout, na, rank, nr) > _INT32_MAX:
+        raise ValueError("a size exceeds 32 bits")
     _like("weight", weight, (cout, cin), dt, dev)
     if bias is not None:
         _like("bias", bias, (cout,), dt, dev)
@@ -745,10 +759,9 @@ def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optio
     L = lib()
     if workspace is None:
         workspace = x.new_empty(_adapters_workspace_bytes(*sizes), dtype=torch.uint8)
-    else:
-        _cuda_tensor("workspace", workspace)
+    ws_ptr, ws_bytes = _workspace(workspace, dev)
     _launch(dev, L.dcn_proj_adapters_forward, ctypes.byref(p), x.data_ptr(), weight.data_ptr(),
             None if bias is None else bias.data_ptr(), a.data_ptr(), b.data_ptr(),
             None if scale is None else scale.data_ptr(), request_start.data_ptr(), request_adapter.data_ptr(),
-            out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            out.data_ptr(), ws_ptr, ws_bytes)
     return out

@@ -493,6 +493,7 @@ dcn_status dcn_add_rms_norm_forward(const dnorm_params *p, const void *x, const 
     if (q != (out8 != nullptr) || q != (scale != nullptr))
         return fail(DCN_ERR_NULL, "out8 and scale are given exactly with an 8-bit output");
     if (!out && !q) return fail(DCN_ERR_NULL, "out is required without an 8-bit output");
+    if (out && out == residual_out) return fail(DCN_ERR_UNSUPPORTED, "out and residual_out are the same buffer");
     const size_t es = dtype_size(p->dtype);
     if (!aligned(x, es) || !aligned(residual, es) || !aligned(weight, es) || !aligned(residual_out, es) ||
         !aligned(out, es) || !aligned(scale, 4) || !aligned(rstd, 4))

@@ -304,7 +304,8 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, CTAS)
         const float rstd = next_rstd;
         next_rstd = r + step < a.rows ? __ldg(a.rstd + r + step) : 0.0f;
         if (!mbar_wait_bounded(full + 8 * s, phase, kRowWaitNs)) {
-            if (t == 0) atomicOr(err, kDevErrTmaTimeout);
+            if (t == 0) give_up(full, s, phase, slots, err);
+            __syncwarp();
             break;
         }
         if (r < a.rows) {

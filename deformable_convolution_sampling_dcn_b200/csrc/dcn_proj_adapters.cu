@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *sm.tmem_slot;
     if (blockIdx.x == 0 && warp >= 2)
-        for (int i = threadIdx.x - 64; i < p.requests; i += 128) report_bad_adapter(req.which[i], p.adapters, p.err);
+        for (int i = threadIdx.x - 64; i < p.requests; i += 128)
+            if (req.at(i + 1) > req.at(i)) report_bad_adapter(req.which[i], p.adapters, p.err);
     const int blocks = (p.cin + kBK - 1) / kBK;
     // this CTA's part of the contraction and its cluster's job
     const int split = p.splits > 1 ? (int)cta_rank() : 0;

@@ -305,8 +305,9 @@ dcn_status deform_roi_pool_forward(const droi_params *p, const void *x, const fl
  * Rows before request_start[0] and from request_start[num_requests] on (a
  * padded batch) are left as they were.  Values of request_start are cut to
  * [0, rows]; an order that is not ascending gives wrong values but no access
- * out of range.  An adapter outside [-1, num_adapters) counts as none and sets
- * bit 1 of the device error word (dcn_take_device_error).
+ * out of range.  An adapter outside [-1, num_adapters) counts as none and, where
+ * its request owns a row, sets bit 1 of the device error word
+ * (dcn_take_device_error).  out and workspace must not overlap any input.
  * Sums are fp32.  With at most 64 rows A[a] x stays in fp32; with more it may be
  * (and above 256 rows is) scaled and rounded once to the storage dtype, as an
  * operand of the second tensor-core product.  Values of one row do not depend
@@ -357,8 +358,10 @@ int64_t dcn_proj_adapters_workspace_bytes(const dadapt_params *p);
  * residual_out is given exactly when residual is, out8 and scale exactly when
  * quant is not DCN_QUANT_NONE; out may be NULL when out8 is given.
  * residual_out and out may each be the buffer of x or of residual (a row is
- * read before any of it is written), but not the same one; buffers that
- * overlap in any other way give wrong results.
+ * read before any of it is written), but not the same one
+ * (DCN_ERR_UNSUPPORTED); buffers that overlap in any other way give wrong
+ * results.  The sum of squares is fp32: a row whose sum leaves its range
+ * (values of 1e19, say) has rstd 0.
  * A NaN or infinite h makes the statistics of its row NaN or rstd 0; a scale
  * over a NaN is NaN, so the dequantised values are too (e4m3 codes of a NaN are
  * NaN; int8 codes under a NaN scale mean nothing).
@@ -412,10 +415,11 @@ int64_t dcn_add_rms_norm_backward_workspace_bytes(const dnorm_params *p);
  * grads, outs, numel and the dtype arrays are HOST arrays of num_tensors
  * entries, read during the call (a captured graph keeps their contents); the
  * pointers in them are device pointers to dense buffers aligned to their
- * element, of at most 2^40 elements in all.  outs NULL: in place.  Otherwise out_dtypes names the type of each
- * out buffer (an fp32 master gradient of a 16-bit gradient, say), and a buffer
- * may be its own gradient's.  Buffers must not overlap otherwise, nor occur
- * twice.  A tensor with numel 0 is skipped (its pointers may be NULL).
+ * element, of at most 2^40 elements in at most 2^20 tensors.  outs NULL: in
+ * place.  Otherwise out_dtypes names the type of each out buffer (an fp32 master
+ * gradient of a 16-bit gradient, say), and a buffer may be its own gradient's in
+ * the same type.  Buffers must not overlap otherwise, nor occur twice.  A tensor
+ * with numel 0 is skipped (its pointers may be NULL).
  * *norm (device, fp32) receives N; no element at all gives 0.  A NaN gradient
  * gives a NaN norm and NaN gradients, an infinite one an infinite norm and
  * c = 0.  In place with c = 1 nothing is written.  The squares of 16 bytes of
@@ -429,8 +433,8 @@ typedef enum { DCN_NORM_L2 = 0, DCN_NORM_MAX = 1 } dcn_norm_kind;
 typedef struct {
     int32_t num_tensors;
     int32_t kind;     /* dcn_norm_kind */
-    float max_norm;   /* >= 0 (dcn_clip_grads only) */
-    float eps;        /* > 0 (dcn_clip_grads only) */
+    float max_norm;   /* finite, >= 0 (dcn_clip_grads only) */
+    float eps;        /* finite, > 0 (dcn_clip_grads only) */
 } dclip_params;
 
 dcn_status dcn_grad_norm(const dclip_params *p, const void *const *grads, const int64_t *numel,
@@ -440,7 +444,7 @@ dcn_status dcn_clip_grads(const dclip_params *p, const void *const *grads, const
                           const int32_t *dtypes, void *const *outs, const int32_t *out_dtypes, float *norm,
                           void *workspace, int64_t workspace_bytes, dcn_stream_t stream);
 
-/* Workspace bytes of the two calls above; -1 for a negative count. */
+/* Workspace bytes of the two calls above; -1 for a count outside [0, 2^20]. */
 int64_t dcn_grad_norm_workspace_bytes(int32_t num_tensors);
 
 /* Static, human-readable name of a status. */

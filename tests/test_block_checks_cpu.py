@@ -152,3 +152,29 @@ def test_adapter_pointers(lib):
     assert proj(lib, adapt(rows=0), x=None, out=None) == B.DCN_OK
     assert proj(lib, adapt(num_requests=0), x=None) == B.DCN_OK
     assert lib.dcn_proj_adapters_forward(None, 16, 16, 16, 16, 16, 16, 16, 16, 16, 16, 1 << 20, None) == B.DCN_ERR_NULL
+
+
+def test_out_is_not_the_new_residual(lib):
+    assert fwd(lib, norm(), res=32, res_out=16, out=16) == B.DCN_ERR_UNSUPPORTED
+
+
+def test_python_refusals_without_a_gpu(lib):
+    import torch
+    # an empty list takes its device from the norm, which has to be on one
+    for call in (lambda n: B.dcn_grad_norm([], norm=n), lambda n: B.dcn_clip_grads([], 1.0, norm=n)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call(torch.zeros(()))
+    # sizes that would not fit the library's 32 bits
+    with pytest.raises(ValueError, match="32 bits"):
+        B._rows(torch.empty(0, 2 ** 32 + 8))
+    assert B._rows(torch.empty(0, 2 ** 31 - 1)) == (0, 2 ** 31 - 1)
+    # a workspace on another device than the tensors
+    class Elsewhere(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+    other = torch.zeros(64, dtype=torch.uint8).as_subclass(Elsewhere)
+    assert B._workspace(other, 1) == (other.data_ptr(), 64)
+    with pytest.raises(ValueError, match="workspace is on"):
+        B._workspace(other, 0)

@@ -189,6 +189,16 @@ def test_bad_adapter_index_is_reported(cuda_dev):
         assert d._binding.take_device_error() == 0
 
 
+def test_adapter_of_an_empty_request_is_not_looked_at(cuda_dev):
+    for lens in ([3, 0, 4], [300, 0, 90]):
+        s = make(lens, [0, 9, 1], 64, 64, 16, 2, "bf16", 81)
+        y = call(s)
+        torch.cuda.synchronize()
+        assert d._binding.take_device_error() == 0
+        want, tol = definition(s)
+        assert ((y.double().cpu() - want).abs() <= tol).all()
+
+
 def test_tables_out_of_range_stay_in_bounds(cuda_dev):
     """Starts outside [0, rows]: cut off; the rows of the well-formed requests are right."""
     for rows in (50, 400):
