@@ -74,7 +74,10 @@ class DeformAggFunction(torch.autograd.Function):
 
 class AddRmsNormFunction(torch.autograd.Function):
     """autograd over dcn_add_rms_norm_forward/backward: (out, h) of x, residual and weight, all
-    differentiable; residual and weight may be None, h is x + residual (x itself without one)."""
+    differentiable; residual and weight may be None, h is x + residual (x itself without one).
+
+    Inside a CUDA graph capture, let no uncaptured autograd graph of the same leaves live: PyTorch would run their
+    gradients' accumulation on the stream of that graph and end the capture with an error."""
 
     @staticmethod
     def forward(ctx, x, residual, weight, eps: float = 1e-6):

@@ -347,8 +347,8 @@ int64_t dcn_proj_adapters_workspace_bytes(const dadapt_params *p);
  * with the maximum over the row (group = 0) or over each 128 neighbouring
  * columns (group = 128; the last group of a row may be shorter), top = 448
  * (DCN_QUANT_E4M3, saturating) or 127 (DCN_QUANT_INT8); out8 * scale is y up
- * to the 8-bit rounding.  h is rounded to the storage type before the norm is
- * taken of it; everything after that is fp32 and rounded once, 8-bit codes
+ * to the 8-bit rounding.  h is the fp32 sum, rounded to the storage type before
+ * the norm is taken of it; everything after that is fp32 and rounded once, 8-bit codes
  * from the fp32 value.
  *   x, residual, residual_out, out  [rows, cols]  storage dtype
  *   weight                          [cols]        storage dtype, or NULL

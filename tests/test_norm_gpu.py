@@ -333,6 +333,28 @@ def test_autograd_forms(cuda_dev):
     assert x.grad is not None and w.grad is not None
 
 
+def test_autograd_captured(cuda_dev):
+    x, r, w = gpu(*inputs(200, 256, torch.bfloat16, 21))
+    gy, gh = torch.randn_like(x), torch.randn_like(x)
+    leaves = [t.clone().requires_grad_() for t in (x, r, w)]
+
+    def step():
+        return torch.autograd.grad(d.AddRmsNormFunction.apply(*leaves, EPS), leaves, (gy, gh))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        want = [t.clone() for t in step()]
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for t in got:
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_empty_and_streams_and_graph(cuda_dev):
     w = torch.ones(64, device="cuda")
     o = d.dcn_add_rms_norm_forward(torch.empty(0, 64, device="cuda"), weight=w, quant="int8", save_rstd=True)
@@ -369,6 +391,28 @@ def test_empty_and_streams_and_graph(cuda_dev):
     assert torch.equal(graphs[0][3][0], wb[0]) and torch.equal(graphs[0][3][1], wb[1])
     other = d.dcn_add_rms_norm_forward(x * 2, r, w)
     assert torch.equal(graphs[1][2].out, other.out)
+
+
+@pytest.mark.parametrize("cols", [64, 512, 4096, 4099])
+def test_more_than_32_bit_elements(cols, cuda_dev):
+    """Offsets are 64-bit: the last rows of more than 2^32 elements give what they give by themselves."""
+    rows = (1 << 32) // cols + 70
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(40, cols, dtype=torch.bfloat16, device="cuda")
+    x[-40:] = tail
+    w = torch.rand(cols, dtype=torch.bfloat16, device="cuda")
+    o = d.dcn_add_rms_norm_forward(x, None, w, quant="int8", keep_out=True, save_rstd=True)
+    want = d.dcn_add_rms_norm_forward(tail, None, w, quant="int8", keep_out=True, save_rstd=True)
+    for a, b in zip(o, want):
+        assert (a is None and b is None) or torch.equal(a[-40:], b)
+    assert not o.out[:-40].any() and not o.out8[:-40].any()
+    del o
+    gx, gw = d.dcn_add_rms_norm_backward(x, x, torch.cat([torch.ones(rows - 40, device="cuda"), want.rstd]), w)
+    gx40, gw40 = d.dcn_add_rms_norm_backward(tail, tail, want.rstd, w)
+    assert torch.equal(gx[-40:], gx40) and not gx[:-40].any()
+    # the weight gradient adds 40 rows' products and zeros, in another order
+    mag = (tail.double() ** 2 * want.rstd.double()[:, None]).abs().sum(0)
+    assert ((gw.double() - gw40.double()).abs() <= mag * 2 * 50 * U + gw40.double().abs() * 2 * half_step(w.dtype)).all()
 
 
 def test_binding_refusals(cuda_dev):

@@ -199,6 +199,31 @@ def test_adapter_of_an_empty_request_is_not_looked_at(cuda_dev):
         assert ((y.double().cpu() - want).abs() <= tol).all()
 
 
+def test_more_than_32_bit_elements(cuda_dev):
+    """Offsets are 64-bit: the last rows of a batch, and the last adapter, of more than 2^32 elements."""
+    s = make([70, 200], [0, 1], 512, 512, 16, 2, "bf16", 82)
+    rows = (1 << 32) // 512 + 700
+    x = torch.zeros(rows, 512, dtype=torch.bfloat16, device="cuda")
+    x[-270:] = s["x"].cuda()
+    big = dict(s, x=x, start=torch.tensor([0, rows - 270, rows - 200, rows], dtype=torch.int32),
+               which=torch.tensor([-1, 0, 1], dtype=torch.int32))
+    y = call(big)
+    want, tol = definition(s)
+    assert ((y[-270:].double().cpu() - want).abs() <= tol).all()
+    assert (y[:-270] == s["bias"].cuda()).all()
+    del x, y, big
+    n = (1 << 32) // (1024 * 32) + 3
+    for lens in ([5, 7], [200, 100]):
+        s = make(lens, [1, 0], 1024, 1024, 32, 2, "bf16", 83)
+        want, tol = definition(s)
+        a = torch.zeros(n, 32, 1024, dtype=torch.bfloat16, device="cuda")
+        b = torch.zeros(n, 1024, 32, dtype=torch.bfloat16, device="cuda")
+        scale = torch.zeros(n, device="cuda")
+        a[-2:], b[-2:], scale[-2:] = s["a"].cuda(), s["b"].cuda(), s["scale"].cuda()
+        y = call(dict(s, a=a, b=b, scale=scale, which=s["which"] + (n - 2)))
+        assert ((y.double().cpu() - want).abs() <= tol).all()
+
+
 def test_tables_out_of_range_stay_in_bounds(cuda_dev):
     """Starts outside [0, rows]: cut off; the rows of the well-formed requests are right."""
     for rows in (50, 400):
