@@ -4,11 +4,19 @@
 // consecutive vectors: loads and stores are coalesced, and 128 neighbouring
 // columns sit in 16 (16-bit storage) or 32 (fp32) neighbouring lanes.
 //
-// A team is 8 lanes, a warp, or the whole CTA (TPR = 0).  Rows whose byte
-// length or base address is not a multiple of 16 go by elements: thread t holds
+// A team is 8 lanes, a warp, or the whole CTA (TPR = 0).
+//
+// Rows that do not start on 16 bytes are held by the vectors of the aligned grid
+// (SHIFT): vector v of a row has the columns v * VEC - shift .. + VEC - 1, where
+// shift, the elements by which the row's start is past a 16-byte boundary, is
+// the same in all tensors.  The vectors at a row's two ends also hold elements
+// of its neighbours: they are read, not used and not written.  A team's rows are
+// a multiple of VEC apart, so its shift, and with it the columns that a thread
+// holds, stays the same over all of them.
+//
+// Tensors that are out of step with one another go by elements: thread t holds
 // the columns t, t + TPR, t + 2*TPR, ..., so a warp's accesses are 64 or 128
-// neighbouring bytes (the vector mapping with accesses by elements measured
-// three times slower: its warps touch 16 sectors an access).
+// neighbouring bytes.
 #pragma once
 
 #include "dcn_common.cuh"
@@ -82,6 +90,64 @@ template <typename T> __device__ __forceinline__ uint4 load_cols(const T *row, i
 
 template <typename T> __device__ __forceinline__ void store_cols(T *row, int c, int cols, const uint4 &v) {
     if (c < cols) *reinterpret_cast<uint4 *>(row + c) = v;
+}
+
+// Elements by which the rows r0, r0 + a multiple of VEC, ... of a tensor start past a 16-byte boundary.
+template <typename T> __device__ __forceinline__ int shift_of_rows(const void *base, long long r0, int cols) {
+    constexpr int VEC = Storage<T>::kVec;
+    return (int)(((reinterpret_cast<uintptr_t>(base) % 16) / sizeof(T) + (unsigned long long)r0 * cols) % VEC);
+}
+
+// The same for a vector of the aligned grid at columns c .. of the row at `off` in a tensor of `total` elements:
+// whole, neighbours included, where it lies within the tensor.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ uint4 load_vec(const T *base, long long off, int c, int cols, long long total) {
+    constexpr int VEC = Storage<T>::kVec;
+    if (!SHIFT) return load_cols<T>(base + off, c, cols);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c >= cols) return v;
+    if (off + c >= 0 && off + c + VEC <= total) return *reinterpret_cast<const uint4 *>(base + off + c);
+    T e[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) e[j] = c + j >= 0 && c + j < cols ? base[off + c + j] : from_f32<T>(0.0f);
+    memcpy(&v, e, 16);
+    return v;
+}
+
+// A vector at any alignment, zeros outside the row.
+template <typename T> __device__ __forceinline__ uint4 load_any(const T *row, int c, int cols) {
+    constexpr int VEC = Storage<T>::kVec;
+    T e[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) e[j] = c + j >= 0 && c + j < cols ? row[c + j] : from_f32<T>(0.0f);
+    uint4 v;
+    memcpy(&v, e, 16);
+    return v;
+}
+
+// Only the row's own elements are written.
+template <typename T, bool SHIFT> __device__ __forceinline__ void store_vec(T *row, int c, int cols, const uint4 &v) {
+    constexpr int VEC = Storage<T>::kVec;
+    if (!SHIFT) {
+        store_cols<T>(row, c, cols, v);
+    } else if (c >= 0 && c + VEC <= cols) {
+        *reinterpret_cast<uint4 *>(row + c) = v;
+    } else if (c < cols) {
+        T e[VEC];
+        memcpy(e, &v, 16);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (c + j >= 0 && c + j < cols) row[c + j] = e[j];
+    }
+}
+
+// Zeros where a vector reaches out of its row.
+template <bool SHIFT, int VEC> __device__ __forceinline__ void clear_outside(float *f, int c, int cols) {
+    if (SHIFT && (c < 0 || c + VEC > cols)) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (c + j < 0 || c + j >= cols) f[j] = 0.0f;
+    }
 }
 
 // By elements: value k of a thread is column k * tpr + t.

@@ -29,27 +29,60 @@ constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126: 1 / s stays finite, an 
 // Four values to four 8-bit codes, in memory order.  int8 rounds by adding
 // 1.5 * 2^23 in the fused product: the low byte of the sum is the rounded value
 // (|y * inv| <= 127 * (1 + 2^-22)).
-__device__ __forceinline__ uint32_t pack8(const float *y, float inv, int quant) {
+__device__ __forceinline__ uint32_t pack8(const float *y, const float *inv, int quant) {
     if (quant == kQuantE4M3) {
-        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv), __NV_SATFINITE,
-                                                                 __NV_E4M3);
-        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv, y[3] * inv), __NV_SATFINITE,
-                                                                 __NV_E4M3);
+        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv[0], y[1] * inv[1]),
+                                                                 __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv[2], y[3] * inv[3]),
+                                                                 __NV_SATFINITE, __NV_E4M3);
         return (uint32_t)lo | ((uint32_t)hi << 16);
     }
     uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(fmaf(y[i], inv, 12582912.0f));
+    for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(fmaf(y[i], inv[i], 12582912.0f));
     return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
 }
 
-// The codes of a thread's vector at an address that is a multiple of VEC.
-template <int VEC>
-__device__ __forceinline__ void store_codes(unsigned char *dst, const float *y, float inv, int quant) {
-    if constexpr (VEC == 8)
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack8(y, inv, quant), pack8(y + 4, inv, quant));
-    else
-        *reinterpret_cast<uint32_t *>(dst) = pack8(y, inv, quant);
+// The codes of a thread's vector at columns c ..; row + c is a multiple of VEC.  The first `lo` elements take the
+// factor `before`, the others `inv`.
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ void store_codes(unsigned char *row, int c, int cols, const float *y, float inv, float before,
+                                            int lo, int quant) {
+    if (c >= cols) return;
+    float f[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = SHIFT && j < lo ? before : inv;
+    uint32_t q[VEC / 4];
+#pragma unroll
+    for (int k = 0; k < VEC / 4; ++k) q[k] = pack8(y + 4 * k, f + 4 * k, quant);
+    if (!SHIFT || (c >= 0 && c + VEC <= cols)) {
+        if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(row + c) = make_uint2(q[0], q[1]);
+        else *reinterpret_cast<uint32_t *>(row + c) = q[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (c + j >= 0 && c + j < cols) row[c + j] = (unsigned char)(q[j / 4] >> (8 * (j % 4)));
+    }
+}
+
+// Largest magnitude of a vector's elements in the row: of those from `lo` on, and into `before` of those ahead.
+template <int VEC, bool SHIFT>
+__device__ __forceinline__ float vec_max(const float *y, int c, int cols, int lo, float &before) {
+    float m = 0.0f;
+    before = 0.0f;
+    if (c >= cols) return m;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        // elements outside the row hold 0 * rstd * 0, which is NaN where rstd is
+        if (SHIFT && (c + j < 0 || c + j >= cols)) continue;
+        if (SHIFT && j < lo) before = max_nan(before, fabsf(y[j]));
+        else m = max_nan(m, fabsf(y[j]));
+    }
+    return m;
+}
+
+__device__ __forceinline__ float scale_of(float amax, int quant) {
+    return max_nan(amax / (quant == kQuantE4M3 ? 448.0f : 127.0f), kScaleMin);
 }
 
 constexpr int kMaxSlots = 8;
@@ -61,19 +94,22 @@ constexpr int kMaxSlots = 8;
 constexpr int kTeamThreads = 256;
 constexpr int ctas_per_sm(int c) { return c <= 8 ? 4 : c <= 16 ? 3 : 2; }
 
-template <typename T, int TPR, int NV, bool QUANT>
+template <typename T, int TPR, int NV, bool QUANT, bool SHIFT>
 __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVec))
     norm_forward_kernel(const NormArgs a) {
     constexpr int VEC = Storage<T>::kVec;
     constexpr bool AHEAD = NV * VEC <= 16;
-    constexpr int tpr = TPR, teams = kTeamThreads / TPR;
+    constexpr int tpr = TPR, teams = kTeamThreads / TPR;  // teams: a multiple of VEC
     const int t = (int)threadIdx.x % TPR, team = (int)threadIdx.x / TPR;
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
     const T *weight = static_cast<const T *>(a.weight);
+    const long long total = a.rows * a.cols;
+    const int sh = SHIFT ? shift_of_rows<T>(a.x, (long long)blockIdx.x * teams + team, a.cols) : 0;
+    auto column = [&](int i) { return (t + i * tpr) * VEC - sh; };
     uint4 w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (weight) w[i] = load_cols<T>(weight, (t + i * tpr) * VEC, a.cols);
+        if (weight) w[i] = SHIFT ? load_any<T>(weight, column(i), a.cols) : load_cols<T>(weight, column(i), a.cols);
 
     uint4 xn[NV], rn[NV];
     auto fetch = [&](long long r) {
@@ -81,8 +117,8 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
         const int cols = r < a.rows ? a.cols : 0;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            xn[i] = load_cols<T>(x + off, (t + i * tpr) * VEC, cols);
-            if (res) rn[i] = load_cols<T>(res + off, (t + i * tpr) * VEC, cols);
+            xn[i] = load_vec<T, SHIFT>(x, off, column(i), cols, total);
+            if (res) rn[i] = load_vec<T, SHIFT>(res, off, column(i), cols, total);
         }
     };
     const long long step = (long long)gridDim.x * teams;
@@ -105,9 +141,10 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) y[i][j] += g[j];
                 const uint4 h = pack16<T>(y[i]);
-                store_cols<T>(static_cast<T *>(a.residual_out) + off, (t + i * tpr) * VEC, cols, h);
+                store_vec<T, SHIFT>(static_cast<T *>(a.residual_out) + off, column(i), cols, h);
                 unpack16<T>(h, y[i]);
             }
+            clear_outside<SHIFT, VEC>(y[i], column(i), cols);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) ss = fmaf(y[i][j], y[i][j], ss);
         }
@@ -127,41 +164,48 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
                 for (int j = 0; j < VEC; ++j) y[i][j] *= rstd;
             }
             if (!QUANT || a.out)
-                store_cols<T>(static_cast<T *>(a.out) + off, (t + i * tpr) * VEC, cols, pack16<T>(y[i]));
+                store_vec<T, SHIFT>(static_cast<T *>(a.out) + off, column(i), cols, pack16<T>(y[i]));
         }
         if constexpr (QUANT) {
-            float amax = 0.0f, gmax[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                gmax[i] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    // columns past the row hold 0 * rstd * 0, which is NaN where rstd is
-                    gmax[i] = max_nan(gmax[i], (t + i * tpr) * VEC < cols ? fabsf(y[i][j]) : 0.0f);
-                }
-                amax = max_nan(amax, gmax[i]);
-            }
-            const float top = a.quant == kQuantE4M3 ? 448.0f : 127.0f;
             // lanes that share 128 columns; a team narrower than that holds rows of at most 128 columns
             constexpr int GL = 128 / VEC;
             const bool grouped = a.group != 0 && TPR >= GL;
-            float s = 0.0f, inv = 0.0f;
+            // of shifted vectors the first of a group also holds the end of the group before
+            float gmax[NV], before[NV], amax = 0.0f, s[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                gmax[i] = vec_max<VEC, SHIFT>(y[i], column(i), cols, grouped && t % GL == 0 ? sh : 0, before[i]);
+                amax = max_nan(amax, gmax[i]);
+            }
             if (!grouped) {
-                s = max_nan(lanes_reduce<MaxOp, TPR>(amax) / top, kScaleMin);
-                inv = 1.0f / s;
-                if (t == 0 && live) a.scale[r] = s;
+                s[0] = scale_of(lanes_reduce<MaxOp, TPR>(amax), a.quant);
+                if (t == 0 && live) a.scale[r] = s[0];
+#pragma unroll
+                for (int i = 1; i < NV; ++i) s[i] = s[0];
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    float m = lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]);
+                    if (SHIFT) {
+                        const float here = __shfl_sync(0xffffffffu, before[i], 16);
+                        const float next = i + 1 < NV ? __shfl_sync(0xffffffffu, before[i + 1 < NV ? i + 1 : i], 0) : 0.0f;
+                        m = max_nan(m, GL == 16 && t < 16 ? here : next);
+                    }
+                    s[i] = scale_of(m, a.quant);
+                    const int v = t + i * tpr;
+                    if (v % GL == 0 && v * VEC < cols) a.scale[r * a.groups + v / GL] = s[i];
+                }
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int v = t + i * tpr, c = v * VEC;
-                if (grouped) {
-                    s = max_nan(lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]) / top, kScaleMin);
-                    inv = 1.0f / s;
-                    if (v % GL == 0 && c < cols) a.scale[r * a.groups + c / 128] = s;
+                float inv0 = 0.0f;
+                if (SHIFT && grouped) {
+                    const float here = __shfl_sync(0xffffffffu, s[i], 15);
+                    const float last = __shfl_sync(0xffffffffu, s[i ? i - 1 : 0], 31);
+                    if (t % GL == 0) inv0 = 1.0f / (GL == 16 && t == 16 ? here : last);
                 }
-                if (c < cols) {
-                    store_codes<VEC>(static_cast<unsigned char *>(a.out8) + off + c, y[i], inv, a.quant);
-                }
+                store_codes<VEC, SHIFT>(static_cast<unsigned char *>(a.out8) + off, column(i), cols, y[i], 1.0f / s[i],
+                                        inv0, grouped && t % GL == 0 ? sh : 0, a.quant);
             }
         }
     }
@@ -170,35 +214,44 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
 // Rows wider than a warp team holds, 16-byte aligned: a CTA of 16 columns a
 // thread per row, the rows staged by bulk copies (bf16 2047 x 4096 to int8: 16.8
 // us with the next row's loads in registers, 13.8 us staged).
-template <typename T, bool QUANT>
+template <typename T, bool QUANT, bool SHIFT>
 __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormArgs a, int slots, unsigned int *err) {
     constexpr int VEC = Storage<T>::kVec, NV = 16 / VEC, GL = 128 / VEC;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ float red[64];
     __shared__ __align__(8) uint64_t bars[kMaxSlots];
+    // shifted rows: maxima of the groups (bits of values >= 0), two rows' sets
+    __shared__ int gmax_s[2][QUANT && SHIFT ? 128 : 1];
     const int t = threadIdx.x, tpr = blockDim.x;
-    const uint32_t row_bytes = (uint32_t)a.cols * sizeof(T), slot_bytes = a.residual ? 2 * row_bytes : row_bytes;
     const T *weight = static_cast<const T *>(a.weight);
-    int turn = 0;
+    const long long step = gridDim.x, total = a.rows * a.cols;  // SHIFT: step is a multiple of VEC, or no CTA has two rows
+    const int sh = SHIFT ? shift_of_rows<T>(a.x, blockIdx.x, a.cols) : 0, nvec = (a.cols + sh + VEC - 1) / VEC;
+    // a row in the ring: its vectors of the aligned grid, without one that reaches out of the tensor at either end
+    const uint32_t row_bytes = (uint32_t)nvec * 16, slot_bytes = a.residual ? 2 * row_bytes : row_bytes;
+    int turn = 0, set = 0;
     if (t == 0) {
         for (int i = 0; i < slots; ++i) mbar_init(smem_u32(bars + i), 1);
         fence_mbar_init();
     }
+    if (QUANT && SHIFT)
+        for (int i = t; i < 256; i += tpr) gmax_s[i / 128][i % 128] = 0;
     __syncthreads();
     auto stage = [&](long long r, int s) {  // by thread 0
         if (r >= a.rows) return;
-        const uint32_t bar = smem_u32(bars + s), dst = smem_u32(ring) + s * slot_bytes;
-        mbar_arrive_expect_tx(bar, slot_bytes);
-        bulk_load(dst, static_cast<const T *>(a.x) + r * a.cols, row_bytes, bar);
-        if (a.residual) bulk_load(dst + row_bytes, static_cast<const T *>(a.residual) + r * a.cols, row_bytes, bar);
+        const long long e = r * a.cols - sh;
+        const int skip = SHIFT && e < 0, n = nvec - skip - (SHIFT && e + (long long)nvec * VEC > total);
+        const uint32_t bar = smem_u32(bars + s), dst = smem_u32(ring) + s * slot_bytes + 16 * skip;
+        mbar_arrive_expect_tx(bar, (a.residual ? 32u : 16u) * n);
+        bulk_load(dst, static_cast<const T *>(a.x) + e + skip * VEC, 16u * n, bar);
+        if (a.residual) bulk_load(dst + row_bytes, static_cast<const T *>(a.residual) + e + skip * VEC, 16u * n, bar);
     };
-    const long long step = gridDim.x;
     if (t == 0)
         for (int i = 0; i < slots; ++i) stage(blockIdx.x + i * step, i);
+    auto column = [&](int i) { return (t + i * tpr) * VEC - sh; };
     uint4 w[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if (weight) w[i] = load_cols<T>(weight, (t + i * tpr) * VEC, a.cols);
+        if (weight) w[i] = SHIFT ? load_any<T>(weight, column(i), a.cols) : load_cols<T>(weight, column(i), a.cols);
 
     int s = 0;
     uint32_t phase = 0;
@@ -209,21 +262,27 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
             return;
         }
         const unsigned char *slot = ring + s * slot_bytes;
+        auto staged = [&](const unsigned char *row, const void *tensor, int c) {
+            if (SHIFT && c < a.cols && (off + c < 0 || off + c + VEC > total))
+                return load_any<T>(static_cast<const T *>(tensor) + off, c, a.cols);
+            return load_cols<T>(reinterpret_cast<const T *>(row) + sh, c, a.cols);
+        };
         float y[NV][VEC];
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * tpr) * VEC;
-            unpack16<T>(load_cols<T>(reinterpret_cast<const T *>(slot), c, a.cols), y[i]);
+            const int c = column(i);
+            unpack16<T>(staged(slot, a.x, c), y[i]);
             if (a.residual) {
                 float g[VEC];
-                unpack16<T>(load_cols<T>(reinterpret_cast<const T *>(slot + row_bytes), c, a.cols), g);
+                unpack16<T>(staged(slot + row_bytes, a.residual, c), g);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) y[i][j] += g[j];
                 const uint4 h = pack16<T>(y[i]);
-                store_cols<T>(static_cast<T *>(a.residual_out) + off, c, a.cols, h);
+                store_vec<T, SHIFT>(static_cast<T *>(a.residual_out) + off, c, a.cols, h);
                 unpack16<T>(h, y[i]);
             }
+            clear_outside<SHIFT, VEC>(y[i], c, a.cols);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) ss = fmaf(y[i][j], y[i][j], ss);
         }
@@ -235,10 +294,11 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
         }
         const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
         if (a.rstd && t == 0) a.rstd[r] = rstd;
-        float gmax[NV], amax = 0.0f;
+        float gmax[NV], before[NV], amax = 0.0f;
+        const int lo = a.group && t % GL == 0 ? sh : 0;  // tpr is a multiple of GL: the same for all vectors
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (t + i * tpr) * VEC;
+            const int c = column(i);
             if (weight) {
                 float g[VEC];
                 unpack16<T>(w[i], g);
@@ -248,39 +308,50 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) y[i][j] *= rstd;
             }
-            if (!QUANT || a.out) store_cols<T>(static_cast<T *>(a.out) + off, c, a.cols, pack16<T>(y[i]));
+            if (!QUANT || a.out) store_vec<T, SHIFT>(static_cast<T *>(a.out) + off, c, a.cols, pack16<T>(y[i]));
             if (QUANT) {
-                gmax[i] = 0.0f;
-                if (c < a.cols) {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) gmax[i] = max_nan(gmax[i], fabsf(y[i][j]));
-                }
+                gmax[i] = vec_max<VEC, SHIFT>(y[i], c, a.cols, lo, before[i]);
                 amax = max_nan(amax, gmax[i]);
             }
         }
         if constexpr (QUANT) {
-            const float top = a.quant == kQuantE4M3 ? 448.0f : 127.0f;
-            float sc = 0.0f, inv = 0.0f;
+            float inv = 0.0f, inv0 = 0.0f;
             if (!a.group) {
-                sc = max_nan(team_reduce<MaxOp, 0>(amax, red, turn) / top, kScaleMin);
+                const float sc = scale_of(team_reduce<MaxOp, 0>(amax, red, turn), a.quant);
                 inv = 1.0f / sc;
                 if (t == 0) a.scale[r] = sc;
+            } else if (SHIFT) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int v = t + i * tpr;
+                    const float m = lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]);
+                    if (v % GL == 0 && v * VEC < a.cols) atomicMax(&gmax_s[set][v / GL], __float_as_int(m));
+                    if (lo && v && column(i) < a.cols) atomicMax(&gmax_s[set][v / GL - 1], __float_as_int(before[i]));
+                }
+                __syncthreads();
+                for (int i = t; i < a.groups; i += tpr) a.scale[r * a.groups + i] = scale_of(__int_as_float(gmax_s[set][i]), a.quant);
+                for (int i = t; i < 128; i += tpr) gmax_s[set ^ 1][i] = 0;  // the next row's, last read before this row's sum
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int v = t + i * tpr, c = v * VEC;
-                if (a.group) {
-                    sc = max_nan(lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]) / top, kScaleMin);
+                const int v = t + i * tpr, c = column(i);
+                if (a.group && !SHIFT) {
+                    const float sc = scale_of(lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]), a.quant);
                     inv = 1.0f / sc;
                     if (v % GL == 0 && c < a.cols) a.scale[r * a.groups + c / 128] = sc;
+                } else if (a.group) {
+                    // a vector behind the start of a group that is not there only holds the end of the last one
+                    inv = 1.0f / scale_of(__int_as_float(gmax_s[set][min(v / GL, a.groups - 1)]), a.quant);
+                    inv0 = lo && v && c < a.cols ? 1.0f / scale_of(__int_as_float(gmax_s[set][v / GL - 1]), a.quant) : 0.0f;
                 }
-                if (c < a.cols) store_codes<VEC>(static_cast<unsigned char *>(a.out8) + off + c, y[i], inv, a.quant);
+                store_codes<VEC, SHIFT>(static_cast<unsigned char *>(a.out8) + off, c, a.cols, y[i], inv, inv0, lo, a.quant);
             }
+            set ^= 1;
         }
     }
 }
 
-// Rows at any alignment, by elements; warp or CTA teams of C columns a thread.
+// Tensors out of step with one another, by elements; warp or CTA teams of C columns a thread.
 template <typename T, int TPR, int C, bool QUANT>
 __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 ? 1 : ctas_per_sm(C))
     norm_forward_elems_kernel(const NormArgs a) {
@@ -373,8 +444,8 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 ? 1 :
                     if (t == 0 && c < a.cols) a.scale[r * a.groups + k / 4] = s;
                 }
                 if (c < a.cols) {
-                    const float q4[4] = {y[k], 0.0f, 0.0f, 0.0f};
-                    dst[c] = (unsigned char)pack8(q4, inv, a.quant);
+                    const float q4[4] = {y[k], 0.0f, 0.0f, 0.0f}, f4[4] = {inv, 0.0f, 0.0f, 0.0f};
+                    dst[c] = (unsigned char)pack8(q4, f4, a.quant);
                 }
             }
         }
@@ -392,19 +463,20 @@ cudaError_t launch_elems(const NormArgs &a, int threads, const DeviceInfo *dev, 
     return cudaGetLastError();
 }
 
-template <typename T, int TPR, int NV>
+template <typename T, int TPR, int NV, bool SHIFT>
 cudaError_t launch_one(const NormArgs &a, const DeviceInfo *dev, cudaStream_t stream) {
     constexpr int teams = kTeamThreads / TPR;
     const long long need = (a.rows + teams - 1) / teams, most = (long long)dev->sms * ctas_per_sm(NV * Storage<T>::kVec);
     const unsigned grid = (unsigned)(need < most ? need : most);
-    if (a.quant) norm_forward_kernel<T, TPR, NV, true><<<grid, kTeamThreads, 0, stream>>>(a);
-    else norm_forward_kernel<T, TPR, NV, false><<<grid, kTeamThreads, 0, stream>>>(a);
+    if (a.quant) norm_forward_kernel<T, TPR, NV, true, SHIFT><<<grid, kTeamThreads, 0, stream>>>(a);
+    else norm_forward_kernel<T, TPR, NV, false, SHIFT><<<grid, kTeamThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t launch_wide(const NormArgs &a, const DeviceInfo *dev, cudaStream_t stream) {
-    const int threads = ((a.cols + 15) / 16 + 31) / 32 * 32;  // at most 1024
-    const int slot = a.cols * (int)sizeof(T) * (a.residual ? 2 : 1);
+template <typename T, bool SHIFT> cudaError_t launch_wide(const NormArgs &a, const DeviceInfo *dev, cudaStream_t stream) {
+    constexpr int VEC = Storage<T>::kVec;
+    const int span = a.cols + (SHIFT ? VEC - 1 : 0), threads = ((span + 15) / 16 + 31) / 32 * 32;  // at most 1024
+    const int slot = (span + VEC - 1) / VEC * 16 * (a.residual ? 2 : 1);
     // as many CTAs as the registers allow (64 a thread), fewer where a slot would not fit their share
     int per_sm = 1024 / threads;
     if (per_sm > 8) per_sm = 8;
@@ -413,34 +485,44 @@ template <typename T> cudaError_t launch_wide(const NormArgs &a, const DeviceInf
     if (slots > 4) slots = 4;
     const int smem = slots * slot;
     static std::atomic<bool> plain_ok[kMaxDev], quant_ok[kMaxDev];
-    const cudaError_t e = a.quant ? allow_smem(norm_forward_wide_kernel<T, true>, staged_budget(1), quant_ok)
-                                  : allow_smem(norm_forward_wide_kernel<T, false>, staged_budget(1), plain_ok);
+    const cudaError_t e = a.quant ? allow_smem(norm_forward_wide_kernel<T, true, SHIFT>, staged_budget(1), quant_ok)
+                                  : allow_smem(norm_forward_wide_kernel<T, false, SHIFT>, staged_budget(1), plain_ok);
     if (e != cudaSuccess) return e;
-    const long long most = (long long)dev->sms * per_sm;
+    long long most = (long long)dev->sms * per_sm;
+    if (SHIFT) most -= most % VEC;  // a CTA's rows have the same shift
     const unsigned grid = (unsigned)(a.rows < most ? a.rows : most);
-    if (a.quant) norm_forward_wide_kernel<T, true><<<grid, threads, smem, stream>>>(a, slots, dev->err);
-    else norm_forward_wide_kernel<T, false><<<grid, threads, smem, stream>>>(a, slots, dev->err);
+    if (a.quant) norm_forward_wide_kernel<T, true, SHIFT><<<grid, threads, smem, stream>>>(a, slots, dev->err);
+    else norm_forward_wide_kernel<T, false, SHIFT><<<grid, threads, smem, stream>>>(a, slots, dev->err);
     return cudaGetLastError();
 }
 
+template <typename T, bool SHIFT> cudaError_t launch_vec(const NormArgs &a, const DeviceInfo *dev, cudaStream_t stream) {
+    constexpr int VEC = Storage<T>::kVec;
+    const int nvec = (a.cols + (SHIFT ? VEC - 1 : 0) + VEC - 1) / VEC;
+    if (nvec <= 8) return launch_one<T, 8, 1, SHIFT>(a, dev, stream);
+    if (nvec <= 32) return launch_one<T, 32, 1, SHIFT>(a, dev, stream);
+    if (nvec <= 64) return launch_one<T, 32, 2, SHIFT>(a, dev, stream);
+    if (nvec <= 128) return launch_one<T, 32, 4, SHIFT>(a, dev, stream);
+    return launch_wide<T, SHIFT>(a, dev, stream);
+}
+
 template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t stream) {
+    constexpr int VEC = Storage<T>::kVec;
     const DeviceInfo *dev = device_info();
     if (!dev) return cudaErrorNotSupported;
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual) |
-                           reinterpret_cast<uintptr_t>(a.weight) | reinterpret_cast<uintptr_t>(a.residual_out) |
-                           reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.out8) |
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.x), res = reinterpret_cast<uintptr_t>(a.residual);
+    const uintptr_t res_out = reinterpret_cast<uintptr_t>(a.residual_out), out = reinterpret_cast<uintptr_t>(a.out);
+    const uintptr_t out8 = reinterpret_cast<uintptr_t>(a.out8);
+    const uintptr_t bits = x | res | reinterpret_cast<uintptr_t>(a.weight) | res_out | out | out8 |
                            (uintptr_t)((size_t)a.cols * sizeof(T));
-    if (bits % 16) {
-        if (a.cols <= 128) return launch_elems<T, 32, 4>(a, kTeamThreads, dev, stream);
-        if (a.cols <= 512) return launch_elems<T, 32, 16>(a, kTeamThreads, dev, stream);
-        return launch_elems<T, 0, 16>(a, ((a.cols + 15) / 16 + 31) / 32 * 32, dev, stream);  // at most 1024 threads
-    }
-    const int nvec = a.cols / Storage<T>::kVec;
-    if (nvec <= 8) return launch_one<T, 8, 1>(a, dev, stream);
-    if (nvec <= 32) return launch_one<T, 32, 1>(a, dev, stream);
-    if (nvec <= 64) return launch_one<T, 32, 2>(a, dev, stream);
-    if (nvec <= 128) return launch_one<T, 32, 4>(a, dev, stream);
-    return launch_wide<T>(a, dev, stream);
+    if (bits % 16 == 0) return launch_vec<T, false>(a, dev, stream);
+    // in step: an element of all tensors is equally far from a vector's start
+    const bool in_step = (!res || ((x ^ res) % 16 == 0 && (x ^ res_out) % 16 == 0)) && (!out || (x ^ out) % 16 == 0) &&
+                         (!out8 || out8 % VEC == x % 16 / sizeof(T));
+    if (in_step && a.cols + VEC - 1 <= 16384) return launch_vec<T, true>(a, dev, stream);
+    if (a.cols <= 128) return launch_elems<T, 32, 4>(a, kTeamThreads, dev, stream);
+    if (a.cols <= 512) return launch_elems<T, 32, 16>(a, kTeamThreads, dev, stream);
+    return launch_elems<T, 0, 16>(a, ((a.cols + 15) / 16 + 31) / 32 * 32, dev, stream);  // at most 1024 threads
 }
 
 }  // namespace

@@ -169,6 +169,58 @@ def test_unaligned_views(cols, cuda_dev):
         check_backward(11, cols, dtype, 22, place=off)
 
 
+def step_off(t, k, fill):
+    """(tensor k elements into a larger buffer, the buffer): the start is off 16 bytes by the same number of elements
+    for all types, 8-bit ones included, with `fill` around it."""
+    b = torch.full((t.numel() + 32,), fill, dtype=torch.float32).to(t.dtype).cuda()
+    v = b[16 + k:16 + k + t.numel()].view(t.shape)
+    v.copy_(t)
+    return v, b
+
+
+@pytest.mark.parametrize("quant,group", [(None, 0), ("e4m3", 0), ("int8", 128)])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", [1, 3, 13, 57, 64, 67, 121, 127, 131, 250, 257, 300, 505, 515, 1000, 1017, 1023, 1025,
+                                  2047, 4383, 9001, 16377, 16383])
+def test_rows_in_step(cols, dtype, quant, group, cuda_dev):
+    """Rows at every offset to 16 bytes, the same in all tensors; infinities around the inputs never count, the bytes
+    around the outputs stay, in place too."""
+    dt = DT[dtype]
+    dt8 = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8, None: None}[quant]
+    for rows, k in ((1, 3), (9, 0), (4, 1), (37, 7 if dtype != "f32" else 2)):
+        x, r, w = inputs(rows, cols, dt, cols + k, residual=k != 1)
+        h, y, rstd = definition(x, r, w)
+        xv, xb = step_off(x, k, float("inf"))
+        rv, rb = (None, None) if r is None else step_off(r, k, float("inf"))
+        ov, ob = step_off(torch.zeros_like(x), k, 5.0)
+        qv, qb = (None, None) if quant is None else step_off(torch.zeros(rows, cols).to(dt8), k, 5.0)
+        o = d.dcn_add_rms_norm_forward(xv, rv, w.cuda(), eps=EPS, quant=quant, group=group, out=ov, out8=qv,
+                                       residual_out=None if r is None else xv, save_rstd=True)
+        if r is not None:
+            assert torch.equal(xv.cpu(), h)
+        assert ((ov.double().cpu() - y).abs() <= y.abs() * (32 * U + half_step(dt)) + tiny(dt)).all()
+        assert ((o.rstd.double().cpu() - rstd).abs() <= rstd * 26 * U).all()
+        if quant:
+            check_quant(o, y, quant, group)
+        for b, fill in ((xb, float("inf")), (rb, float("inf")), (ob, 5.0), (qb, 5.0)):
+            if b is not None:
+                f = b.float()
+                assert (f[:16 + k] == fill).all() and (f[16 + k + rows * cols:] == fill).all()
+
+
+def test_many_rows_in_step(cuda_dev):
+    """More rows than the persistent grids have teams."""
+    for rows, cols, dtype, quant, group in ((9013, 61, "bf16", "int8", 0), (12001, 505, "f16", "e4m3", 128),
+                                            (5734, 4383, "f16", "int8", 128), (2411, 2051, "f32", None, 0)):
+        x, r, w = inputs(rows, cols, DT[dtype], 24)
+        o = d.dcn_add_rms_norm_forward(*gpu(x, r, w), eps=EPS, quant=quant, group=group, keep_out=True)
+        h, y, _ = definition(x, r, w)
+        assert torch.equal(o.residual_out.cpu(), h)
+        assert ((o.out.double().cpu() - y).abs() <= y.abs() * (32 * U + half_step(DT[dtype])) + tiny(DT[dtype])).all()
+        if quant:
+            check_quant(o, y, quant, group)
+
+
 def test_outputs_end_with_the_row(cuda_dev):
     """Unaligned outputs inside larger buffers: nothing around them is written."""
     for rows, cols in ((5, 13), (3, 300), (2, 1001)):
@@ -395,8 +447,10 @@ def test_empty_and_streams_and_graph(cuda_dev):
 
 @pytest.mark.parametrize("cols", [64, 512, 4096, 4099])
 def test_more_than_32_bit_elements(cols, cuda_dev):
-    """Offsets are 64-bit: the last rows of more than 2^32 elements give what they give by themselves."""
-    rows = (1 << 32) // cols + 70
+    """Offsets are 64-bit: the last rows of more than 2^32 elements give what they give by themselves.  Equal bits
+    need equal orders of the sums, which rows off 16-byte boundaries have at equal offsets from one: 40 rows and a
+    multiple of 8 rows before them."""
+    rows = ((1 << 32) // cols + 70) // 8 * 8
     x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
     tail = torch.randn(40, cols, dtype=torch.bfloat16, device="cuda")
     x[-40:] = tail
