@@ -125,29 +125,75 @@ template <typename T> __device__ __forceinline__ uint4 load_any(const T *row, in
     return v;
 }
 
+// Bytes [b0, b1), all but not the whole, of a vector of 4 * W bytes whose elements have ES bytes, to the aligned `dst`:
+// one store for each power of two that the part is made of, in which its two ends differ only by the places.
+template <int W, int ES> __device__ __forceinline__ void store_part(void *dst, const uint32_t *w, int b0, int b1) {
+    constexpr int S = 4 * W;
+    unsigned char *p = static_cast<unsigned char *>(dst);
+    auto word = [&](int at) {
+        if constexpr (W == 1) return w[0];
+        else if constexpr (W == 2) return at & 4 ? w[1] : w[0];
+        else return at & 8 ? (at & 4 ? w[3] : w[2]) : (at & 4 ? w[1] : w[0]);
+    };
+    if (b0 > 0 && b1 < S) {
+        // both ends in one vector: a row of fewer elements than it has
+#pragma unroll
+        for (int k = 0; k < S / ES; ++k) {
+            if (k * ES < b0 || k * ES >= b1) continue;
+            const uint32_t v = w[k * ES / 4] >> (8 * (k * ES % 4));
+            if constexpr (ES == 4) *reinterpret_cast<uint32_t *>(p + k * ES) = v;
+            else if constexpr (ES == 2) *reinterpret_cast<uint16_t *>(p + k * ES) = (uint16_t)v;
+            else p[k] = (unsigned char)v;
+        }
+        return;
+    }
+    const bool head = b1 == S;  // a row's first vector: bytes from b0 on
+    if constexpr (S > 8) {
+        if (head ? b0 <= 8 : (b1 & 8) != 0) *reinterpret_cast<uint2 *>(p + (head ? 8 : 0)) = head ? make_uint2(w[2], w[3]) : make_uint2(w[0], w[1]);
+    }
+    if constexpr (S > 4) {
+        const int at = head ? (b0 + 3) & ~3 : b1 & (S - 1) & ~7;
+        if ((head ? at & 4 : b1 & 4) != 0) *reinterpret_cast<uint32_t *>(p + at) = word(at);
+    }
+    if constexpr (ES < 4) {
+        const int at = head ? (b0 + 1) & ~1 : b1 & ~3;
+        if ((head ? at & 2 : b1 & 2) != 0) *reinterpret_cast<uint16_t *>(p + at) = (uint16_t)(word(at) >> (8 * (at & 2)));
+    }
+    if constexpr (ES < 2) {
+        const int at = head ? b0 : b1 & ~1;
+        if ((head ? at & 1 : b1 & 1) != 0) p[at] = (unsigned char)(word(at) >> (8 * (at & 3)));
+    }
+}
+
 // Only the row's own elements are written.
 template <typename T, bool SHIFT> __device__ __forceinline__ void store_vec(T *row, int c, int cols, const uint4 &v) {
-    constexpr int VEC = Storage<T>::kVec;
+    constexpr int VEC = Storage<T>::kVec, ES = (int)sizeof(T);
     if (!SHIFT) {
         store_cols<T>(row, c, cols, v);
     } else if (c >= 0 && c + VEC <= cols) {
         *reinterpret_cast<uint4 *>(row + c) = v;
     } else if (c < cols) {
-        T e[VEC];
-        memcpy(e, &v, 16);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-            if (c + j >= 0 && c + j < cols) row[c + j] = e[j];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        store_part<4, ES>(row + c, w, max(-c, 0) * ES, min(cols - c, VEC) * ES);
     }
 }
 
-// Zeros where a vector reaches out of its row.
-template <bool SHIFT, int VEC> __device__ __forceinline__ void clear_outside(float *f, int c, int cols) {
-    if (SHIFT && (c < 0 || c + VEC > cols)) {
+// Ones over the elements of a vector that lie in the row.
+template <typename T> __device__ __forceinline__ uint4 row_mask(int c, int cols) {
+    constexpr int VEC = Storage<T>::kVec;
+    uint32_t w[4] = {};
 #pragma unroll
-        for (int j = 0; j < VEC; ++j)
-            if (c + j < 0 || c + j >= cols) f[j] = 0.0f;
-    }
+    for (int j = 0; j < VEC; ++j)
+        if (c + j >= 0 && c + j < cols) w[j * 4 / VEC] |= VEC == 4 ? 0xffffffffu : 0xffffu << (16 * (j % 2));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 operator&(const uint4 &a, const uint4 &b) {
+    return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
+}
+// Zeros where a vector reaches out of its row.
+template <typename T, bool SHIFT> __device__ __forceinline__ uint4 clear_outside(const uint4 &v, int c, int cols) {
+    if (!SHIFT || (c >= 0 && c + Storage<T>::kVec <= cols)) return v;
+    return v & row_mask<T>(c, cols);
 }
 
 // By elements: value k of a thread is column k * tpr + t.

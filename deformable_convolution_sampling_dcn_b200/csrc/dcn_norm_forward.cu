@@ -59,24 +59,24 @@ __device__ __forceinline__ void store_codes(unsigned char *row, int c, int cols,
         if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(row + c) = make_uint2(q[0], q[1]);
         else *reinterpret_cast<uint32_t *>(row + c) = q[0];
     } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-            if (c + j >= 0 && c + j < cols) row[c + j] = (unsigned char)(q[j / 4] >> (8 * (j % 4)));
+        store_part<VEC / 4, 1>(row + c, q, max(-c, 0), min(cols - c, VEC));
     }
 }
 
-// Largest magnitude of a vector's elements in the row: of those from `lo` on, and into `before` of those ahead.
-template <int VEC, bool SHIFT>
-__device__ __forceinline__ float vec_max(const float *y, int c, int cols, int lo, float &before) {
+// Largest magnitude of a vector's elements from `lo` on, and into `before` of those ahead.  Elements outside the row
+// hold 0 * rstd * 0: zero, or NaN where every element of the row is.
+template <int VEC, bool SHIFT> __device__ __forceinline__ float vec_max(const float *y, int lo, float &before) {
     float m = 0.0f;
     before = 0.0f;
-    if (c >= cols) return m;
+    if (SHIFT && lo) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        // elements outside the row hold 0 * rstd * 0, which is NaN where rstd is
-        if (SHIFT && (c + j < 0 || c + j >= cols)) continue;
-        if (SHIFT && j < lo) before = max_nan(before, fabsf(y[j]));
-        else m = max_nan(m, fabsf(y[j]));
+        for (int j = 0; j < VEC; ++j) {
+            before = max_nan(before, j < lo ? fabsf(y[j]) : 0.0f);
+            m = max_nan(m, j < lo ? 0.0f : fabsf(y[j]));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) m = max_nan(m, fabsf(y[j]));
     }
     return m;
 }
@@ -87,10 +87,11 @@ __device__ __forceinline__ float scale_of(float amax, int quant) {
 
 constexpr int kMaxSlots = 8;
 
-// 8-lane and warp teams in CTAs of 256 threads.  A thread holds C = NV * VEC
-// columns of a row: up to 16 with the loads of its team's next row in flight
-// meanwhile, or 32 without; CTAs on an SM follow from the registers that leaves
-// (64, 80 or 128).
+// Teams of 8, 16 and 32 lanes in CTAs of 256 threads.  A thread holds C = NV * VEC
+// columns of a row: up to two vectors with the loads of its team's next row in
+// flight meanwhile, or four without (which fp32 has the registers for, but only
+// with spills: 40000 x 304 to e4m3 58 us against 31); CTAs on an SM follow from
+// the registers that leaves (64, 80 or 128).
 constexpr int kTeamThreads = 256;
 constexpr int ctas_per_sm(int c) { return c <= 8 ? 4 : c <= 16 ? 3 : 2; }
 
@@ -98,7 +99,7 @@ template <typename T, int TPR, int NV, bool QUANT, bool SHIFT>
 __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVec))
     norm_forward_kernel(const NormArgs a) {
     constexpr int VEC = Storage<T>::kVec;
-    constexpr bool AHEAD = NV * VEC <= 16;
+    constexpr bool AHEAD = NV <= 2;
     constexpr int tpr = TPR, teams = kTeamThreads / TPR;  // teams: a multiple of VEC
     const int t = (int)threadIdx.x % TPR, team = (int)threadIdx.x / TPR;
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
@@ -110,6 +111,14 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (weight) w[i] = SHIFT ? load_any<T>(weight, column(i), a.cols) : load_cols<T>(weight, column(i), a.cols);
+    uint4 keep[NV];
+    constexpr bool KEEP = SHIFT && NV <= 2;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (KEEP) keep[i] = row_mask<T>(column(i), a.cols);
+    auto own = [&](const uint4 &v, int i) {
+        return !SHIFT ? v : KEEP ? v & keep[i] : clear_outside<T, SHIFT>(v, column(i), a.cols);
+    };
 
     uint4 xn[NV], rn[NV];
     auto fetch = [&](long long r) {
@@ -134,17 +143,16 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            unpack16<T>(xn[i], y[i]);
+            unpack16<T>(own(xn[i], i), y[i]);
             if (res) {
                 float g[VEC];
-                unpack16<T>(rn[i], g);
+                unpack16<T>(own(rn[i], i), g);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) y[i][j] += g[j];
                 const uint4 h = pack16<T>(y[i]);
                 store_vec<T, SHIFT>(static_cast<T *>(a.residual_out) + off, column(i), cols, h);
                 unpack16<T>(h, y[i]);
             }
-            clear_outside<SHIFT, VEC>(y[i], column(i), cols);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) ss = fmaf(y[i][j], y[i][j], ss);
         }
@@ -167,14 +175,14 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
                 store_vec<T, SHIFT>(static_cast<T *>(a.out) + off, column(i), cols, pack16<T>(y[i]));
         }
         if constexpr (QUANT) {
-            // lanes that share 128 columns; a team narrower than that holds rows of at most 128 columns
+            // lanes that share 128 columns; teams narrower than a warp hold rows of at most 128 columns
             constexpr int GL = 128 / VEC;
-            const bool grouped = a.group != 0 && TPR >= GL;
+            const bool grouped = a.group != 0 && TPR == 32;
             // of shifted vectors the first of a group also holds the end of the group before
             float gmax[NV], before[NV], amax = 0.0f, s[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                gmax[i] = vec_max<VEC, SHIFT>(y[i], column(i), cols, grouped && t % GL == 0 ? sh : 0, before[i]);
+                gmax[i] = vec_max<VEC, SHIFT>(y[i], grouped && t % GL == 0 ? sh : 0, before[i]);
                 amax = max_nan(amax, gmax[i]);
             }
             if (!grouped) {
@@ -220,21 +228,22 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ float red[64];
     __shared__ __align__(8) uint64_t bars[kMaxSlots];
-    // shifted rows: maxima of the groups (bits of values >= 0), two rows' sets
-    __shared__ int gmax_s[2][QUANT && SHIFT ? 128 : 1];
+    // shifted rows: maxima of the groups (bits of values >= 0) and the factors that follow from them
+    __shared__ int gmax_s[QUANT && SHIFT ? 128 : 1];
+    __shared__ float inv_s[QUANT && SHIFT ? 128 : 1];
     const int t = threadIdx.x, tpr = blockDim.x;
     const T *weight = static_cast<const T *>(a.weight);
     const long long step = gridDim.x, total = a.rows * a.cols;  // SHIFT: step is a multiple of VEC, or no CTA has two rows
     const int sh = SHIFT ? shift_of_rows<T>(a.x, blockIdx.x, a.cols) : 0, nvec = (a.cols + sh + VEC - 1) / VEC;
     // a row in the ring: its vectors of the aligned grid, without one that reaches out of the tensor at either end
     const uint32_t row_bytes = (uint32_t)nvec * 16, slot_bytes = a.residual ? 2 * row_bytes : row_bytes;
-    int turn = 0, set = 0;
+    int turn = 0;
     if (t == 0) {
         for (int i = 0; i < slots; ++i) mbar_init(smem_u32(bars + i), 1);
         fence_mbar_init();
     }
     if (QUANT && SHIFT)
-        for (int i = t; i < 256; i += tpr) gmax_s[i / 128][i % 128] = 0;
+        for (int i = t; i < 128; i += tpr) gmax_s[i] = 0;
     __syncthreads();
     auto stage = [&](long long r, int s) {  // by thread 0
         if (r >= a.rows) return;
@@ -265,7 +274,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
         auto staged = [&](const unsigned char *row, const void *tensor, int c) {
             if (SHIFT && c < a.cols && (off + c < 0 || off + c + VEC > total))
                 return load_any<T>(static_cast<const T *>(tensor) + off, c, a.cols);
-            return load_cols<T>(reinterpret_cast<const T *>(row) + sh, c, a.cols);
+            return clear_outside<T, SHIFT>(load_cols<T>(reinterpret_cast<const T *>(row) + sh, c, a.cols), c, a.cols);
         };
         float y[NV][VEC];
         float ss = 0.0f;
@@ -282,7 +291,6 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
                 store_vec<T, SHIFT>(static_cast<T *>(a.residual_out) + off, c, a.cols, h);
                 unpack16<T>(h, y[i]);
             }
-            clear_outside<SHIFT, VEC>(y[i], c, a.cols);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) ss = fmaf(y[i][j], y[i][j], ss);
         }
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
             }
             if (!QUANT || a.out) store_vec<T, SHIFT>(static_cast<T *>(a.out) + off, c, a.cols, pack16<T>(y[i]));
             if (QUANT) {
-                gmax[i] = vec_max<VEC, SHIFT>(y[i], c, a.cols, lo, before[i]);
+                gmax[i] = vec_max<VEC, SHIFT>(y[i], lo, before[i]);
                 amax = max_nan(amax, gmax[i]);
             }
         }
@@ -325,12 +333,17 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
                 for (int i = 0; i < NV; ++i) {
                     const int v = t + i * tpr;
                     const float m = lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]);
-                    if (v % GL == 0 && v * VEC < a.cols) atomicMax(&gmax_s[set][v / GL], __float_as_int(m));
-                    if (lo && v && column(i) < a.cols) atomicMax(&gmax_s[set][v / GL - 1], __float_as_int(before[i]));
+                    if (v % GL == 0 && v * VEC < a.cols) atomicMax(&gmax_s[v / GL], __float_as_int(m));
+                    if (lo && v && column(i) < a.cols) atomicMax(&gmax_s[v / GL - 1], __float_as_int(before[i]));
                 }
                 __syncthreads();
-                for (int i = t; i < a.groups; i += tpr) a.scale[r * a.groups + i] = scale_of(__int_as_float(gmax_s[set][i]), a.quant);
-                for (int i = t; i < 128; i += tpr) gmax_s[set ^ 1][i] = 0;  // the next row's, last read before this row's sum
+                for (int i = t; i < a.groups; i += tpr) {
+                    const float sc = scale_of(__int_as_float(gmax_s[i]), a.quant);
+                    a.scale[r * a.groups + i] = sc;
+                    inv_s[i] = 1.0f / sc;
+                    gmax_s[i] = 0;
+                }
+                __syncthreads();
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -341,12 +354,11 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
                     if (v % GL == 0 && c < a.cols) a.scale[r * a.groups + c / 128] = sc;
                 } else if (a.group) {
                     // a vector behind the start of a group that is not there only holds the end of the last one
-                    inv = 1.0f / scale_of(__int_as_float(gmax_s[set][min(v / GL, a.groups - 1)]), a.quant);
-                    inv0 = lo && v && c < a.cols ? 1.0f / scale_of(__int_as_float(gmax_s[set][v / GL - 1]), a.quant) : 0.0f;
+                    inv = inv_s[min(v / GL, a.groups - 1)];
+                    if (lo && v && c < a.cols) inv0 = inv_s[v / GL - 1];
                 }
                 store_codes<VEC, SHIFT>(static_cast<unsigned char *>(a.out8) + off, c, a.cols, y[i], inv, inv0, lo, a.quant);
             }
-            set ^= 1;
         }
     }
 }
@@ -500,6 +512,7 @@ template <typename T, bool SHIFT> cudaError_t launch_vec(const NormArgs &a, cons
     constexpr int VEC = Storage<T>::kVec;
     const int nvec = (a.cols + (SHIFT ? VEC - 1 : 0) + VEC - 1) / VEC;
     if (nvec <= 8) return launch_one<T, 8, 1, SHIFT>(a, dev, stream);
+    if (nvec <= 16) return launch_one<T, 16, 1, SHIFT>(a, dev, stream);
     if (nvec <= 32) return launch_one<T, 32, 1, SHIFT>(a, dev, stream);
     if (nvec <= 64) return launch_one<T, 32, 2, SHIFT>(a, dev, stream);
     if (nvec <= 128) return launch_one<T, 32, 4, SHIFT>(a, dev, stream);
@@ -519,7 +532,12 @@ template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t strea
     // in step: an element of all tensors is equally far from a vector's start
     const bool in_step = (!res || ((x ^ res) % 16 == 0 && (x ^ res_out) % 16 == 0)) && (!out || (x ^ out) % 16 == 0) &&
                          (!out8 || out8 % VEC == x % 16 / sizeof(T));
-    if (in_step && a.cols + VEC - 1 <= 16384) return launch_vec<T, true>(a, dev, stream);
+    // four vectors a lane of shifted fp32 lose to elements: 40000 x 301 38.3 us against 32.7 (e4m3 44.7 against 36.6),
+    // 20011 x 501 29.3 against 28.4; narrower and wider rows, and 16 bits, gain: fp16 5734 x 4383 42 us against 72 (e4m3
+    // 51 against 127), 100000 x 61 fp32 20 against 25
+    const int nvec = (a.cols + 2 * (VEC - 1)) / VEC;
+    if (in_step && a.cols + VEC - 1 <= 16384 && !(VEC == 4 && nvec > 64 && nvec <= 128))
+        return launch_vec<T, true>(a, dev, stream);
     if (a.cols <= 128) return launch_elems<T, 32, 4>(a, kTeamThreads, dev, stream);
     if (a.cols <= 512) return launch_elems<T, 32, 16>(a, kTeamThreads, dev, stream);
     return launch_elems<T, 0, 16>(a, ((a.cols + 15) / 16 + 31) / 32 * 32, dev, stream);  // at most 1024 threads
