@@ -30,7 +30,7 @@ constexpr int kSms = 148;
 template <typename T, int NV, int WARPS> constexpr int kSumFloats = (WARPS / 2) * 32 * NV * Storage<T>::kVec;
 template <typename T, int TPR, int NV, int WARPS, bool ELEMS = false>
 __device__ __forceinline__ void store_partial(const NormArgs &a, float2 (&gw)[NV][Storage<T>::kVec / 2], float *sums, int t,
-                                              int tpr) {
+                                              int tpr, int shift = 0) {
     constexpr int VEC = Storage<T>::kVec;
     float *part = a.partial + (long long)blockIdx.x * a.cols;
     if constexpr (TPR != 0) {
@@ -74,19 +74,20 @@ __device__ __forceinline__ void store_partial(const NormArgs &a, float2 (&gw)[NV
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            const int c = ELEMS ? (i * VEC + j) * tpr + t : (t + i * tpr) * VEC + j;
-            if (c < a.cols) part[c] = j % 2 ? gw[i][j / 2].y : gw[i][j / 2].x;
+            const int c = ELEMS ? (i * VEC + j) * tpr + t : (t + i * tpr) * VEC + j - shift;
+            if (c >= 0 && c < a.cols) part[c] = j % 2 ? gw[i][j / 2].y : gw[i][j / 2].x;
         }
 }
 
-template <typename T, int NV>
+template <typename T, int NV, bool SHIFT = false>
 __device__ __forceinline__ void load_weight(const NormArgs &a, int t, int tpr, float2 (&w)[NV][Storage<T>::kVec / 2],
-                                            float2 (&gw)[NV][Storage<T>::kVec / 2]) {
+                                            float2 (&gw)[NV][Storage<T>::kVec / 2], int shift = 0) {
     constexpr int VEC = Storage<T>::kVec;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (a.weight)
-            unpack16x2<T>(load_cols<T>(static_cast<const T *>(a.weight), (t + i * tpr) * VEC, a.cols), w[i]);
+        const T *weight = static_cast<const T *>(a.weight);
+        const int c = (t + i * tpr) * VEC - shift;
+        if (a.weight) unpack16x2<T>(SHIFT ? load_any<T>(weight, c, a.cols) : load_cols<T>(weight, c, a.cols), w[i]);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
             if (!a.weight) w[i][j] = make_float2(1.0f, 1.0f);
@@ -199,8 +200,9 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : 256, TPR == 0 ? 1 : 2) norm_
 
 // A row's products from its staged tensors: xh and grad_out in registers, the weight gradient, and this thread's part
 // of sum(g * xh).
-template <typename T, int NV>
-__device__ __forceinline__ float staged_row(const unsigned char *h, const unsigned char *g, int t, int tpr, int cols,
+template <typename T, int NV, bool SHIFT>
+__device__ __forceinline__ float staged_row(const RowVecs<T, SHIFT, true> &in, const NormArgs &a, const unsigned char *h,
+                                            const unsigned char *g, int t, int tpr,
                                             float rstd, const float2 (&w)[NV][Storage<T>::kVec / 2],
                                             float2 (&xh)[NV][Storage<T>::kVec / 2], float2 (&gy)[NV][Storage<T>::kVec / 2],
                                             float2 (&gw)[NV][Storage<T>::kVec / 2]) {
@@ -208,9 +210,9 @@ __device__ __forceinline__ float staged_row(const unsigned char *h, const unsign
     float2 dot = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * tpr) * VEC;
-        unpack16x2<T>(load_cols<T>(reinterpret_cast<const T *>(h), c, cols), xh[i]);
-        unpack16x2<T>(load_cols<T>(reinterpret_cast<const T *>(g), c, cols), gy[i]);
+        const int c = (t + i * tpr) * VEC - in.shift;
+        unpack16x2<T>(in.load(h, a.h, i, c), xh[i]);
+        unpack16x2<T>(in.load(g, a.grad_out, i, c), gy[i]);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
             xh[i][j] = f2_mul(xh[i][j], make_float2(rstd, rstd));
@@ -223,23 +225,23 @@ __device__ __forceinline__ float staged_row(const unsigned char *h, const unsign
 }
 
 // grad_x of the row; `r` the staged gradient of the new residual, or nullptr.
-template <typename T, int NV>
-__device__ __forceinline__ void staged_output(T *out, const unsigned char *r, int t, int tpr, int cols, float rstd,
-                                              float mean, const float2 (&w)[NV][Storage<T>::kVec / 2],
+template <typename T, int NV, bool SHIFT>
+__device__ __forceinline__ void staged_output(const RowVecs<T, SHIFT, true> &in, const NormArgs &a, const unsigned char *r, int t,
+                                              int tpr, float rstd, float mean, const float2 (&w)[NV][Storage<T>::kVec / 2],
                                               const float2 (&xh)[NV][Storage<T>::kVec / 2],
                                               const float2 (&gy)[NV][Storage<T>::kVec / 2]) {
     constexpr int VEC = Storage<T>::kVec;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (t + i * tpr) * VEC;
+        const int c = (t + i * tpr) * VEC - in.shift;
         float2 o[VEC / 2];
-        if (r) unpack16x2<T>(load_cols<T>(reinterpret_cast<const T *>(r), c, cols), o);
+        if (r) unpack16x2<T>(in.load(r, a.grad_residual_out, i, c), o);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
             const float2 d = f2_fma(xh[i][j], make_float2(-mean, -mean), f2_mul(gy[i][j], w[i][j]));
             o[j] = r ? f2_fma(d, make_float2(rstd, rstd), o[j]) : f2_mul(d, make_float2(rstd, rstd));
         }
-        store_cols<T>(out, c, cols, pack16<T>(reinterpret_cast<const float *>(o)));
+        store_vec<T, SHIFT>(static_cast<T *>(a.grad_x) + in.off, c, in.cols, pack16<T>(reinterpret_cast<const float *>(o)));
     }
 }
 
@@ -311,10 +313,11 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, CTAS)
         if (r < a.rows) {
             const unsigned char *base = ring + s * slot_bytes + warp * row_bytes;
             float2 xh[NV][VEC / 2], gy[NV][VEC / 2];
-            float dot = staged_row<T, NV>(base, base + tile_bytes, t, 32, a.cols, rstd, w, xh, gy, gw);
+            const RowVecs<T, false, true> in{a.cols, r * a.cols};
+            float dot = staged_row<T, NV, false>(in, a, base, base + tile_bytes, t, 32, rstd, w, xh, gy, gw);
             dot = lanes_reduce<SumOp, 32>(dot) * inv_cols;
-            staged_output<T, NV>(static_cast<T *>(a.grad_x) + r * a.cols,
-                                 a.grad_residual_out ? base + 2 * tile_bytes : nullptr, t, 32, a.cols, rstd, dot, w, xh, gy);
+            staged_output<T, NV, false>(in, a, a.grad_residual_out ? base + 2 * tile_bytes : nullptr, t, 32, rstd, dot, w, xh,
+                                        gy);
         }
         __syncwarp();
         if (t == 0) mbar_arrive(empty + 8 * s);
@@ -328,10 +331,10 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, CTAS)
     store_partial<T, 32, NV, WARPS>(a, gw, reinterpret_cast<float *>(ring), t, 32);
 }
 
-// Wider rows, 16-byte aligned, of up to 8192 columns: a CTA of 16 columns a thread per row, each row of the tensors
-// copied into the ring by one bulk copy.  The slot of a row is handed back behind the barrier of the next row's
+// Wider rows of up to 8192 columns: a CTA of 16 columns a thread per row, each row of the tensors copied into the ring
+// by one bulk copy (rows off 16-byte boundaries by vectors of the aligned grid, dcn_norm.cuh).  The slot of a row is handed back behind the barrier of the next row's
 // reduction, when the whole CTA is past its output.
-template <typename T>
+template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(512, 1) norm_backward_wide_kernel(const NormArgs a, int slots, unsigned int *err) {
     constexpr int VEC = Storage<T>::kVec, NV = 16 / VEC;
     extern __shared__ __align__(128) unsigned char ring[];
@@ -339,7 +342,10 @@ __global__ void __launch_bounds__(512, 1) norm_backward_wide_kernel(const NormAr
     __shared__ __align__(8) uint64_t bars_s[kMaxSlots];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t = threadIdx.x, tpr = blockDim.x;
-    const uint32_t row_bytes = (uint32_t)a.cols * sizeof(T), slot_bytes = (a.grad_residual_out ? 3 : 2) * row_bytes;
+    const long long total = a.rows * a.cols;
+    // SHIFT: the grid is a multiple of VEC, or no CTA has two rows
+    const int sh = SHIFT ? shift_of_rows<T>(a.h, blockIdx.x, a.cols) : 0, nvec = (a.cols + sh + VEC - 1) / VEC;
+    const uint32_t row_bytes = (uint32_t)nvec * 16, slot_bytes = (a.grad_residual_out ? 3 : 2) * row_bytes;
     const uint32_t bars = smem_u32(bars_s);
     int turn = 0;
     if (t == 0) {
@@ -349,18 +355,24 @@ __global__ void __launch_bounds__(512, 1) norm_backward_wide_kernel(const NormAr
     __syncthreads();
     auto stage = [&](long long r, int s) {  // by thread 0
         if (r >= a.rows) return;
-        const uint32_t bar = bars + 8 * s, dst = smem_u32(ring) + s * slot_bytes;
-        mbar_arrive_expect_tx(bar, slot_bytes);
-        bulk_load(dst, static_cast<const T *>(a.h) + r * a.cols, row_bytes, bar);
-        bulk_load(dst + row_bytes, static_cast<const T *>(a.grad_out) + r * a.cols, row_bytes, bar);
+        // without a vector that reaches out of the tensor at either end
+        const long long first_vec = r * a.cols - sh;
+        const int skip = SHIFT && first_vec < 0, n = nvec - skip - (SHIFT && first_vec + (long long)nvec * VEC > total);
+        const long long e = first_vec + skip * VEC;
+        const uint32_t bar = bars + 8 * s, dst = smem_u32(ring) + s * slot_bytes + 16 * skip;
+        mbar_arrive_expect_tx(bar, (a.grad_residual_out ? 48u : 32u) * n);
+        bulk_load(dst, static_cast<const T *>(a.h) + e, 16u * n, bar);
+        bulk_load(dst + row_bytes, static_cast<const T *>(a.grad_out) + e, 16u * n, bar);
         if (a.grad_residual_out)
-            bulk_load(dst + 2 * row_bytes, static_cast<const T *>(a.grad_residual_out) + r * a.cols, row_bytes, bar);
+            bulk_load(dst + 2 * row_bytes, static_cast<const T *>(a.grad_residual_out) + e, 16u * n, bar);
     };
     const long long step = gridDim.x, first = blockIdx.x;
     if (t == 0)
         for (int i = 0; i < slots; ++i) stage(first + i * step, i);
     float2 w[NV][VEC / 2], gw[NV][VEC / 2];
-    load_weight<T, NV>(a, t, tpr, w, gw);
+    load_weight<T, NV, SHIFT>(a, t, tpr, w, gw, sh);
+    RowVecs<T, SHIFT, true> in{a.cols, 0};
+    in.init(sh, nvec, t, tpr);
     const float inv_cols = 1.0f / (float)a.cols;
     float next_rstd = first < a.rows ? __ldg(a.rstd + first) : 0.0f;
     int s = 0;
@@ -374,18 +386,19 @@ __global__ void __launch_bounds__(512, 1) norm_backward_wide_kernel(const NormAr
         }
         const unsigned char *base = ring + s * slot_bytes;
         float2 xh[NV][VEC / 2], gy[NV][VEC / 2];
-        float dot = staged_row<T, NV>(base, base + row_bytes, t, tpr, a.cols, rstd, w, xh, gy, gw);
+        in.at(r, total);
+        float dot = staged_row<T, NV, SHIFT>(in, a, base, base + row_bytes, t, tpr, rstd, w, xh, gy, gw);
         dot = team_reduce<SumOp, 0>(dot, red, turn) * inv_cols;
         if (t == 0 && r != first) stage(r + (slots - 1) * step, s ? s - 1 : slots - 1);
-        staged_output<T, NV>(static_cast<T *>(a.grad_x) + r * a.cols, a.grad_residual_out ? base + 2 * row_bytes : nullptr,
-                             t, tpr, a.cols, rstd, dot, w, xh, gy);
+        staged_output<T, NV, SHIFT>(in, a, a.grad_residual_out ? base + 2 * row_bytes : nullptr, t, tpr, rstd, dot, w, xh,
+                                    gy);
         if (++s == slots) {
             s = 0;
             phase ^= 1;
         }
     }
     if (!a.grad_weight) return;
-    store_partial<T, 0, NV, 0>(a, gw, red, t, tpr);
+    store_partial<T, 0, NV, 0>(a, gw, red, t, tpr, sh);
 }
 
 // grad_weight[c] = sum over the CTAs of the first kernel, in a fixed order: 8
@@ -419,32 +432,41 @@ enum Route { kNarrow, kTiles, kWide, kElems };
 struct Config {
     Route route;
     int nv, threads, rows, per_sm;  // nv vectors (kElems: groups of VEC columns) a thread
+    int shift;                      // 0, or the largest shift of a row, VEC - 1
 };
-Config config_of(int cols, int vec, bool aligned) {
+// How all tensors' rows lie: on 16-byte boundaries, off them by the same in all tensors, or in any way.
+enum Lie { kAligned, kInStep, kAnyhow };
+Config config_of(int cols, int vec, Lie lie) {
+    const bool aligned = lie == kAligned;
     const int nvec = (cols + vec - 1) / vec, nv16 = 16 / vec;
-    const int wide = ((cols + 15) / 16 + 31) / 32 * 32;  // threads of a CTA for a row, 16 columns each
-    if (aligned && nvec <= 8) return {kNarrow, 1, kTeamThreads, kTeamThreads / 8, 2};
+    if (aligned && nvec <= 8) return {kNarrow, 1, kTeamThreads, kTeamThreads / 8, 2, 0};
     if (aligned && nvec <= 128) {
         // columns a thread -> registers -> warps: 72 registers for two CTAs of 13 warps, 112 for one of 17
         const int nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, c = nv * vec;
-        if (c <= 8) return {kTiles, nv, 13 * 32, 12, 2};
-        if (c <= 16) return {kTiles, nv, 17 * 32, 16, 1};
-        return {kTiles, nv, 13 * 32, 12, 1};
+        if (c <= 8) return {kTiles, nv, 13 * 32, 12, 2, 0};
+        if (c <= 16) return {kTiles, nv, 17 * 32, 16, 1, 0};
+        return {kTiles, nv, 13 * 32, 12, 1, 0};
     }
-    if (aligned && cols <= 8192) {
+    const int shift = aligned ? 0 : vec - 1, span = cols + shift;  // columns of a row's vectors
+    // fp32 rows in step gain from 2048 columns on (9093 x 2047 54.7 us against 51.8 by elements, 7001 x 3001 59.5 against
+    // 64.4, 4001 x 6001 68 against 90), 16 bits at all widths (fp16 20011 x 1101 63 against 67, 4001 x 6001 57 against 95)
+    if (span <= 8192 && (aligned ? nvec > 128 : lie == kInStep && cols > (vec == 4 ? 2048 : 1024))) {
+        const int wide = ((span + 15) / 16 + 31) / 32 * 32;  // threads of a CTA for a row, 16 columns each
         int per_sm = 512 / wide < 4 ? 512 / wide : 4;
         // fewer CTAs where two staged rows of three tensors would not fit their share of the shared memory
-        while (per_sm > 1 && 2 * 3 * cols * (16 / vec) > staged_budget(per_sm)) --per_sm;
-        return {kWide, nv16, wide, 1, per_sm};
+        while (per_sm > 1 && 2 * 3 * (span + vec - 1) / vec * 16 > staged_budget(per_sm)) --per_sm;
+        return {kWide, nv16, wide, 1, per_sm, shift};
     }
-    if (cols <= 32 * vec) return {kElems, 1, 256, 8, 2};
-    if (cols <= 512) return {kElems, nv16, 256, 8, 2};
+    if (cols <= 32 * vec) return {kElems, 1, 256, 8, 2, 0};
+    if (cols <= 512) return {kElems, nv16, 256, 8, 2, 0};
     const int c = cols <= 8192 ? 8 : 16, threads = ((cols + c - 1) / c + 31) / 32 * 32;  // at most 1024
-    return {kElems, c / vec, threads, 1, 1024 / threads < 8 ? 1024 / threads : 8};
+    return {kElems, c / vec, threads, 1, 1024 / threads < 8 ? 1024 / threads : 8, 0};
 }
 
 int grid_of(int64_t rows, const Config &c) {
-    const int64_t need = (rows + c.rows - 1) / c.rows, most = (int64_t)kSms * c.per_sm;
+    const int64_t need = (rows + c.rows - 1) / c.rows;
+    int64_t most = (int64_t)kSms * c.per_sm;
+    most -= most % (c.shift + 1);  // shifted: a CTA's rows have the same shift
     return (int)(need < most ? need : most);
 }
 
@@ -473,7 +495,8 @@ template <typename K> cudaError_t launch_plain(K kern, const NormArgs &a, const 
 template <typename K>
 cudaError_t launch_staged(K kern, const NormArgs &a, const Config &c, int budget, int es, std::atomic<bool> (&ok)[kMaxDev],
                           const DeviceInfo *dev, cudaStream_t stream) {
-    const int slot = a.cols * es * (a.grad_residual_out ? 3 : 2) * c.rows;
+    const int row_bytes = ((a.cols + c.shift) * es + 15) / 16 * 16;  // the tiles' rows are multiples of 16 bytes
+    const int slot = row_bytes * (a.grad_residual_out ? 3 : 2) * c.rows;
     int slots = budget / slot;
     if (slots > kMaxSlots) slots = kMaxSlots;
     const cudaError_t e = allow_smem(kern, staged_budget(1), ok);
@@ -505,9 +528,11 @@ template <typename T> cudaError_t launch_rows(const NormArgs &a, const Config &c
                 return launch_tiles<T, 4, 12, 1>(a, c, dev, stream);
             }
         case kWide: {
-            static std::atomic<bool> ok[kMaxDev];
-            return launch_staged(norm_backward_wide_kernel<T>, a, c, staged_budget(c.per_sm), (int)sizeof(T), ok, dev,
-                                 stream);
+            static std::atomic<bool> ok[kMaxDev], shift_ok[kMaxDev];
+            return c.shift ? launch_staged(norm_backward_wide_kernel<T, true>, a, c, staged_budget(c.per_sm), (int)sizeof(T),
+                                           shift_ok, dev, stream)
+                           : launch_staged(norm_backward_wide_kernel<T, false>, a, c, staged_budget(c.per_sm), (int)sizeof(T),
+                                           ok, dev, stream);
         }
         case kElems:
             if (c.rows > 1)
@@ -520,10 +545,11 @@ template <typename T> cudaError_t launch_rows(const NormArgs &a, const Config &c
 }
 
 template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t stream) {
-    const uintptr_t bits = reinterpret_cast<uintptr_t>(a.h) | reinterpret_cast<uintptr_t>(a.grad_out) |
-                           reinterpret_cast<uintptr_t>(a.grad_residual_out) | reinterpret_cast<uintptr_t>(a.weight) |
-                           reinterpret_cast<uintptr_t>(a.grad_x) | (uintptr_t)((size_t)a.cols * sizeof(T));
-    const Config c = config_of(a.cols, Storage<T>::kVec, bits % 16 == 0);
+    const uintptr_t h = reinterpret_cast<uintptr_t>(a.h), gy = reinterpret_cast<uintptr_t>(a.grad_out);
+    const uintptr_t gh = reinterpret_cast<uintptr_t>(a.grad_residual_out), gx = reinterpret_cast<uintptr_t>(a.grad_x);
+    const uintptr_t bits = h | gy | gh | gx | reinterpret_cast<uintptr_t>(a.weight) | (uintptr_t)((size_t)a.cols * sizeof(T));
+    const bool in_step = (h ^ gy) % 16 == 0 && (h ^ gx) % 16 == 0 && (!gh || (h ^ gh) % 16 == 0);
+    const Config c = config_of(a.cols, Storage<T>::kVec, bits % 16 == 0 ? kAligned : in_step ? kInStep : kAnyhow);
     const cudaError_t e = launch_rows<T>(a, c, stream);
     return e != cudaSuccess ? e : launch_grad_weight<T>(a, grid_of(a.rows, c), stream);
 }
@@ -531,10 +557,14 @@ template <typename T> cudaError_t launch_t(const NormArgs &a, cudaStream_t strea
 }  // namespace
 
 int norm_backward_partial_rows(int64_t rows, int cols, DType dtype) {
-    // whether the tensors are aligned is not known yet
+    // how the tensors lie is not known yet
     const int vec = dtype == DType::F32 ? 4 : 8;
-    const int x = grid_of(rows, config_of(cols, vec, true)), y = grid_of(rows, config_of(cols, vec, false));
-    return x > y ? x : y;
+    int most = 0;
+    for (const Lie lie : {kAligned, kInStep, kAnyhow}) {
+        const int n = grid_of(rows, config_of(cols, vec, lie));
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 cudaError_t launch_norm_backward(const NormArgs &a, cudaStream_t stream) {

@@ -12,8 +12,10 @@
 // Bound: device memory.  One pass: a row stays in the registers of its team
 // between the statistics and the output, so each byte moves once.  Measured (one
 // B200): bf16 102400 x 256 with a residual 34.4 us (210 MB: 6.1 TB/s of 6.56),
-// fp16 12800 x 512 to e4m3 9.1 us (46 MB: 5.0 TB/s), bf16 2047 x 4096 to int8 in
-// groups 13.8 us (59 MB: 4.3 TB/s).
+// fp16 12800 x 512 to e4m3 8.9 us (46 MB: 5.2 TB/s), bf16 2047 x 4096 to int8 in
+// groups 14.0 us (59 MB: 4.2 TB/s); off 16-byte boundaries fp16 5734 x 4383 with a
+// residual 39.7 us (201 MB: 5.1 TB/s), to int8 in groups 57 us, where the
+// instructions bound it.
 #include <cuda_fp8.h>
 
 #include "dcn_device.h"
@@ -219,9 +221,10 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
     }
 }
 
-// Rows wider than a warp team holds, 16-byte aligned: a CTA of 16 columns a
-// thread per row, the rows staged by bulk copies (bf16 2047 x 4096 to int8: 16.8
-// us with the next row's loads in registers, 13.8 us staged).
+// Rows wider than a warp team holds: a CTA of 16 columns a thread per row, the
+// rows staged by bulk copies (bf16 2047 x 4096 to int8: 16.8 us with the next
+// row's loads in registers, 14.0 us staged).  A shifted row's groups of 128
+// columns begin inside vectors, so their maxima meet in shared memory.
 template <typename T, bool QUANT, bool SHIFT>
 __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormArgs a, int slots, unsigned int *err) {
     constexpr int VEC = Storage<T>::kVec, NV = 16 / VEC, GL = 128 / VEC;
@@ -262,6 +265,8 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
     for (int i = 0; i < NV; ++i)
         if (weight) w[i] = SHIFT ? load_any<T>(weight, column(i), a.cols) : load_cols<T>(weight, column(i), a.cols);
 
+    RowVecs<T, SHIFT, VEC == 8 && !QUANT> in{a.cols, 0};
+    in.init(sh, nvec, t, tpr);
     int s = 0;
     uint32_t phase = 0;
     for (long long r = blockIdx.x; r < a.rows; r += step) {
@@ -271,20 +276,16 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
             return;
         }
         const unsigned char *slot = ring + s * slot_bytes;
-        auto staged = [&](const unsigned char *row, const void *tensor, int c) {
-            if (SHIFT && c < a.cols && (off + c < 0 || off + c + VEC > total))
-                return load_any<T>(static_cast<const T *>(tensor) + off, c, a.cols);
-            return clear_outside<T, SHIFT>(load_cols<T>(reinterpret_cast<const T *>(row) + sh, c, a.cols), c, a.cols);
-        };
+        in.at(r, total);
         float y[NV][VEC];
         float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = column(i);
-            unpack16<T>(staged(slot, a.x, c), y[i]);
+            unpack16<T>(in.load(slot, a.x, i, c), y[i]);
             if (a.residual) {
                 float g[VEC];
-                unpack16<T>(staged(slot + row_bytes, a.residual, c), g);
+                unpack16<T>(in.load(slot + row_bytes, a.residual, i, c), g);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) y[i][j] += g[j];
                 const uint4 h = pack16<T>(y[i]);

@@ -365,9 +365,12 @@ int64_t dcn_proj_adapters_workspace_bytes(const dadapt_params *p);
  * A NaN or infinite h makes the statistics of its row NaN or rstd 0; a scale
  * over a NaN is NaN, so the dequantised values are too (e4m3 codes of a NaN are
  * NaN; int8 codes under a NaN scale mean nothing).
- * cols in [1, 16384], eps > 0.  Tensors are aligned to their element; where
- * all of them are 16-byte aligned and a row is a multiple of 16 bytes the
- * kernel moves 16-byte vectors, else elements.  rows == 0 is a no-op.
+ * cols in [1, 16384], eps > 0.  Tensors are aligned to their element.  Rows on
+ * 16-byte boundaries are the fastest; other rows move by vectors too where all
+ * tensors are off such a boundary by the same number of elements, else by
+ * elements.  The order of a row's sums depends on the width and on how the rows
+ * lie, so the last bits of equal rows may differ where one is off a boundary by
+ * more than the other.  rows == 0 is a no-op.
  */
 typedef enum { DCN_QUANT_NONE = 0, DCN_QUANT_E4M3 = 1, DCN_QUANT_INT8 = 2 } dcn_quant8;
 

@@ -318,6 +318,29 @@ def test_backward_many_rows(rows, cols, dtype, cuda_dev):
     check_backward(rows, cols, dtype, 7)
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", [5, 61, 131, 505, 515, 1001, 1025, 1031, 2047, 4383, 8185, 8187, 8191, 12001])
+def test_backward_in_step(cols, dtype, cuda_dev):
+    """Rows off 16-byte boundaries by the same in all tensors, infinities around them, more rows than CTAs."""
+    for rows, k in ((1, 3), (9, 0), (4, 1), (37, 7 if dtype != "f32" else 2), (1201, 0)):
+        check_backward(rows, cols, dtype, cols + k, residual=k != 1, place=lambda t: step_off(t, k, float("inf"))[0])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_backward_in_step_in_place(dtype, cuda_dev):
+    h, gh, w = inputs(300, 1029, DT[dtype], 61)
+    gy = torch.randn(300, 1029).to(DT[dtype])
+    rstd = definition(h, None, None)[2].float().cuda()
+    want = d.dcn_add_rms_norm_backward(*gpu(gy, h), rstd, w.cuda(), grad_residual_out=gh.cuda())
+    for which in range(2):
+        t = [step_off(v, 0, 5.0) for v in (gy, h, gh)]
+        got = d.dcn_add_rms_norm_backward(t[0][0], t[1][0], rstd, w.cuda(), grad_residual_out=t[2][0],
+                                          grad_x=t[2 * which][0])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        b = t[2 * which][1].float()
+        assert (b[:16] == 5).all() and (b[16 + 300 * 1029:] == 5).all()
+
+
 def test_backward_repeats_bit_for_bit(cuda_dev):
     h, gh, w = gpu(*inputs(9001, 256, torch.float32, 4))
     gy = torch.randn_like(h)
