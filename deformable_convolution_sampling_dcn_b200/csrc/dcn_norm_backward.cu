@@ -12,7 +12,8 @@
 // timing (no atomics).
 // Measured (one B200): fp32 12800 x 512 with a gradient of the new residual 20.4
 // us (105 MB: 5.1 TB/s; 16.4 us = 6.4 TB/s without a weight), bf16 102400 x 256
-// 38.2 us (210 MB: 5.5 TB/s).
+// 38.2 us (210 MB: 5.5 TB/s); off 16-byte boundaries fp16 5734 x 4383 73 us (201 MB: 2.8 TB/s; one CTA of 9 warps an
+// SM), fp32 4001 x 6001 69 us (384 MB: 5.6 TB/s).
 #include "dcn_device.h"
 #include "dcn_host.h"
 #include "dcn_launch.h"
@@ -25,13 +26,12 @@ constexpr int kTeamThreads = 512;  // CTA of 8-lane and warp teams
 constexpr int kSms = 148;
 
 // One row of partial sums of the weight gradient from the CTA's first WARPS warps.  Narrow teams add up pairs of
-// warps through shared memory (`sums`, kSumFloats), halving their number each time; 8-lane teams of a warp first
+// warps through shared memory (`sums`, sum_floats()), halving their number each time; 8-lane teams of a warp first
 // among themselves.
-template <typename T, int NV, int WARPS> constexpr int kSumFloats = (WARPS / 2) * 32 * NV * Storage<T>::kVec;
-template <typename T, int TPR, int NV, int WARPS, bool ELEMS = false>
-__device__ __forceinline__ void store_partial(const NormArgs &a, float2 (&gw)[NV][Storage<T>::kVec / 2], float *sums, int t,
-                                              int tpr, int shift = 0) {
-    constexpr int VEC = Storage<T>::kVec;
+constexpr int sum_floats(int columns, int warps) { return (warps / 2) * 32 * columns; }  // columns of a thread
+template <int TPR, int NV, int VEC, int WARPS, bool ELEMS = false>
+__device__ __forceinline__ void store_partial(const NormArgs &a, float2 (&gw)[NV][VEC / 2], float *sums, int t, int tpr,
+                                              int shift = 0) {
     float *part = a.partial + (long long)blockIdx.x * a.cols;
     if constexpr (TPR != 0) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -100,7 +100,7 @@ __device__ __forceinline__ void load_weight(const NormArgs &a, int t, int tpr, f
 // while it works on the current one.
 template <typename T> __global__ void __launch_bounds__(kTeamThreads, 2) norm_backward_narrow_kernel(const NormArgs a) {
     constexpr int VEC = Storage<T>::kVec, TPR = 8, TEAMS = kTeamThreads / TPR;
-    __shared__ __align__(16) float sums[kSumFloats<T, 1, kTeamThreads / 32>];
+    __shared__ __align__(16) float sums[sum_floats(VEC, kTeamThreads / 32)];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
     const T *hp = static_cast<const T *>(a.h), *gyp = static_cast<const T *>(a.grad_out);
@@ -147,27 +147,30 @@ template <typename T> __global__ void __launch_bounds__(kTeamThreads, 2) norm_ba
                           pack16<T>(reinterpret_cast<const float *>(o)));
     }
     if (!a.grad_weight) return;
-    store_partial<T, TPR, 1, kTeamThreads / 32>(a, gw, sums, t, TPR);
+    store_partial<TPR, 1, VEC, kTeamThreads / 32>(a, gw, sums, t, TPR);
 }
 
-// Rows at any alignment, by elements: warp or CTA teams of NV * VEC columns a thread.  Also the widest aligned fp32
-// rows, of which two do not fit the shared memory.
-template <typename T, int TPR, int NV>
-__global__ void __launch_bounds__(TPR == 0 ? 1024 : 256, TPR == 0 ? 1 : 2) norm_backward_elems_kernel(const NormArgs a) {
-    constexpr int VEC = Storage<T>::kVec, C = NV * VEC, WARPS = 8;
-    __shared__ __align__(16) float sums[TPR == 0 ? 64 : kSumFloats<T, NV, WARPS>];
+// Rows at any alignment, by elements: warp or CTA teams of C columns a thread.  Also the widest aligned fp32 rows, of
+// which two do not fit the shared memory.  Nothing is loaded ahead: narrow rows take many warps instead, of as few
+// columns a lane as hold the row (fp16 100000 x 61 24 us, with 8 columns a lane 59; 300000 x 21 55 against 161).
+constexpr int elems_per_sm(int c) { return c <= 4 ? 6 : c <= 8 ? 4 : 2; }
+template <typename T, int TPR, int C>
+__global__ void __launch_bounds__(TPR == 0 ? 1024 : 256, TPR == 0 ? 1 : elems_per_sm(C))
+    norm_backward_elems_kernel(const NormArgs a) {
+    constexpr int WARPS = 8;
+    __shared__ __align__(16) float sums[TPR == 0 ? 64 : sum_floats(C, WARPS)];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
     const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % 32;
     const int teams = TPR == 0 ? 1 : WARPS, team = TPR == 0 ? 0 : (int)threadIdx.x / 32;
     int turn = 0;
     float w[C];
-    float2 gw[NV][VEC / 2];
+    float2 gw[1][C / 2];
     if (a.weight) load_elems<T, C>(static_cast<const T *>(a.weight), t, tpr, a.cols, w);
 #pragma unroll
     for (int k = 0; k < C; ++k) {
         if (!a.weight) w[k] = 1.0f;
-        if (k % 2 == 0) gw[k / VEC][k % VEC / 2] = make_float2(0.0f, 0.0f);
+        if (k % 2 == 0) gw[0][k / 2] = make_float2(0.0f, 0.0f);
     }
     const float inv_cols = 1.0f / (float)a.cols;
     const long long step = (long long)gridDim.x * teams;
@@ -182,8 +185,8 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : 256, TPR == 0 ? 1 : 2) norm_
         for (int k = 0; k < C; ++k) {
             xh[k] *= rstd;
             const float p = gy[k] * xh[k];
-            if (k % 2) gw[k / VEC][k % VEC / 2].y += p;
-            else gw[k / VEC][k % VEC / 2].x += p;
+            if (k % 2) gw[0][k / 2].y += p;
+            else gw[0][k / 2].x += p;
             dot = fmaf(p, w[k], dot);
         }
         dot = -team_reduce<SumOp, TPR>(dot, sums, turn) * inv_cols;
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : 256, TPR == 0 ? 1 : 2) norm_
         }
     }
     if (!a.grad_weight) return;
-    store_partial<T, TPR, NV, WARPS, true>(a, gw, sums, t, tpr);
+    store_partial<TPR, 1, C, WARPS, true>(a, gw, sums, t, tpr);
 }
 
 // A row's products from its staged tensors: xh and grad_out in registers, the weight gradient, and this thread's part
@@ -328,12 +331,12 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, CTAS)
     }
     if (!a.grad_weight) return;
     // every tile has been read: the ring is free (two slots of WARPS rows hold more than the sums of WARPS / 2)
-    store_partial<T, 32, NV, WARPS>(a, gw, reinterpret_cast<float *>(ring), t, 32);
+    store_partial<32, NV, VEC, WARPS>(a, gw, reinterpret_cast<float *>(ring), t, 32);
 }
 
 // Wider rows of up to 8192 columns: a CTA of 16 columns a thread per row, each row of the tensors copied into the ring
-// by one bulk copy (rows off 16-byte boundaries by vectors of the aligned grid, dcn_norm.cuh).  The slot of a row is handed back behind the barrier of the next row's
-// reduction, when the whole CTA is past its output.
+// by one bulk copy (rows off 16-byte boundaries by vectors of the aligned grid, dcn_norm.cuh).  The slot of a row is
+// handed back behind the barrier of the next row's reduction, when the whole CTA is past its output.
 template <typename T, bool SHIFT>
 __global__ void __launch_bounds__(512, 1) norm_backward_wide_kernel(const NormArgs a, int slots, unsigned int *err) {
     constexpr int VEC = Storage<T>::kVec, NV = 16 / VEC;
@@ -398,7 +401,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_wide_kernel(const NormAr
         }
     }
     if (!a.grad_weight) return;
-    store_partial<T, 0, NV, 0>(a, gw, red, t, tpr, sh);
+    store_partial<0, NV, VEC, 0>(a, gw, red, t, tpr, sh);
 }
 
 // grad_weight[c] = sum over the CTAs of the first kernel, in a fixed order: 8
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(kRedX *Y) norm_grad_weight_kernel(const float 
 enum Route { kNarrow, kTiles, kWide, kElems };
 struct Config {
     Route route;
-    int nv, threads, rows, per_sm;  // nv vectors (kElems: groups of VEC columns) a thread
+    int nv, threads, rows, per_sm;  // nv vectors (kElems: columns) a thread
     int shift;                      // 0, or the largest shift of a row, VEC - 1
 };
 // How all tensors' rows lie: on 16-byte boundaries, off them by the same in all tensors, or in any way.
@@ -457,10 +460,10 @@ Config config_of(int cols, int vec, Lie lie) {
         while (per_sm > 1 && 2 * 3 * (span + vec - 1) / vec * 16 > staged_budget(per_sm)) --per_sm;
         return {kWide, nv16, wide, 1, per_sm, shift};
     }
-    if (cols <= 32 * vec) return {kElems, 1, 256, 8, 2, 0};
-    if (cols <= 512) return {kElems, nv16, 256, 8, 2, 0};
+    for (int c = 2; c <= 16; c *= 2)
+        if (cols <= 32 * c) return {kElems, c, 256, 8, elems_per_sm(c), 0};
     const int c = cols <= 8192 ? 8 : 16, threads = ((cols + c - 1) / c + 31) / 32 * 32;  // at most 1024
-    return {kElems, c / vec, threads, 1, 1024 / threads < 8 ? 1024 / threads : 8, 0};
+    return {kElems, c, threads, 1, 1024 / threads < 8 ? 1024 / threads : 8, 0};
 }
 
 int grid_of(int64_t rows, const Config &c) {
@@ -513,7 +516,7 @@ cudaError_t launch_tiles(const NormArgs &a, const Config &c, const DeviceInfo *d
 }
 
 template <typename T> cudaError_t launch_rows(const NormArgs &a, const Config &c, cudaStream_t stream) {
-    constexpr int VEC = Storage<T>::kVec, NVC = 16 / VEC;
+    constexpr int VEC = Storage<T>::kVec;
     const DeviceInfo *dev = device_info();
     if (!dev) return cudaErrorNotSupported;
     switch (c.route) {
@@ -536,10 +539,12 @@ template <typename T> cudaError_t launch_rows(const NormArgs &a, const Config &c
         }
         case kElems:
             if (c.rows > 1)
-                return c.nv == 1 ? launch_plain(norm_backward_elems_kernel<T, 32, 1>, a, c, stream)
-                                 : launch_plain(norm_backward_elems_kernel<T, 32, NVC>, a, c, stream);
-            return c.nv == NVC ? launch_plain(norm_backward_elems_kernel<T, 0, NVC>, a, c, stream)
-                               : launch_plain(norm_backward_elems_kernel<T, 0, NVC / 2>, a, c, stream);
+                return c.nv == 2   ? launch_plain(norm_backward_elems_kernel<T, 32, 2>, a, c, stream)
+                       : c.nv == 4 ? launch_plain(norm_backward_elems_kernel<T, 32, 4>, a, c, stream)
+                       : c.nv == 8 ? launch_plain(norm_backward_elems_kernel<T, 32, 8>, a, c, stream)
+                                   : launch_plain(norm_backward_elems_kernel<T, 32, 16>, a, c, stream);
+            return c.nv == 16 ? launch_plain(norm_backward_elems_kernel<T, 0, 16>, a, c, stream)
+                              : launch_plain(norm_backward_elems_kernel<T, 0, 8>, a, c, stream);
     }
     return cudaErrorInvalidValue;
 }
