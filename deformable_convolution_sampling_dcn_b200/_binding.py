@@ -590,8 +590,11 @@ def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: tor
         grad_weight = torch.empty_like(weight) if grad_weight is None else \
             _like("grad_weight", grad_weight, (cols,), dt, dev)
         if workspace is None:
-            workspace = h.new_empty(_norm_backward_workspace_bytes(rows, cols, eps, _DTYPE_CODE[dt]), dtype=torch.uint8)
-        ws_ptr, ws_bytes = _workspace(workspace, dev)
+            ws_bytes = _norm_backward_workspace_bytes(rows, cols, eps, _DTYPE_CODE[dt])
+            workspace = h.new_empty(ws_bytes, dtype=torch.uint8)
+            ws_ptr = workspace.data_ptr()
+        else:
+            ws_ptr, ws_bytes = _workspace(workspace, dev)
     elif grad_weight is not None:
         raise ValueError("grad_weight without a weight")
     _launch(dev, lib().dcn_add_rms_norm_backward, ctypes.byref(p), grad_out.data_ptr(), h.data_ptr(),
@@ -684,16 +687,21 @@ def _grad_call(grads, out, norm_type, norm, workspace):
         dev = norm.get_device()
     if norm is not None:
         _like("norm", norm, (), torch.float32, dev)
+    if workspace is not None:
+        ws_ptr, ws_bytes = _workspace(workspace, dev)
     if norm is None or workspace is None:
         n, w = grads._new(dev)
-        norm, workspace = n if norm is None else norm, w if workspace is None else workspace
-    return (grads, dev, norm) + _workspace(workspace, dev)
+        if norm is None:
+            norm = n
+        if workspace is None:
+            workspace, ws_ptr, ws_bytes = w, w.data_ptr(), grads._ws
+    return grads, dev, norm, workspace, ws_ptr, ws_bytes
 
 
 def dcn_grad_norm(grads, *, norm_type: float = 2.0, norm=None, workspace=None) -> torch.Tensor:
     """The 2-norm (or largest magnitude, norm_type inf) of all gradients together, an fp32 scalar on the
     device; grads is a GradList or a sequence of tensors.  See dcn_b200.h."""
-    grads, dev, norm, ws_ptr, ws_bytes = _grad_call(grads, None, norm_type, norm, workspace)
+    grads, dev, norm, workspace, ws_ptr, ws_bytes = _grad_call(grads, None, norm_type, norm, workspace)
     p = DclipParams(grads.count, _NORM_KIND[norm_type], 0.0, 1.0)
     _launch(dev, lib().dcn_grad_norm, ctypes.byref(p), grads._g, grads._n, grads._d, norm.data_ptr(),
             ws_ptr, ws_bytes)
@@ -704,7 +712,7 @@ def dcn_clip_grads(grads, max_norm: float, *, norm_type: float = 2.0, eps: float
                    workspace=None) -> torch.Tensor:
     """Scales all gradients by min(1, max_norm / (norm + eps)), in place or into `out`, and returns the norm
     before that (fp32 scalar on the device; nothing synchronises).  See dcn_b200.h."""
-    grads, dev, norm, ws_ptr, ws_bytes = _grad_call(grads, out, norm_type, norm, workspace)
+    grads, dev, norm, workspace, ws_ptr, ws_bytes = _grad_call(grads, out, norm_type, norm, workspace)
     p = DclipParams(grads.count, _NORM_KIND[norm_type], max_norm, eps)
     _launch(dev, lib().dcn_clip_grads, ctypes.byref(p), grads._g, grads._n, grads._d, grads._o, grads._od,
             norm.data_ptr(), ws_ptr, ws_bytes)
@@ -738,7 +746,7 @@ def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optio
     if len(ws) != 2 or len(sa) != 3 or len(sr) != 1:
         raise ValueError("weight must be [cout, cin], a [adapters, rank, cin], request_adapter [requests]")
     cout, na, rank, nr = ws[0], sa[0], sa[1], sr[0]
-    if max(cout, na, rank, nr) > _INT32_MAX:
+    if cout > _INT32_MAX or na > _INT32_MAX or rank > _INT32_MAX or nr > _INT32_MAX:
         raise ValueError("a size exceeds 32 bits")
     _like("weight", weight, (cout, cin), dt, dev)
     if bias is not None:
@@ -749,17 +757,19 @@ def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optio
     _like("request_adapter", request_adapter, (nr,), torch.int32, dev)
     if scale is not None:
         _like("scale", scale, (na,), torch.float32, dev)
-    shape = x.shape[:-1] + (cout,)
     if out is not None:
-        _like("out", out, shape, dt, dev)
+        _like("out", out, x.shape[:-1] + (cout,), dt, dev)
     else:
-        out = torch.empty_like(x) if cout == cin else x.new_empty(shape)
+        out = torch.empty_like(x) if cout == cin else x.new_empty(x.shape[:-1] + (cout,))
     sizes = (rows, cin, cout, rank, na, nr, _DTYPE_CODE[dt])
     p = DadaptParams(*sizes)
     L = lib()
     if workspace is None:
-        workspace = x.new_empty(_adapters_workspace_bytes(*sizes), dtype=torch.uint8)
-    ws_ptr, ws_bytes = _workspace(workspace, dev)
+        ws_bytes = _adapters_workspace_bytes(*sizes)
+        workspace = x.new_empty(ws_bytes, dtype=torch.uint8)
+        ws_ptr = workspace.data_ptr()
+    else:
+        ws_ptr, ws_bytes = _workspace(workspace, dev)
     _launch(dev, L.dcn_proj_adapters_forward, ctypes.byref(p), x.data_ptr(), weight.data_ptr(),
             None if bias is None else bias.data_ptr(), a.data_ptr(), b.data_ptr(),
             None if scale is None else scale.data_ptr(), request_start.data_ptr(), request_adapter.data_ptr(),
