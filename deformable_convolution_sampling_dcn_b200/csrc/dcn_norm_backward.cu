@@ -250,7 +250,7 @@ __device__ __forceinline__ void staged_output(const RowVecs<T, SHIFT, true> &in,
 
 constexpr int kMaxSlots = 8;
 
-// Rows of up to 128 vectors, 16-byte aligned: WARPS rows at a time, one per warp, are contiguous in memory, and a
+// Rows of up to 512 columns, 16-byte aligned: WARPS rows at a time, one per warp, are contiguous in memory, and a
 // further warp copies such tiles of the two or three tensors into a ring in shared memory, one bulk copy each
 // (copies of single rows measured 51 us on bf16 102400 x 256, tiles 38.2 us).
 template <typename T, int NV, int WARPS, int CTAS>
@@ -443,19 +443,21 @@ Config config_of(int cols, int vec, Lie lie) {
     const bool aligned = lie == kAligned;
     const int nvec = (cols + vec - 1) / vec, nv16 = 16 / vec;
     if (aligned && nvec <= 8) return {kNarrow, 1, kTeamThreads, kTeamThreads / 8, 2, 0};
-    if (aligned && nvec <= 128) {
+    if (aligned && cols <= 512) {
         // columns a thread -> registers -> warps: 72 registers for two CTAs of 13 warps, 112 for one of 17
-        const int nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4, c = nv * vec;
-        if (c <= 8) return {kTiles, nv, 13 * 32, 12, 2, 0};
-        if (c <= 16) return {kTiles, nv, 17 * 32, 16, 1, 0};
-        return {kTiles, nv, 13 * 32, 12, 1, 0};
+        const int nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4;
+        if (nv * vec <= 8) return {kTiles, nv, 13 * 32, 12, 2, 0};
+        return {kTiles, nv, 17 * 32, 16, 1, 0};
     }
     const int shift = aligned ? 0 : vec - 1, span = cols + shift;  // columns of a row's vectors
     // fp32 rows in step gain from 2048 columns on (9093 x 2047 54.7 us against 51.8 by elements, 7001 x 3001 59.5 against
-    // 64.4, 4001 x 6001 68 against 90), 16 bits at all widths (fp16 20011 x 1101 63 against 67, 4001 x 6001 57 against 95)
-    if (span <= 8192 && (aligned ? nvec > 128 : lie == kInStep && cols > (vec == 4 ? 2048 : 1024))) {
+    // 64.4, 4001 x 6001 68 against 90), 16 bits from 1024 (fp16 20011 x 1101 63 against 67, 4001 x 6001 57 against 95;
+    // below, 30011 x 769 57 against 74, but 2000 x 1001 15 against 11)
+    if (span <= 8192 && (aligned || (lie == kInStep && cols > (vec == 4 ? 2048 : 1024)))) {
         const int wide = ((span + 15) / 16 + 31) / 32 * 32;  // threads of a CTA for a row, 16 columns each
-        int per_sm = 512 / wide < 4 ? 512 / wide : 4;
+        // 16 bits up to 1024 columns: 30011 x 600 53 us in tiles (32 columns a lane), 34 so; fp32 is at the copy rate with 4
+        const int cap = vec == 8 && cols <= 1024 ? 8 : 4;
+        int per_sm = 512 / wide < cap ? 512 / wide : cap;
         // fewer CTAs where two staged rows of three tensors would not fit their share of the shared memory
         while (per_sm > 1 && 2 * 3 * (span + vec - 1) / vec * 16 > staged_budget(per_sm)) --per_sm;
         return {kWide, nv16, wide, 1, per_sm, shift};
@@ -469,6 +471,9 @@ Config config_of(int cols, int vec, Lie lie) {
 int grid_of(int64_t rows, const Config &c) {
     const int64_t need = (rows + c.rows - 1) / c.rows;
     int64_t most = (int64_t)kSms * c.per_sm;
+    // narrow rows' many CTAs: four rows each at least, or their partial sums cost more than they give (fp16 1000 x 600 9.2 us
+    // with a row each, 6.9 so)
+    if (c.route == kWide && c.per_sm > 4 && most > rows / 4) most = rows / 4 > kSms ? rows / 4 : kSms;
     most -= most % (c.shift + 1);  // shifted: a CTA's rows have the same shift
     return (int)(need < most ? need : most);
 }
@@ -527,8 +532,7 @@ template <typename T> cudaError_t launch_rows(const NormArgs &a, const Config &c
                 if (c.nv == 2) return launch_tiles<T, 2, 12, 2>(a, c, dev, stream);
                 return launch_tiles<T, 4, 16, 1>(a, c, dev, stream);
             } else {
-                if (c.nv == 2) return launch_tiles<T, 2, 16, 1>(a, c, dev, stream);
-                return launch_tiles<T, 4, 12, 1>(a, c, dev, stream);
+                return launch_tiles<T, 2, 16, 1>(a, c, dev, stream);
             }
         case kWide: {
             static std::atomic<bool> ok[kMaxDev], shift_ok[kMaxDev];
