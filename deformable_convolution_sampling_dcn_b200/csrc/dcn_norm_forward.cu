@@ -4,7 +4,7 @@
 //   rstd = 1 / sqrt(mean_c(h^2) + eps)
 //   y    = h * rstd * weight
 //   8 bit: s = max(max|y| / top, 2^-126) over the row or over 128 columns,
-//          q = rnd(y * (1 / s)), top = 448 (e4m3) or 127 (int8)
+//          q = rnd(y / s), top = 448 (e4m3) or 127 (int8)
 // h is rounded to the storage type first because that is the value the next
 // block's residual and the backward pass read; everything after it is fp32 and
 // rounded once.
@@ -12,9 +12,9 @@
 // Bound: device memory.  One pass: a row stays in the registers of its team
 // between the statistics and the output, so each byte moves once.  Measured (one
 // B200): bf16 102400 x 256 with a residual 34.4 us (210 MB: 6.1 TB/s of 6.56),
-// fp16 12800 x 512 to e4m3 8.9 us (46 MB: 5.2 TB/s), bf16 2047 x 4096 to int8 in
-// groups 14.0 us (59 MB: 4.2 TB/s); off 16-byte boundaries fp16 5734 x 4383 with a
-// residual 39.7 us (201 MB: 5.1 TB/s), to int8 in groups 57 us, where the
+// fp16 12800 x 512 to e4m3 9.8 us (46 MB: 4.7 TB/s), bf16 2047 x 4096 to int8 in
+// groups 14.9 us (59 MB: 4.0 TB/s); off 16-byte boundaries fp16 5734 x 4383 with a
+// residual 39.7 us (201 MB: 5.1 TB/s), to int8 in groups 64 us, where the
 // instructions bound it.
 #include <cuda_fp8.h>
 
@@ -26,37 +26,93 @@
 namespace dcnb {
 namespace {
 
-constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126: 1 / s stays finite, an all-zero row gives q = 0
+constexpr float kScaleMin = 1.17549435e-38f;  // 2^-126: a normal number, an all-zero row gives q = 0
 
-// Four values to four 8-bit codes, in memory order.  int8 rounds by adding
-// 1.5 * 2^23 in the fused product: the low byte of the sum is the rounded value
-// (|y * inv| <= 127 * (1 + 2^-22)).
-__device__ __forceinline__ uint32_t pack8(const float *y, const float *inv, int quant) {
+// Four values times `f` to four 8-bit codes, in memory order.  int8 rounds by
+// adding 1.5 * 2^23 in the fused product: the low byte of the sum is the rounded
+// value (|v * f| <= 127 * (1 + 2^-20)).
+__device__ __forceinline__ uint32_t pack8(float2 v0, float2 v1, float f, int quant) {
+    const float2 ff = make_float2(f, f);
     if (quant == kQuantE4M3) {
-        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv[0], y[1] * inv[1]),
-                                                                 __NV_SATFINITE, __NV_E4M3);
-        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv[2], y[3] * inv[3]),
-                                                                 __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(f2_mul(v0, ff), __NV_SATFINITE, __NV_E4M3);
+        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(f2_mul(v1, ff), __NV_SATFINITE, __NV_E4M3);
         return (uint32_t)lo | ((uint32_t)hi << 16);
     }
-    uint32_t q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = __float_as_uint(fmaf(y[i], inv[i], 12582912.0f));
-    return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+    const float2 round = make_float2(12582912.0f, 12582912.0f);
+    const float2 q0 = f2_fma(v0, ff, round), q1 = f2_fma(v1, ff, round);
+    return __byte_perm(__byte_perm(__float_as_uint(q0.x), __float_as_uint(q0.y), 0x0040),
+                       __byte_perm(__float_as_uint(q1.x), __float_as_uint(q1.y), 0x0040), 0x5410);
 }
 
-// The codes of a thread's vector at columns c ..; row + c is a multiple of VEC.  The first `lo` elements take the
-// factor `before`, the others `inv`.
+// A code is the quotient y / s, divided in fp32 and rounded once more.  A product
+// with 1 / s is off by up to 1.5 steps of fp32, which puts some values on the other
+// side of a border between two codes; but a product 2^-21 below it and one as far
+// above have the quotient between them, so where both give the same code it is the
+// quotient's (rounding is monotonic), and only the others, a vector in some ten
+// thousand, divide.  (bf16 2047 x 4096 to int8: 14.8 us, 13.7 with the products alone,
+// 16.4 with divisions alone.)
+constexpr float kBelow = 1.0f - 0x1p-21f, kAbove = 1.0f + 0x1p-21f;
+
+// A scale and its inverse.
+struct Scale {
+    float s, inv;
+};
+__device__ __forceinline__ Scale with_inverse(float s) { return {s, 1.0f / s}; }
+
+// The codes of N values (a multiple of 4), the first `lo` (SHIFT) with the scale `before`, the others with `s`.
+template <int N, bool SHIFT>
+__device__ __forceinline__ void codes_of(const float *y, Scale s, Scale before, int lo, int quant, uint32_t *q) {
+    const float below = SHIFT ? kBelow : s.inv * kBelow, above = SHIFT ? kAbove : s.inv * kAbove;
+    uint32_t differ = 0;
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            float2 v[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = 4 * k + 2 * i;
+                v[i] = f2_mul(make_float2(y[j], y[j + 1]), make_float2(j < lo ? before.inv : s.inv, j + 1 < lo ? before.inv : s.inv));
+            }
+            q[k] = pack8(v[0], v[1], below, quant);
+            differ |= q[k] ^ pack8(v[0], v[1], above, quant);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            const float2 v0 = make_float2(y[4 * k], y[4 * k + 1]), v1 = make_float2(y[4 * k + 2], y[4 * k + 3]);
+            q[k] = pack8(v0, v1, below, quant);
+            differ |= q[k] ^ pack8(v0, v1, above, quant);
+        }
+    }
+    if (differ) {
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = y[4 * k + i] / (SHIFT && 4 * k + i < lo ? before.s : s.s);
+            q[k] = pack8(make_float2(v[0], v[1]), make_float2(v[2], v[3]), 1.0f, quant);
+        }
+    }
+}
+
+// The same for one value.
+__device__ __forceinline__ unsigned char code1(float v, float f, int quant) {
+    if (quant == kQuantE4M3) return __nv_cvt_float_to_fp8(v * f, __NV_SATFINITE, __NV_E4M3);
+    return (unsigned char)__float_as_uint(fmaf(v, f, 12582912.0f));
+}
+__device__ __forceinline__ unsigned char code_of(float y, Scale s, int quant) {
+    const unsigned char q = code1(y, s.inv * kBelow, quant);
+    return q == code1(y, s.inv * kAbove, quant) ? q : code1(y / s.s, 1.0f, quant);
+}
+
+// The codes of a thread's vector at columns c ..; row + c is a multiple of VEC.  The first `lo` elements have the
+// scale `before`, the others `s`.
 template <int VEC, bool SHIFT>
-__device__ __forceinline__ void store_codes(unsigned char *row, int c, int cols, const float *y, float inv, float before,
+__device__ __forceinline__ void store_codes(unsigned char *row, int c, int cols, const float *y, Scale s, Scale before,
                                             int lo, int quant) {
     if (c >= cols) return;
-    float f[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] = SHIFT && j < lo ? before : inv;
     uint32_t q[VEC / 4];
-#pragma unroll
-    for (int k = 0; k < VEC / 4; ++k) q[k] = pack8(y + 4 * k, f + 4 * k, quant);
+    codes_of<VEC, SHIFT>(y, s, before, lo, quant, q);
     if (!SHIFT || (c >= 0 && c + VEC <= cols)) {
         if constexpr (VEC == 8) *reinterpret_cast<uint2 *>(row + c) = make_uint2(q[0], q[1]);
         else *reinterpret_cast<uint32_t *>(row + c) = q[0];
@@ -208,14 +264,14 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float inv0 = 0.0f;
+                Scale s0 = {};
                 if (SHIFT && grouped) {
                     const float here = __shfl_sync(0xffffffffu, s[i], 15);
                     const float last = __shfl_sync(0xffffffffu, s[i ? i - 1 : 0], 31);
-                    if (t % GL == 0) inv0 = 1.0f / (GL == 16 && t == 16 ? here : last);
+                    if (t % GL == 0) s0 = with_inverse(GL == 16 && t == 16 ? here : last);
                 }
-                store_codes<VEC, SHIFT>(static_cast<unsigned char *>(a.out8) + off, column(i), cols, y[i], 1.0f / s[i],
-                                        inv0, grouped && t % GL == 0 ? sh : 0, a.quant);
+                store_codes<VEC, SHIFT>(static_cast<unsigned char *>(a.out8) + off, column(i), cols, y[i], with_inverse(s[i]), s0,
+                                        grouped && t % GL == 0 ? sh : 0, a.quant);
             }
         }
     }
@@ -223,7 +279,7 @@ __global__ void __launch_bounds__(kTeamThreads, ctas_per_sm(NV * Storage<T>::kVe
 
 // Rows wider than a warp team holds: a CTA of 16 columns a thread per row, the
 // rows staged by bulk copies (bf16 2047 x 4096 to int8: 16.8 us with the next
-// row's loads in registers, 14.0 us staged).  A shifted row's groups of 128
+// row's loads in registers, 14.0 us staged, before the codes were quotients).  A shifted row's groups of 128
 // columns begin inside vectors, so their maxima meet in shared memory.
 template <typename T, bool QUANT, bool SHIFT>
 __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormArgs a, int slots, unsigned int *err) {
@@ -231,9 +287,9 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ float red[64];
     __shared__ __align__(8) uint64_t bars[kMaxSlots];
-    // shifted rows: maxima of the groups (bits of values >= 0) and the factors that follow from them
+    // shifted rows: maxima of the groups (bits of values >= 0) and the scales that follow from them, with their inverses
     __shared__ int gmax_s[QUANT && SHIFT ? 128 : 1];
-    __shared__ float inv_s[QUANT && SHIFT ? 128 : 1];
+    __shared__ Scale scale_s[QUANT && SHIFT ? 128 : 1];
     const int t = threadIdx.x, tpr = blockDim.x;
     const T *weight = static_cast<const T *>(a.weight);
     const long long step = gridDim.x, total = a.rows * a.cols;  // SHIFT: step is a multiple of VEC, or no CTA has two rows
@@ -324,11 +380,10 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
             }
         }
         if constexpr (QUANT) {
-            float inv = 0.0f, inv0 = 0.0f;
+            Scale s8 = {}, s0 = {};
             if (!a.group) {
-                const float sc = scale_of(team_reduce<MaxOp, 0>(amax, red, turn), a.quant);
-                inv = 1.0f / sc;
-                if (t == 0) a.scale[r] = sc;
+                s8 = with_inverse(scale_of(team_reduce<MaxOp, 0>(amax, red, turn), a.quant));
+                if (t == 0) a.scale[r] = s8.s;
             } else if (SHIFT) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -341,7 +396,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
                 for (int i = t; i < a.groups; i += tpr) {
                     const float sc = scale_of(__int_as_float(gmax_s[i]), a.quant);
                     a.scale[r * a.groups + i] = sc;
-                    inv_s[i] = 1.0f / sc;
+                    scale_s[i] = with_inverse(sc);
                     gmax_s[i] = 0;
                 }
                 __syncthreads();
@@ -350,15 +405,14 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_wide_kernel(const NormAr
             for (int i = 0; i < NV; ++i) {
                 const int v = t + i * tpr, c = column(i);
                 if (a.group && !SHIFT) {
-                    const float sc = scale_of(lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]), a.quant);
-                    inv = 1.0f / sc;
-                    if (v % GL == 0 && c < a.cols) a.scale[r * a.groups + c / 128] = sc;
+                    s8 = with_inverse(scale_of(lanes_reduce<MaxOp, (GL < 32 ? GL : 32)>(gmax[i]), a.quant));
+                    if (v % GL == 0 && c < a.cols) a.scale[r * a.groups + c / 128] = s8.s;
                 } else if (a.group) {
                     // a vector behind the start of a group that is not there only holds the end of the last one
-                    inv = inv_s[min(v / GL, a.groups - 1)];
-                    if (lo && v && c < a.cols) inv0 = inv_s[v / GL - 1];
+                    s8 = scale_s[min(v / GL, a.groups - 1)];
+                    if (lo && v && c < a.cols) s0 = scale_s[v / GL - 1];
                 }
-                store_codes<VEC, SHIFT>(static_cast<unsigned char *>(a.out8) + off, c, a.cols, y[i], inv, inv0, lo, a.quant);
+                store_codes<VEC, SHIFT>(static_cast<unsigned char *>(a.out8) + off, c, a.cols, y[i], s8, s0, lo, a.quant);
             }
         }
     }
@@ -369,9 +423,9 @@ template <typename T, int TPR, int C, bool QUANT>
 __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 ? 1 : ctas_per_sm(C))
     norm_forward_elems_kernel(const NormArgs a) {
     __shared__ float red[64];
-    // maxima of the groups (bits of values >= 0, two rows' sets) and the factors that follow from them
+    // maxima of the groups (bits of values >= 0, two rows' sets), the scales that follow from them and their inverses
     __shared__ int gmax_s[2][TPR == 0 && QUANT ? 128 : 1];
-    __shared__ float inv_s[TPR == 0 && QUANT ? 128 : 1];
+    __shared__ Scale scale_s[TPR == 0 && QUANT ? 128 : 1];
     const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
     const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % 32;
     const int teams = TPR == 0 ? 1 : kTeamThreads / 32, team = TPR == 0 ? 0 : (int)threadIdx.x / 32;
@@ -416,12 +470,10 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 ? 1 :
             }
         }
         if constexpr (QUANT) {
-            const float top = a.quant == kQuantE4M3 ? 448.0f : 127.0f;
-            float s = 0.0f, inv = 0.0f;
+            Scale s = {};
             if (!a.group) {
-                s = max_nan(team_reduce<MaxOp, TPR>(amax, red, turn) / top, kScaleMin);
-                inv = 1.0f / s;
-                if (t == 0) a.scale[r] = s;
+                s = with_inverse(scale_of(team_reduce<MaxOp, TPR>(amax, red, turn), a.quant));
+                if (t == 0) a.scale[r] = s.s;
             } else if (TPR == 0) {
                 // 32 columns of a warp lie in one group
 #pragma unroll
@@ -432,9 +484,9 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 ? 1 :
                 }
                 __syncthreads();
                 for (int i = t; i < a.groups; i += tpr) {
-                    s = max_nan(__int_as_float(gmax_s[set][i]) / top, kScaleMin);
-                    inv_s[i] = 1.0f / s;
-                    a.scale[r * a.groups + i] = s;
+                    s = with_inverse(scale_of(__int_as_float(gmax_s[set][i]), a.quant));
+                    scale_s[i] = s;
+                    a.scale[r * a.groups + i] = s.s;
                     gmax_s[set ^ 1][i] = 0;  // the next row's, last read two barriers ago
                 }
                 __syncthreads();
@@ -445,20 +497,18 @@ __global__ void __launch_bounds__(TPR == 0 ? 1024 : kTeamThreads, TPR == 0 ? 1 :
             for (int k = 0; k < C; ++k) {
                 const int c = k * tpr + t;
                 if (a.group && TPR == 0) {
-                    inv = inv_s[c < a.cols ? c / 128 : 0];
+                    s = scale_s[c < a.cols ? c / 128 : 0];
                 } else if (a.group && k % 4 == 0) {
                     // a warp's values k .. k + 3 are 128 columns
                     float m = fabsf(y[k]);
 #pragma unroll
                     for (int q = 1; q < 4; ++q)
                         if (k + q < C) m = max_nan(m, fabsf(y[k + q]));
-                    s = max_nan(lanes_reduce<MaxOp, 32>(m) / top, kScaleMin);
-                    inv = 1.0f / s;
-                    if (t == 0 && c < a.cols) a.scale[r * a.groups + k / 4] = s;
+                    s = with_inverse(scale_of(lanes_reduce<MaxOp, 32>(m), a.quant));
+                    if (t == 0 && c < a.cols) a.scale[r * a.groups + k / 4] = s.s;
                 }
                 if (c < a.cols) {
-                    const float q4[4] = {y[k], 0.0f, 0.0f, 0.0f}, f4[4] = {inv, 0.0f, 0.0f, 0.0f};
-                    dst[c] = (unsigned char)pack8(q4, f4, a.quant);
+                    dst[c] = code_of(y[k], s, a.quant);
                 }
             }
         }

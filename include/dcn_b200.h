@@ -343,13 +343,13 @@ int64_t dcn_proj_adapters_workspace_bytes(const dadapt_params *p);
  *   h    = rnd(x + residual)            residual_out; h = x without a residual
  *   rstd = 1 / sqrt(mean_c(h^2) + eps)
  *   y    = h * rstd * weight            out; weight NULL: h * rstd
- *   out8 = rnd(y * (1 / scale)),  scale = max(max|y| / top, 2^-126)
+ *   out8 = rnd(y / scale),  scale = max(max|y| / top, 2^-126)
  * with the maximum over the row (group = 0) or over each 128 neighbouring
  * columns (group = 128; the last group of a row may be shorter), top = 448
  * (DCN_QUANT_E4M3, saturating) or 127 (DCN_QUANT_INT8); out8 * scale is y up
  * to the 8-bit rounding.  h is the fp32 sum, rounded to the storage type before
  * the norm is taken of it; everything after that is fp32 and rounded once, 8-bit codes
- * from the fp32 value.
+ * from the fp32 quotient.
  *   x, residual, residual_out, out  [rows, cols]  storage dtype
  *   weight                          [cols]        storage dtype, or NULL
  *   out8                            [rows, cols]  one byte each

@@ -521,3 +521,21 @@ def test_binding_refusals(cuda_dev):
     with pytest.raises(d.DcnError):
         d.dcn_add_rms_norm_backward(x, x, torch.ones(4, device="cuda"), torch.ones(64, device="cuda"),
                                     workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("quant", ["e4m3", "int8"])
+@pytest.mark.parametrize("cols,k", [(32, 0), (61, 0), (128, 0), (256, 0), (250, 1), (300, 3), (512, 0), (1000, 2),
+                                    (1001, 0), (4096, 0), (4383, 1), (9001, 0)])
+def test_codes_are_the_rounded_quotients(cols, k, quant, group, cuda_dev):
+    """In fp32 `out` is the value that the codes are made of: they are out / scale, divided and rounded once each, with
+    no step between (a product with 1 / scale puts some values on the other side of a border)."""
+    x, r, w = inputs(4001, cols, torch.float32, cols + 5)
+    place = gpu if k == 0 else lambda *ts: [step_off(t, k, 0.0)[0] for t in ts]
+    o = d.dcn_add_rms_norm_forward(*place(x, r, w), eps=EPS, quant=quant, group=group, keep_out=True)
+    s = o.scale.cpu().repeat_interleave(group or cols, 1)[:, :cols]
+    v = o.out.cpu() / s
+    if quant == "e4m3":
+        assert torch.equal(o.out8.cpu().view(torch.uint8), v.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    else:
+        assert torch.equal(o.out8.cpu(), v.round().to(torch.int8))
