@@ -32,7 +32,7 @@ EXPORTS = ("dcn_core_output_hw", "dcn_core_forward", "dcn_core_backward", "defor
            "dcn_core_forward_proj_workspace_bytes", "dcn_core_forward_proj_noalloc",
            "dcn_add_rms_norm_forward", "dcn_add_rms_norm_backward", "dcn_add_rms_norm_backward_workspace_bytes",
            "dcn_grad_norm", "dcn_clip_grads", "dcn_grad_norm_workspace_bytes",
-           "dcn_proj_adapters_forward", "dcn_proj_adapters_workspace_bytes")
+           "dcn_proj_adapters_forward", "dcn_proj_adapters_workspace_bytes", "dcn_proj_adapters_workspace_full_bytes")
 ABI_VERSION = 2
 
 
@@ -128,8 +128,9 @@ def _declare(lib):
     R = ctypes.POINTER(DadaptParams)
     lib.dcn_proj_adapters_forward.argtypes = [R, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp]
     lib.dcn_proj_adapters_forward.restype = st
-    lib.dcn_proj_adapters_workspace_bytes.argtypes = [R]
-    lib.dcn_proj_adapters_workspace_bytes.restype = ctypes.c_int64
+    for f in ("dcn_proj_adapters_workspace_bytes", "dcn_proj_adapters_workspace_full_bytes"):
+        getattr(lib, f).argtypes = [R]
+        getattr(lib, f).restype = ctypes.c_int64
     return lib
 
 
@@ -721,8 +722,8 @@ def dcn_clip_grads(grads, max_norm: float, *, norm_type: float = 2.0, eps: float
 
 @functools.lru_cache(maxsize=1024)
 def _adapters_workspace_bytes(*sizes) -> int:
-    """Workspace of a problem of these sizes (a function of them alone); 16 where they are refused."""
-    return max(16, lib().dcn_proj_adapters_workspace_bytes(ctypes.byref(DadaptParams(*sizes))))
+    """Workspace of a problem of these sizes (a function of them alone) in one pass; 16 where they are refused."""
+    return max(16, lib().dcn_proj_adapters_workspace_full_bytes(ctypes.byref(DadaptParams(*sizes))))
 
 
 def dcn_proj_adapters_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor],

@@ -624,6 +624,12 @@ int64_t dcn_proj_adapters_workspace_bytes(const dadapt_params *p) {
     return (int64_t)dcnb::proj_adapters_workspace(a);
 }
 
+int64_t dcn_proj_adapters_workspace_full_bytes(const dadapt_params *p) {
+    dcnb::AdapterArgs a;
+    if (check_adapters(p, &a) != DCN_OK) return -1;
+    return (int64_t)dcnb::proj_adapters_workspace_full(a);
+}
+
 dcn_status dcn_proj_adapters_forward(const dadapt_params *p, const void *x, const void *weight, const void *bias,
                                      const void *a, const void *b, const float *scale, const int32_t *request_start,
                                      const int32_t *request_adapter, void *out, void *workspace,
@@ -646,7 +652,7 @@ dcn_status dcn_proj_adapters_forward(const dadapt_params *p, const void *x, cons
         return fail(DCN_ERR_SHAPE, "workspace has %lld bytes, %zu needed", (long long)workspace_bytes, need);
     g.x = x; g.weight = weight; g.bias = bias; g.a = a; g.b = b; g.scale = scale;
     g.start = request_start; g.which = request_adapter;
-    g.out = out; g.workspace = workspace;
+    g.out = out; g.workspace = workspace; g.workspace_bytes = (size_t)workspace_bytes;
     return cuda_status(dcnb::launch_proj_adapters(g, (cudaStream_t)stream), "dcn_proj_adapters_forward launch");
 }
 

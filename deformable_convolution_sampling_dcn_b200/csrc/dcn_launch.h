@@ -100,7 +100,8 @@ struct AdapterArgs {
     const float *scale;             // [adapters] or nullptr (ones)
     const int32_t *start, *which;   // [requests + 1] row starts, [requests] adapters
     void *out;                      // [rows, cout]
-    void *workspace;                // proj_adapters_workspace() bytes
+    void *workspace;
+    size_t workspace_bytes;         // proj_adapters_workspace() at least, proj_adapters_workspace_full() for one pass
     int64_t rows;
     int cin, cout, rank, adapters, requests;
     DType dtype;
@@ -142,5 +143,6 @@ cudaError_t launch_grad_clip(const ClipArgs &a, cudaStream_t stream);
 int64_t grad_clip_partials(int num_tensors);
 cudaError_t launch_proj_adapters(const AdapterArgs &a, cudaStream_t stream);
 size_t proj_adapters_workspace(const AdapterArgs &a);
+size_t proj_adapters_workspace_full(const AdapterArgs &a);
 
 }  // namespace dcnb

@@ -10,9 +10,15 @@
 // carry an infinity of one request's adapter into its neighbours' rows).
 //
 // SHRINK forms t for every pair (tile of 128 rows, request in it) and stores
-// the request's rows, scaled and then rounded once to the storage type, which
-// the operands of the second product have.  Along the rows either the tile or
-// the request advances, so tile + request numbers the pairs.
+// the request's rows, scaled.  The operands of the second product have the
+// storage type, so t is held in 32 bits as the sum of two values of it, t rounded
+// and the rest rounded (22 bits of mantissa in fp16, 16 in bf16, against 11 and 8
+// of one value: bf16 16111 rows 2048 -> 2048, rank 64, the error against 64 bits
+// 1.84e-3 with one value, 1.66e-3 with two, which is the output's own rounding).
+// fp16 has no room above 65504: eight neighbours of a row of t that go beyond 2^15
+// are scaled down by a power of two, whose exponent is kept, and EXPAND adds what is
+// missing in fp32 when it finishes the row.  Along the rows either the tile or the request
+// advances, so tile + request numbers the pairs.
 //
 // EXPAND runs over the tiles of y: the blocks of x and W first, then those of t
 // and B.  A tile is 256 rows x BN channels by a pair of CTAs (cta_group::2):
@@ -21,6 +27,10 @@
 // (128 x 256 tiles of single CTAs: 48 KB for 128 x 256 x 64).  EXPAND is a
 // programmatic dependent of SHRINK and waits for it only before its first load
 // of t.
+//
+// The two values of t take twice the least workspace of a call.  With less than
+// that the rows go in several passes, two launches each, with t of one pass at a
+// time.
 //
 // Where the tiles are fewer than the SMs, a cluster of CTAs (SHRINK) or of pairs
 // (EXPAND) splits the contraction of one tile; the parts meet in distributed
@@ -34,10 +44,10 @@
 // finish it and store.  Every wait is bounded and gives up when another role of
 // the CTA has aborted.
 //
-// Measured (one B200): fp16 12800 rows 512 -> 512, rank 16 21 us (338 TFLOP/s,
+// Measured (one B200): fp16 12800 rows 512 -> 512, rank 16 21.5 us (330 TFLOP/s,
 // bound by the chain of latencies of the two launches and by fetches from L2);
-// bf16 16111 rows 2048 -> 2048, rank 64 120 us (1.2 PFLOP/s), 97 us of it the
-// products with W.
+// bf16 16111 rows 2048 -> 2048, rank 64 128 us (1.1 PFLOP/s), 97 us of it the
+// products with W.  With t rounded to one value they took 21.1 and 121 us.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
@@ -64,7 +74,12 @@ struct LargeParams {
     const int32_t *start, *which;
     const float *scale;
     const void *bias;
-    void *t;               // [rows, rank]
+    // this pass: rows row0 .. row0 + rows - 1 of the request table, t [2, rows, rank] and (fp16) the exponents of its
+    // eighths [rows, 16], both for rows with an adapter only; out starts at row0
+    int row0;
+    void *t;
+    unsigned char *shift;
+    const void *b;
     void *out;
     int NT;                // EXPAND: tiles of output channels
     int BN;                // EXPAND: output channels of a tile; SHRINK: rank rounded up to 16
@@ -75,11 +90,11 @@ struct LargeParams {
     unsigned int *err;
 };
 
-// A request's rows inside [0, rows), from the table (in shared or global memory).
+// A request's rows inside [0, rows) of this pass, from the table (in shared or global memory).
 struct Requests {
     const int32_t *start, *which;
-    int count, rows, adapters;
-    __device__ __forceinline__ int at(int s) const { return min(max(start[s], 0), rows); }
+    int count, row0, rows, adapters;
+    __device__ __forceinline__ int at(int s) const { return min(max(start[s], row0) - row0, rows); }
     __device__ __forceinline__ int adapter(int s) const { return adapter_of(which, s, adapters); }
     // the first request that ends after row r
     __device__ __forceinline__ int first_ending_after(int r) const {
@@ -151,6 +166,7 @@ struct Smem {
         r.start = cached ? cache : p.start;
         r.which = cached ? cache + p.requests + 1 : p.which;
         r.count = p.requests;
+        r.row0 = p.row0;
         r.rows = p.rows;
         r.adapters = p.adapters;
         return r;
@@ -211,11 +227,65 @@ __device__ __forceinline__ void add_splits(uint32_t addr, int c, int splits, int
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+
+constexpr int kShiftBytes = 16;  // of a row: the exponents of its (up to) 128 / 8 groups
+
+// Eight values of t as two of the storage type each, the second of which is the first one's rounding error: exact in
+// fp32, then rounded.  Infinities and NaN are the first value alone.  Returns the exponent of the power of two by which
+// the values are divided, so that the largest finite one stays below 2^15 in fp16; in [0, 113].
+template <typename T> __device__ __forceinline__ uint32_t store_t(T *first, T *second, float *v) {
+    const float inf = __int_as_float(0x7f800000);
+    uint32_t shift = 0;
+    if constexpr (std::is_same<T, __half>::value) {
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fabsf(v[i]) < inf ? fmaxf(m, fabsf(v[i])) : m;
+        shift = (uint32_t)max((int)(__float_as_uint(m) >> 23) - 127 - 14, 0);
+        const float down = __uint_as_float((127 - shift) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= down;
+    } else {
+        // a finite value past the largest of bf16 does not round up to an infinity
+        const float top = __uint_as_float(0x7f7f0000u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(v[i]) < inf) v[i] = fminf(fmaxf(v[i], -top), top);
+    }
+    const uint4 hi = pack16<T>(v);
+    float f[8];
+    unpack16<T>(hi, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = fabsf(f[i]) < inf ? v[i] - f[i] : 0.0f;
+    *reinterpret_cast<uint4 *>(first) = hi;
+    *reinterpret_cast<uint4 *>(second) = pack16<T>(f);
+    return shift;
+}
+
+// What the product with a row of t leaves out for one channel: (2^shift - 1) b . t over the groups with a shift.
+template <typename T>
+__device__ __noinline__ float missing_term(const T *b, const T *first, const T *second, const unsigned char *shift,
+                                           int rank) {
+    float sum = 0.0f;
+    for (int k = 0; k < rank; k += 8) {
+        const uint32_t e = __ldcg(shift + k / 8);
+        if (e == 0) continue;
+        const float mul = __uint_as_float((127 + e) << 23) - 1.0f;
+        float f[8], t0[8], t1[8];
+        unpack16<T>(ld_nc16(b + k), f);
+        unpack16<T>(__ldcg(reinterpret_cast<const uint4 *>(first + k)), t0);
+        unpack16<T>(__ldcg(reinterpret_cast<const uint4 *>(second + k)), t1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(f[i], (t0[i] + t1[i]) * mul, sum);
+    }
+    return sum;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1)
     adapters_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
                            const LargeParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
+    constexpr bool kShifted = std::is_same<T, __half>::value;
     const int sbytes = kABytes + p.BN * kBK * 2;  // BN a multiple of 16: a stage is a multiple of 1 KB
     const Smem sm(smem_raw, p.stages * sbytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -327,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = (int)(j - r) * kBM + quad * 32 + lane, buf = local & 1;
             const bool mine = row >= req.at(r) && row < req.at(r + 1);
             const float mul = p.scale ? p.scale[req.adapter(r)] : 1.0f;
-            T *dst = static_cast<T *>(p.t) + (long long)row * p.rank;
+            T *dst = static_cast<T *>(p.t) + (long long)row * p.rank, *rest = dst + (long long)p.rows * p.rank;
             if (!wait_or_abort(sm.acc_full + 8 * buf, (local >> 1) & 1, sm.abort_flag)) {
                 raise_abort(sm.abort_flag, p.err);
                 break;
@@ -339,14 +409,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  p.BN, 0, 16);
                 break;
             }
+            const uint32_t acc = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * p.BN);
             for (int c = 0; c < p.rank; c += 16) {  // warp-uniform
                 float v[16];
-                tmem_ld16(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(buf * p.BN + c), v);
+                tmem_ld16(acc + (uint32_t)c, v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] *= mul;
                 if (mine) {
-                    *reinterpret_cast<uint4 *>(dst + c) = pack16<T>(v);
-                    if (c + 8 < p.rank) *reinterpret_cast<uint4 *>(dst + c + 8) = pack16<T>(v + 8);
+                    uint32_t shift = store_t<T>(dst + c, rest + c, v);
+                    if (c + 8 < p.rank) shift |= store_t<T>(dst + c + 8, rest + c + 8, v + 8) << 8;
+                    if (kShifted) *reinterpret_cast<uint16_t *>(p.shift + (long long)row * kShiftBytes + c / 8) = (uint16_t)shift;
                 }
             }
             tc_fence_before();
@@ -363,13 +435,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = (int)(job0 - r) * kBM + quad * 32 + lane;
             const float mul = p.scale ? p.scale[req.adapter(r)] : 1.0f;
             const uint32_t addr = smem_u32(sm.ring) + (uint32_t)(quad * 32 + lane) * 4;
+            T *dst = static_cast<T *>(p.t) + (long long)row * p.rank, *rest = dst + (long long)p.rows * p.rank;
             for (int c = 8 * split; c < p.rank; c += 8 * p.splits) {
                 float v[8];
                 add_splits(addr, c, p.splits, 0, 1, v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] *= mul;
-                if (row >= req.at(r) && row < req.at(r + 1))
-                    *reinterpret_cast<uint4 *>(static_cast<T *>(p.t) + (long long)row * p.rank + c) = pack16<T>(v);
+                if (row >= req.at(r) && row < req.at(r + 1)) {
+                    const uint32_t shift = store_t<T>(dst + c, rest + c, v);
+                    if (kShifted) p.shift[(long long)row * kShiftBytes + c / 8] = (unsigned char)shift;
+                }
             }
         }
         __syncwarp();
@@ -396,6 +471,14 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
+                                                 int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
 // Brings a box to L2.
@@ -469,6 +552,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                            const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CUtensorMap bmap,
                            const __grid_constant__ CUtensorMap ymap, const LargeParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
+    constexpr bool kShifted = std::is_same<T, __half>::value;
     const int sbytes = kABytes + p.BN / 2 * kBK * 2;
     const Smem sm(smem_raw, p.stages * sbytes + kOutStage);  // the staged boxes of y follow the ring
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -498,6 +582,29 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     // this pair's part of the contraction; the adapters' blocks belong to the last one
     const int kb0 = blocks * split / p.splits, kb1 = blocks * (split + 1) / p.splits;
     const bool adapters = split == p.splits - 1;
+    // values of t that a stage holds: both where their rows of aw bytes fit the place of the 128-byte rows of x
+    const int held = p.aw < 128 ? 2 : 1;
+    // The adapter of a row of some request whose t has an exponent other than 0, else -1.  The exponents are written for
+    // rows with an adapter only: whether a row has one is asked where they are not zero.
+    auto shifted_row = [&](int row, bool covered) {
+        if (!kShifted || !p.shift || !covered) return -1;
+        const uint4 e = __ldcg(reinterpret_cast<const uint4 *>(p.shift + (long long)row * kShiftBytes));
+        const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int bytes = p.rank / 8 - 4 * i;  // of the word that belong to the rank
+            if (bytes > 0) any |= bytes >= 4 ? w[i] : w[i] & ((1u << (8 * bytes)) - 1);
+        }
+        if (any == 0) return -1;
+        const int r = req.first_ending_after(row);
+        return r < p.requests && req.at(r) <= row ? req.adapter(r) : -1;
+    };
+    auto missing = [&](int row, int ad, int channel) {
+        const T *t = static_cast<const T *>(p.t) + (long long)row * p.rank;
+        return missing_term<T>(static_cast<const T *>(p.b) + ((long long)ad * p.cout + channel) * p.rank, t,
+                               t + (long long)p.rows * p.rank, p.shift + (long long)row * kShiftBytes, p.rank);
+    };
 
     if (warp == 0) {
         // ---- producer: this CTA's rows and half of the channels; both CTAs' loads complete on the first one's
@@ -507,12 +614,14 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             long long issued = 0;
             bool ok = true, waited = false;
             const uint32_t full0 = in_cta(sm.full, leader);
-            auto load = [&](const CUtensorMap *am, int k, int row, const CUtensorMap *bm, int brow, uint32_t bytes) {
+            // the blocks at column k: `value` below 0 of x and W, else of t, from that value of it on, and B
+            auto load = [&](int value, int k, int row, int brow, uint32_t bytes) {
                 if (at.pass >= 1 && !wait_or_abort(sm.empty + 8 * at.s, (at.pass - 1) & 1, sm.abort_flag)) return false;
                 if (rank == 0) mbar_arrive_expect_tx(sm.full + 8 * at.s, 2 * bytes);
                 const uint32_t st = smem_u32(sm.ring) + at.s * sbytes;
-                tma_load_2d_pair(st, am, full0 + 8 * at.s, k, row);
-                tma_load_2d_pair(st + kABytes, bm, full0 + 8 * at.s, k, brow);
+                if (value < 0) tma_load_2d_pair(st, &xmap, full0 + 8 * at.s, k, row);
+                else tma_load_3d_pair(st, &tmap, full0 + 8 * at.s, k, row, value);
+                tma_load_2d_pair(st + kABytes, value < 0 ? &wmap : &bmap, full0 + 8 * at.s, k, brow);
                 ++issued;
                 at.next(p.stages);
                 return true;
@@ -520,7 +629,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             for (long long j = pair0; j < p.jobs && ok; j += pairs) {
                 const int tile = (int)(j / p.NT) * kPairRows, row = tile + rank * kBM;
                 const int n0 = (int)(j % p.NT) * p.BN + rank * (p.BN / 2);
-                for (int kb = kb0; kb < kb1 && ok; ++kb) ok = load(&xmap, kb * kBK, row, &wmap, n0, sbytes);
+                for (int kb = kb0; kb < kb1 && ok; ++kb) ok = load(-1, kb * kBK, row, n0, sbytes);
                 if (!adapters) continue;
                 if (ok && !waited) {
                     // the first tile's B, which does not depend on SHRINK, comes to L2 meanwhile
@@ -536,7 +645,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                     const int ad = req.adapter(r);
                     if (ad < 0 || req.at(r + 1) <= req.at(r)) continue;
                     for (int rb = 0; rb < RB && ok; ++rb)
-                        ok = load(&tmap, rb * kBK, row, &bmap, ad * p.cout + n0, (kBM + p.BN / 2) * p.aw);
+                        for (int v = 0; v < 2 && ok; v += held)
+                            ok = load(v, rb * kBK, row, ad * p.cout + n0, (held * kBM + p.BN / 2) * p.aw);
                 }
             }
             if (!ok) raise_abort(sm.abort_flag, p.err);
@@ -588,15 +698,17 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                     uint32_t off[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) off[i] = ~lane_bits(r0 - 32 * i, r1 - 32 * i);
-                    for (int rb = 0; rb < RB; ++rb) {
+                    for (int st = 0; st < RB * 2 / held; ++st) {  // a block of rank: both values of t, or one after the other
                         if (!wait_or_abort(sm.full + 8 * at.s, at.pass & 1, sm.abort_flag)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint64_t ad = a1 + at.s * sstep, bd = b1 + at.s * sstep;
-                        const int steps = min(4, (p.rank - rb * kBK + 15) / 16);
-                        for (int i = 0; i < steps; ++i) mma_pair_rows(dcol, ad + 2 * i, bd + 2 * i, idesc, off);
+                        const int steps = min(4, (p.rank - st * held / 2 * kBK + 15) / 16);
+                        for (int v = 0; v < held; ++v)
+                            for (int i = 0; i < steps; ++i)
+                                mma_pair_rows(dcol, ad + (uint32_t)(v * kBM * p.aw >> 4) + 2 * i, bd + 2 * i, idesc, off);
                         commit_pair(sm.empty + 8 * at.s, leader);
                         at.next(p.stages);
                     }
@@ -625,12 +737,15 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         const uint32_t stage = smem_u32(own);
         float *bias_s = reinterpret_cast<float *>(sm.ring + p.stages * sbytes + 8 * kOutBytes) + (warp - 2) * kBK;
         int local = 0;
+        if (p.shift) asm volatile("griddepcontrol.wait;" ::: "memory");  // SHRINK's exponents are there
         for (long long j = pair0; j < p.jobs; j += pairs, ++local) {
             const int row0 = (int)(j / p.NT) * kPairRows + rank * kBM + quad * 32, row = row0 + lane;
             const int n0 = (int)(j % p.NT) * p.BN, ncols = min(p.BN, p.cout - n0), buf = local & 1;
             // the map ends at the last row: rows past it are not written either way
             const bool boxes = row0 >= covered0 && min(row0 + 32, p.rows) <= covered1;
             const bool write = row >= covered0 && row < covered1;
+            const int far = shifted_row(row, write);
+            const bool shifted = kShifted && __any_sync(0xffffffffu, far >= 0);
             bool ready = false;
             if (p.splits > 1) {
                 if (!wait_or_abort(sm.acc_full, 0, sm.abort_flag)) {
@@ -666,6 +781,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                         v[4 * i + 1] += b.y;
                         v[4 * i + 2] += b.z;
                         v[4 * i + 3] += b.w;
+                    }
+                    if (shifted) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (far >= 0 && c + 32 * h + i < ncols) v[i] += missing(row, far, n0 + c + 32 * h + i);
+                        __syncwarp();
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -708,6 +829,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             const int row = (int)(pair0 / p.NT) * kPairRows + rank * kBM + quad * 32 + lane;
             const int n0 = (int)(pair0 % p.NT) * p.BN, ncols = min(p.BN, p.cout - n0);
             const bool write = row >= req.at(0) && row < req.at(p.requests);
+            const int far = shifted_row(row, write);
             const uint32_t addr = smem_u32(sm.ring) + (uint32_t)(quad * 32 + lane) * 4;
             for (int c = 8 * (split * 2 + half); c < ncols; c += 16 * p.splits) {
                 float v[8], b[8] = {};
@@ -715,6 +837,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                 add_splits(addr, c, p.splits, rank, 2, v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] += b[i];
+                if (far >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += missing(row, far, n0 + c + i);
+                }
                 if (write)
                     *reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + (long long)row * p.cout + n0 + c) = pack16<T>(v);
             }
@@ -734,19 +860,31 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     }
 }
 
+template <typename T> CUtensorMapDataType data_type() {
+    return std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+CUtensorMapSwizzle swizzle_of(int width) {
+    return width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+}
+
 // Boxes of `box` rows and `width` bytes over a [rows, cols] matrix of T, in the swizzle of that width.
 template <typename T>
 bool encode(CUtensorMap *m, const void *base, long long cols, long long rows, int box, int width = 128) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t str[1] = {(cuuint64_t)cols * 2};
     const cuuint32_t bx[2] = {(cuuint32_t)(width / 2), (cuuint32_t)box}, es[2] = {1, 1};
-    const CUtensorMapSwizzle sw = width == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                  : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                : CU_TENSOR_MAP_SWIZZLE_32B;
-    const CUtensorMapDataType dt = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    return encode_fn()(m, dt, 2, const_cast<void *>(base), dims, str, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                       sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return encode_fn()(m, data_type<T>(), 2, const_cast<void *>(base), dims, str, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       swizzle_of(width), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// t of a pass: boxes of 128 rows of as many of its two values as a stage holds.
+template <typename T> bool encode_t(CUtensorMap *m, const void *base, int rank, int rows, int width) {
+    const cuuint64_t dims[3] = {(cuuint64_t)rank, (cuuint64_t)rows, 2};
+    const cuuint64_t str[2] = {(cuuint64_t)rank * 2, (cuuint64_t)rows * rank * 2};
+    const cuuint32_t bx[3] = {(cuuint32_t)(width / 2), kBM, width < 128 ? 2u : 1u}, es[3] = {1, 1, 1};
+    return encode_fn()(m, data_type<T>(), 3, const_cast<void *>(base), dims, str, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       swizzle_of(width), CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -773,14 +911,23 @@ size_t plan_smem(LargeParams &p, size_t sbytes, size_t sums, size_t extra, size_
     return need > share ? need : share;
 }
 
-template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t stream) {
+// Bytes of t for one row: two values of the storage type for each rank, and in fp16 the exponents.
+size_t t_bytes(const AdapterArgs &a) { return (size_t)a.rank * 4 + (a.dtype == DType::F16 ? kShiftBytes : 0); }
+
+// One pass over rows row0 .. row0 + a.rows - 1 of the request table; x and out of `a` start there.
+template <typename T> cudaError_t launch_pass(const AdapterArgs &a, int row0, cudaStream_t stream) {
     const DeviceInfo *dev = device_info();
     if (!encode_fn() || !dev) return cudaErrorNotSupported;
     LargeParams p;
+    p.row0 = row0;
     p.rows = (int)a.rows;
     p.cin = a.cin; p.cout = a.cout; p.rank = a.rank; p.adapters = a.adapters; p.requests = a.requests;
     p.start = a.start; p.which = a.which; p.scale = a.scale; p.bias = a.bias;
     p.t = a.workspace;
+    p.shift = a.dtype == DType::F16 && a.adapters > 0
+                  ? static_cast<unsigned char *>(a.workspace) + (size_t)a.rows * a.rank * 4
+                  : nullptr;
+    p.b = a.b;
     p.out = a.out;
     p.err = dev->err;
 
@@ -813,7 +960,7 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
         return cudaErrorInvalidValue;
     am = tm = bm = wm;  // never read without adapters
     if (a.adapters > 0 && (!encode<T>(&am, a.a, a.cin, (long long)a.adapters * a.rank, rank16) ||
-                           !encode<T>(&tm, a.workspace, a.rank, a.rows, kBM, p.aw) ||
+                           !encode_t<T>(&tm, a.workspace, a.rank, (int)a.rows, p.aw) ||
                            !encode<T>(&bm, a.b, a.rank, (long long)a.adapters * a.cout, bn / 2, p.aw)))
         return cudaErrorInvalidValue;
 
@@ -868,11 +1015,21 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
 size_t adapters_large_workspace(const AdapterArgs &a) { return (size_t)a.rows * a.rank * 2; }
 
 cudaError_t launch_adapters_large(const AdapterArgs &a, cudaStream_t stream) {
-    switch (a.dtype) {
-        case DType::F16: return launch_t<__half>(a, stream);
-        case DType::BF16: return launch_t<__nv_bfloat16>(a, stream);
-        default: return cudaErrorInvalidValue;
+    if (a.dtype != DType::F16 && a.dtype != DType::BF16) return cudaErrorInvalidValue;
+    // as many rows in a pass as the workspace holds t of, in whole tiles where that is more than one
+    const int64_t fit = (int64_t)(a.workspace_bytes / t_bytes(a));
+    const int64_t step = fit >= a.rows ? a.rows : fit >= kPairRows ? fit / kPairRows * kPairRows : fit;
+    if (step < 1) return cudaErrorInvalidValue;
+    AdapterArgs g = a;
+    for (int64_t row0 = 0; row0 < a.rows; row0 += step) {
+        g.rows = a.rows - row0 < step ? a.rows - row0 : step;
+        g.x = static_cast<const char *>(a.x) + row0 * a.cin * 2;
+        g.out = static_cast<char *>(a.out) + row0 * a.cout * 2;
+        const cudaError_t e = a.dtype == DType::F16 ? launch_pass<__half>(g, (int)row0, stream)
+                                                    : launch_pass<__nv_bfloat16>(g, (int)row0, stream);
+        if (e != cudaSuccess) return e;
     }
+    return cudaSuccess;
 }
 
 // The route by its time in microseconds, as measured (one B200; cin and cout of 256 to 4096, ranks 16 and 64).  The
@@ -890,6 +1047,10 @@ static bool few_rows(const AdapterArgs &a) {
 
 size_t proj_adapters_workspace(const AdapterArgs &a) {
     return few_rows(a) ? adapters_small_workspace(a) : adapters_large_workspace(a);
+}
+
+size_t proj_adapters_workspace_full(const AdapterArgs &a) {
+    return few_rows(a) ? adapters_small_workspace(a) : (size_t)a.rows * t_bytes(a);
 }
 
 cudaError_t launch_proj_adapters(const AdapterArgs &a, cudaStream_t stream) {

@@ -308,16 +308,21 @@ dcn_status deform_roi_pool_forward(const droi_params *p, const void *x, const fl
  * out of range.  An adapter outside [-1, num_adapters) counts as none and, where
  * its request owns a row, sets bit 1 of the device error word
  * (dcn_take_device_error).  out and workspace must not overlap any input.
- * Sums are fp32.  With at most 64 rows A[a] x stays in fp32; with more it may be
- * (and above 256 rows is) scaled and rounded once to the storage dtype, as an
- * operand of the second tensor-core product.  Values of one row do not depend
- * on other requests'.
+ * Sums are fp32.  t = scale[a] * A[a] x is held in 32 bits: up to 64 rows in fp32,
+ * with more it may be (and above 256 rows is) the sum of two values of the
+ * storage dtype, the operands of the second tensor-core product: off by at most
+ * 2^-22 |t| + 2^-25 in fp16 (2^-39 of the largest of eight neighbouring ranks
+ * instead of 2^-25 where that exceeds 2^15) and 2^-16 |t| in bf16, over all of fp32's range.  What
+ * other requests' rows and adapters hold does not reach a row's values; how many
+ * rows the call has may change their last bits (the order of the sums).
  * cin, cout and rank are multiples of 8, cin and cout up to 65536, rank up to
  * 128; rows up to 2^30; num_requests and num_adapters up to 2^20, with
  * num_adapters * cout and num_adapters * rank up to 2^30.  x, weight, bias, a, b
  * and out are 16-byte aligned.  fp32 returns DCN_ERR_UNSUPPORTED.
- * workspace: dcn_proj_adapters_workspace_bytes(p) bytes, 16-byte aligned; calls
- * that overlap on the GPU need one each.  rows == 0 or num_requests == 0 is a
+ * workspace: dcn_proj_adapters_workspace_bytes(p) bytes at least, 16-byte aligned;
+ * with less than dcn_proj_adapters_workspace_full_bytes(p) the rows may be worked
+ * on in several passes, one after the other; calls that overlap on the GPU need
+ * one each.  rows == 0 or num_requests == 0 is a
  * no-op; num_adapters may be 0 (a and b may then be NULL).
  */
 typedef struct {
@@ -332,8 +337,10 @@ dcn_status dcn_proj_adapters_forward(const dadapt_params *p, const void *x, cons
                                      void *out, void *workspace, int64_t workspace_bytes,
                                      dcn_stream_t stream);
 
-/* Workspace bytes of dcn_proj_adapters_forward; -1 for invalid params. */
+/* Least workspace bytes of dcn_proj_adapters_forward, and those with which it works
+ * in one pass; -1 for invalid params. */
 int64_t dcn_proj_adapters_workspace_bytes(const dadapt_params *p);
+int64_t dcn_proj_adapters_workspace_full_bytes(const dadapt_params *p);
 
 /*
  * Residual addition and root-mean-square norm over the channels of each row,

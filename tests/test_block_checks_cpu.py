@@ -180,3 +180,17 @@ def test_python_refusals_without_a_gpu(lib):
     assert B._workspace(other, 1) == (other.data_ptr(), 64)
     with pytest.raises(ValueError, match="workspace is on"):
         B._workspace(other, 0)
+
+
+def test_adapter_workspaces(lib):
+    """The least workspace and the one of a single pass, which holds t of more than 256 rows in 32 bits and, in fp16, 16
+    exponents a row."""
+    least, full = lib.dcn_proj_adapters_workspace_bytes, lib.dcn_proj_adapters_workspace_full_bytes
+    for kw in (dict(rows=1000), dict(rows=257, rank=128), dict(rows=1 << 20, rank=8)):
+        p = adapt(**kw)
+        q = adapt(dtype=2, **kw)
+        assert least(ctypes.byref(p)) == least(ctypes.byref(q)) == p.rows * p.rank * 2
+        assert full(ctypes.byref(p)) == p.rows * (p.rank * 4 + 16) and full(ctypes.byref(q)) == p.rows * p.rank * 4
+    few = ctypes.byref(adapt(rows=10))
+    assert least(few) == full(few)
+    assert full(ctypes.byref(adapt(cin=60))) == -1

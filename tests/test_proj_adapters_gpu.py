@@ -355,3 +355,110 @@ def test_binding_refusals(cuda_dev):
     odd = {k: v.cuda() for k, v in make([4], [0], 60, 64, 16, 1, "f16", 95).items()}
     with pytest.raises(d.DcnError):
         go(**{k: odd[k] for k in ("x", "weight", "a")})
+
+
+def definition_32(s):
+    """(y, tolerance) where t is held in 32 bits: with more than 64 rows it may be two values of the storage type, off by
+    uT^2 |t| (the rounding error, rounded) and half a subnormal of fp16; where eight neighbouring ranks of t go beyond
+    2^15, they are scaled down by a power of two to below it, and that is tiny / 2^14 of their largest."""
+    dt = s["x"].dtype
+    uT = torch.finfo(dt).eps / 2
+    tiny = torch.finfo(dt).smallest_normal * uT
+    _, tol = definition(dict(s, b=torch.zeros_like(s["b"])))  # for the bias, W and the output's tiny; its tr is zero
+    want, _ = definition(s)
+    x, start = s["x"].double(), s["start"].tolist()
+    n = x.shape[1] + s["a"].shape[1] + 16
+    plain, _ = definition(dict(s, b=torch.zeros_like(s["b"])))
+    tol = tol - plain.abs() * uT + want.abs() * uT
+    for i, ad in enumerate(s["which"].tolist()):
+        lo, hi = start[i], start[i + 1]
+        if ad < 0 or lo >= hi:
+            continue
+        sc = float(s["scale"][ad]) if s["scale"] is not None else 1.0
+        a, b = s["a"][ad].double(), s["b"][ad].double()
+        t, tm = sc * (x[lo:hi] @ a.t()), sc * (x[lo:hi].abs() @ a.abs().t())
+        low = torch.clamp(t.abs().view(hi - lo, -1, 8).amax(2).repeat_interleave(8, 1) * 2.0 ** -14, min=1.0) * tiny
+        tol[lo:hi] += tm @ b.abs().t() * n * 2 * U + (t.abs() * uT * uT * (1 + 2 * uT) + low) @ b.abs().t()
+    return want, tol
+
+
+# rows of each request, adapter of each, cin, cout, rank, adapters: blocks of 32, 64 and 128 bytes of t, split and unsplit
+# contractions, both halves of a pair's tile, rows of no adapter
+HELD = [
+    ([300], [0], 16, 64, 8, 1), ([200, 9, 300], [0, -1, 1], 16, 136, 16, 2), ([513], [0], 16, 264, 24, 1),
+    ([90, 400], [1, 0], 16, 72, 32, 2), ([700, 11], [0, 1], 16, 328, 64, 2), ([257], [0], 16, 64, 104, 1),
+    ([800], [0], 16, 512, 128, 1), ([270, 0, 30], [1, 0, 0], 4096, 64, 128, 2), ([200, 57], [0, 1], 2056, 136, 24, 2),
+    ([266], [0], 3768, 64, 16, 1), ([20000, 13, 5000], [0, 1, 1], 64, 256, 32, 2),
+]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("i", range(len(HELD)))
+def test_t_is_held_in_32_bits(i, dtype, cuda_dev):
+    """No rounding of t to the storage type, whose error would show where y is small."""
+    s = make(*HELD[i], dtype, 200 + i)
+    s["bias"] = None
+    s["weight"] = (s["weight"].double() / 64).to(DT[dtype])
+    y = call(s)
+    torch.cuda.synchronize()
+    assert d._binding.take_device_error() == 0
+    want, tol = definition_32(s)
+    err = (y.double().cpu() - want).abs()
+    assert (err <= tol).all(), (float((err / tol).max()), int((err > tol).sum()))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("i", range(len(HELD)))
+def test_t_beyond_the_storage_type(i, dtype, cuda_dev):
+    """Values of t past 65504, up to 2^24, in some rows, with a B so small that y is within its type."""
+    s = make(*HELD[i], dtype, 230 + i)
+    dt = DT[dtype]
+    big = torch.rand(s["x"].shape[0], 1, generator=torch.Generator().manual_seed(i)) < 0.4
+    s["x"] = torch.where(big, s["x"] * 2.0 ** 12, s["x"]).to(dt)
+    s["weight"] = (s["weight"].double() * 2.0 ** -12).to(dt)
+    s["a"] = (s["a"].double() * 2.0 ** 8).to(dt)
+    s["b"] = (s["b"].double() * 2.0 ** -12).to(dt)
+    s["scale"] = s["scale"] * 2.0 ** 2
+    y = call(s)
+    torch.cuda.synchronize()
+    want, tol = definition_32(s)
+    assert (want.abs() < 60000).all()
+    err = (y.double().cpu() - want).abs()
+    assert (err <= tol).all(), (float((err / tol).max()), int((err > tol).sum()))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cin,cout,rank", [(64, 72, 16), (64, 72, 40), (4096, 64, 128)])
+def test_infinite_t_beside_large_values(cin, cout, rank, dtype, cuda_dev):
+    """An infinity in one rank of t gives infinities and NaN where 64 bits do, and no NaN beside them."""
+    s = make([200, 100], [0, 1], cin, cout, rank, 2, dtype, 250)
+    s["x"][:, 1] = s["x"][:, 1].abs() + 1  # times an infinity of A: of one sign
+    s["a"][1, 3, 1] = float("inf")
+    s["a"][1, 4] *= 2.0 ** 14
+    s["b"][1, ::2, 3] = 0.0
+    s["b"][1, :, 4] *= 2.0 ** -10
+    y = call(s).double().cpu()
+    want, _ = definition(s)
+    assert want[200:].isnan().any() and want[200:].isinf().any()
+    assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.isinf(), want.isinf())
+    assert torch.equal(y[y.isinf()], want[y.isinf()])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,first,lens", [(700, 0, [200, 57, 400]), (1500, 3, [900, 0, 590]), (300, 0, [100, 100, 100]),
+                                             (2000, 700, [1, 1, 1200])])
+def test_least_workspace(rows, first, lens, dtype, cuda_dev):
+    """With the least workspace the rows go in passes, which cut requests: the same values, other rows as they were."""
+    s = make(lens, [1, 0, 1], 64, 520, 24, 2, dtype, 260, rows=rows, first=first)
+    p = d._binding.DadaptParams(rows, 64, 520, 24, 2, 3, 1 if dtype == "f16" else 2)
+    least = d.lib().dcn_proj_adapters_workspace_bytes(p)
+    full = d.lib().dcn_proj_adapters_workspace_full_bytes(p)
+    assert rows * 24 * 2 == least and rows * (24 * 4 + (16 if dtype == "f16" else 0)) == full
+    end = first + sum(lens)
+    for n in (least, least + 999, full - 1, full):
+        out = torch.full((rows, 520), 7.0, dtype=DT[dtype], device="cuda")
+        y = call(s, out=out, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+        assert (out[:first] == 7).all() and (out[end:] == 7).all()
+        check(s, y, slice(first, end))
+        want, tol = definition_32(s)
+        assert ((y.double().cpu() - want).abs() <= tol)[first:end].all()
