@@ -19,4 +19,14 @@ template <typename K> cudaError_t allow_smem(K kern, int bytes, std::atomic<bool
     return e;
 }
 
+// Least shared memory of a CTA that allocates `cols` columns of tensor memory, of `limit` bytes that a CTA may have.
+// CTAs of a pair or a cluster wait for one another while they hold tensor memory.  Were a CTA that waits for its columns
+// on an SM where others hold too many to get in the way of a cluster's last CTA there, two such clusters of calls on
+// different streams could hold each other up for good.  So a CTA takes the same share of the shared memory as of the
+// tensor memory: CTAs that fit an SM together find their columns there, and none waits.  All 512 columns leave 13 KB to
+// CTAs without tensor memory: the smallest share of those with some is 14 KB.
+inline size_t tensor_memory_share(size_t limit, int cols) {
+    return cols >= 512 ? limit - 13 * 1024 : limit * cols / 512;
+}
+
 }  // namespace dcnb

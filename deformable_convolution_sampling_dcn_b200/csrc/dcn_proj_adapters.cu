@@ -289,7 +289,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sbytes = kABytes + p.BN * kBK * 2;  // BN a multiple of 16: a stage is a multiple of 1 KB
     const Smem sm(smem_raw, p.stages * sbytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) sm.init(4);
     const Requests req = sm.requests(p);
     if (warp == 1) {
@@ -302,6 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *sm.tmem_slot;
+    // not before this CTA has its columns: EXPAND holds its own while it waits for all of SHRINK
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && warp >= 2)
         for (int i = threadIdx.x - 64; i < p.requests; i += 128)
             if (req.at(i + 1) > req.at(i)) report_bad_adapter(req.which[i], p.adapters, p.err);
@@ -897,9 +898,6 @@ int tmem_columns(int bn) {
 // Stages of `sbytes` that fit and that a CTA's `use` blocks can fill (a short ring leaves EXPAND room beside SHRINK's
 // last CTAs), and the shared memory they take with `extra`; the accumulator of a split, `sums` bytes, takes the ring's
 // place.
-// CTAs of a pair or a cluster wait for one another while they hold tensor memory.  Two calls on two streams must not
-// block each other's other halves, so a CTA takes at least the same share of the shared memory as of the tensor
-// memory: CTAs that fit an SM together then find tensor memory together.
 size_t plan_smem(LargeParams &p, size_t sbytes, size_t sums, size_t extra, size_t limit, long long use) {
     const size_t other = extra + 1024 + (2 * kMaxStages + 5) * 8 + 8 +
                          (p.requests <= kReqCache ? (size_t)(2 * p.requests + 1) * 4 : 0);
@@ -907,7 +905,7 @@ size_t plan_smem(LargeParams &p, size_t sbytes, size_t sums, size_t extra, size_
     while (p.stages > 2 && other + p.stages * sbytes > limit) --p.stages;
     if (p.splits > 1)
         while (p.stages * sbytes < sums && p.stages < kMaxStages) ++p.stages;
-    const size_t need = other + p.stages * sbytes, share = limit * p.tmem_cols / 512;
+    const size_t need = other + p.stages * sbytes, share = tensor_memory_share(limit, p.tmem_cols);
     return need > share ? need : share;
 }
 

@@ -416,7 +416,8 @@ template <typename T> cudaError_t launch_t(const AdapterArgs &a, cudaStream_t st
     const size_t sbytes = kWBytes + (size_t)p.mpad * kBK * 2, other = 1024 + (2 * kMaxStages + 5) * 8 + 8;
     p.stages = run < 2 ? 2 : run < kMaxStages ? run : kMaxStages;
     while (other + p.stages * sbytes > (size_t)dev->smem_optin) --p.stages;
-    const size_t smem = other + p.stages * sbytes;
+    const size_t need = other + p.stages * sbytes, share = tensor_memory_share((size_t)dev->smem_optin, p.tmem_cols);
+    const size_t smem = need > share ? need : share;
     CUtensorMap wm, xm;
     if (!encode<T>(&wm, a.weight, a.cin, a.cout, kTN) || !encode<T>(&xm, a.x, a.cin, a.rows, p.mpad))
         return cudaErrorInvalidValue;

@@ -462,3 +462,33 @@ def test_least_workspace(rows, first, lens, dtype, cuda_dev):
         check(s, y, slice(first, end))
         want, tol = definition_32(s)
         assert ((y.double().cpu() - want).abs() <= tol)[first:end].all()
+
+
+def test_both_routes_on_several_streams(cuda_dev):
+    """The row route with all of an SM's tensor memory (129 to 256 rows) and little shared memory, beside pairs and
+    clusters of the tile route that wait for one another, and beside the fused core + projection."""
+    cases = [make([130], [0], 128, 512, 8, 1, "f16", 1), make([1] * 200, [i % 3 - 1 for i in range(200)], 128, 64, 16, 2, "bf16", 2),
+             make([270, 0, 30], [1, 0, 0], 4096, 64, 128, 2, "f16", 3), make([700], [0], 520, 264, 128, 1, "bf16", 4),
+             make([300], [0], 2048, 64, 16, 1, "f16", 5), make([1600, 1600, 7], [2, -1, 0], 512, 512, 16, 3, "bf16", 6)]
+    dev = [{k: None if v is None else v.cuda() for k, v in c.items()} for c in cases]
+    want = [call(c) for c in cases]
+    g = torch.Generator().manual_seed(7)
+    shapes = (2, 20, 20, 64), (2, 20, 20, 4, 9, 2), (2, 20, 20, 4, 9), (512, 64)
+    core = [torch.randn(s, generator=g).half().cuda() for s in shapes]
+
+    def fused():
+        return d.dcn_core_forward_proj(*core, None, group=4, fused=True)
+    want.append(fused())
+    outs = [[] for _ in want]
+    streams = [torch.cuda.Stream() for _ in want]
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                t = dev[i] if i < len(dev) else None
+                outs[i].append(fused() if t is None else d.dcn_proj_adapters_forward(
+                    t["x"], t["weight"], t["bias"], t["a"], t["b"], t["start"], t["which"], scale=t["scale"]))
+    torch.cuda.synchronize()
+    assert d._binding.take_device_error() == 0
+    for o, y in zip(outs, want):
+        assert all(torch.equal(v, y) for v in o)
