@@ -86,7 +86,7 @@ struct LargeParams {
     int stages, tmem_cols;
     int aw;                // bytes of a row of an adapter block: 32, 64 or 128, its swizzle too
     int splits;            // of the contraction; a cluster has one job where this is not 1
-    long long jobs;        // EXPAND: tiles of y; SHRINK: pairs of a tile and a request
+    long long jobs;        // EXPAND: tiles of y; SHRINK: pairs of a tile and a request, empty requests included
     unsigned int *err;
 };
 
@@ -118,6 +118,39 @@ struct Requests {
         if (s < 0) return -1;
         const int tile = (int)(j - s), r0 = at(s), r1 = at(s + 1);
         return r1 > r0 && tile >= r0 / kBM && tile * kBM < r1 && adapter(s) >= 0 ? s : -1;
+    }
+    // Leaves out the empty requests at the end, with which a program fills its table up to a fixed size.  By all threads,
+    // once the table is there.
+    __device__ __forceinline__ void drop_empty_tail() {
+        const int end = at(count);
+        if (at(count - 1) < end) return;
+        const Requests all = *this;
+        count = warp_first(count, [&](int s) { return all.at(s) >= end; });
+    }
+};
+
+// The requests that own rows of [r0, r1), which are at most as many as the rows (a table that is not ascending ends
+// there); empty ones between them are passed over by search.
+struct RequestsOf {
+    const Requests &q;
+    int r, lo, hi;  // request r, and its rows lo .. hi - 1
+    int r1, left;
+    __device__ __forceinline__ RequestsOf(const Requests &q_, int r0, int r1_) : q(q_), r1(r1_), left(r1_ - r0) {
+        go(q.first_ending_after(r0));
+    }
+    __device__ __forceinline__ bool valid() const { return left > 0 && r < q.count && lo < r1; }
+    __device__ __forceinline__ void next() {
+        --left;
+        if (++r >= q.count) return;
+        lo = hi;
+        hi = q.at(r + 1);
+        if (hi <= lo) go(max(r, q.first_ending_after(lo)));
+    }
+    __device__ __forceinline__ void go(int to) {
+        r = to;
+        if (r >= q.count) return;
+        lo = q.at(r);
+        hi = q.at(r + 1);
     }
 };
 
@@ -290,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Smem sm(smem_raw, p.stages * sbytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) sm.init(4);
-    const Requests req = sm.requests(p);
+    Requests req = sm.requests(p);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sm.tmem_slot)),
                      "r"(p.tmem_cols)
@@ -303,14 +336,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *sm.tmem_slot;
     // not before this CTA has its columns: EXPAND holds its own while it waits for all of SHRINK
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    req.drop_empty_tail();
     if (blockIdx.x == 0 && warp >= 2)
-        for (int i = threadIdx.x - 64; i < p.requests; i += 128)
+        for (int i = threadIdx.x - 64; i < req.count; i += 128)
             if (req.at(i + 1) > req.at(i)) report_bad_adapter(req.which[i], p.adapters, p.err);
     const int blocks = (p.cin + kBK - 1) / kBK;
     // this CTA's part of the contraction and its cluster's job
     const int split = p.splits > 1 ? (int)cta_rank() : 0;
     const int kb0 = blocks * split / p.splits, kb1 = blocks * (split + 1) / p.splits;
     const long long job0 = blockIdx.x / p.splits, jobs_step = gridDim.x / p.splits;
+    const long long jobs = (p.rows + kBM - 1) / kBM + req.count;  // pairs of a tile and a request: at most the launch's
 
     if (warp == 0) {
         // ---- producer
@@ -318,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Slot at;
             long long issued = 0;
             bool ok = true;
-            for (long long j = job0; j < p.jobs && ok; j += jobs_step) {
+            for (long long j = job0; j < jobs && ok; j += jobs_step) {
                 const int r = req.of_pair(j);
                 if (r < 0) continue;
                 const int row = (int)(j - r) * kBM, arow = req.adapter(r) * p.rank;
@@ -351,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Slot at;
             int local = 0;
             bool ok = true, issued = false;
-            for (long long j = job0; j < p.jobs && ok; j += jobs_step) {
+            for (long long j = job0; j < jobs && ok; j += jobs_step) {
                 if (req.of_pair(j) < 0) continue;
                 const int buf = local & 1;
                 if (local >= 2 && !wait_or_abort(sm.acc_empty + 8 * buf, ((local >> 1) - 1) & 1, sm.abort_flag)) {
@@ -392,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- epilogue: warp w reads tensor-memory lanes 32 * (w % 4) .. +31 = rows of the tile
         const int quad = warp & 3;
         int local = 0;
-        for (long long j = job0; j < p.jobs; j += jobs_step) {
+        for (long long j = job0; j < jobs; j += jobs_step) {
             const int r = req.of_pair(j);
             if (r < 0) continue;
             const int row = (int)(j - r) * kBM + quad * 32 + lane, buf = local & 1;
@@ -567,7 +602,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         prefetch_map(&bmap);
         prefetch_map(&ymap);
     }
-    const Requests req = sm.requests(p);
+    Requests req = sm.requests(p);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sm.tmem_slot)),
                      "r"(p.tmem_cols)
@@ -579,6 +614,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     cluster_sync();  // the other CTA's barriers and tensor memory are ready
     tc_fence_after();
     const uint32_t tmem = *sm.tmem_slot;
+    req.drop_empty_tail();
     const int blocks = (p.cin + kBK - 1) / kBK, RB = (p.rank + kBK - 1) / kBK;
     // this pair's part of the contraction; the adapters' blocks belong to the last one
     const int kb0 = blocks * split / p.splits, kb1 = blocks * (split + 1) / p.splits;
@@ -599,7 +635,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         }
         if (any == 0) return -1;
         const int r = req.first_ending_after(row);
-        return r < p.requests && req.at(r) <= row ? req.adapter(r) : -1;
+        return r < req.count && req.at(r) <= row ? req.adapter(r) : -1;
     };
     auto missing = [&](int row, int ad, int channel) {
         const T *t = static_cast<const T *>(p.t) + (long long)row * p.rank;
@@ -634,17 +670,17 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                 if (!adapters) continue;
                 if (ok && !waited) {
                     // the first tile's B, which does not depend on SHRINK, comes to L2 meanwhile
-                    for (int r = req.first_ending_after(tile); r < p.requests && req.at(r) < tile + kPairRows; ++r)
-                        if (req.adapter(r) >= 0 && req.at(r + 1) > req.at(r))
-                            for (int rb = 0; rb < RB; ++rb) prefetch_2d(&bmap, rb * kBK, req.adapter(r) * p.cout + n0);
+                    for (RequestsOf w(req, tile, tile + kPairRows); w.valid(); w.next())
+                        if (w.hi > w.lo && req.adapter(w.r) >= 0)
+                            for (int rb = 0; rb < RB; ++rb) prefetch_2d(&bmap, rb * kBK, req.adapter(w.r) * p.cout + n0);
                     // t comes from the SHRINK kernel: visible from here on, to the TMA too
                     asm volatile("griddepcontrol.wait;" ::: "memory");
                     asm volatile("fence.proxy.async;" ::: "memory");
                     waited = true;
                 }
-                for (int r = req.first_ending_after(tile); ok && r < p.requests && req.at(r) < tile + kPairRows; ++r) {
-                    const int ad = req.adapter(r);
-                    if (ad < 0 || req.at(r + 1) <= req.at(r)) continue;
+                for (RequestsOf w(req, tile, tile + kPairRows); ok && w.valid(); w.next()) {
+                    const int ad = req.adapter(w.r);
+                    if (ad < 0 || w.hi <= w.lo) continue;
                     for (int rb = 0; rb < RB && ok; ++rb)
                         for (int v = 0; v < 2 && ok; v += held)
                             ok = load(v, rb * kBK, row, ad * p.cout + n0, (held * kBM + p.BN / 2) * p.aw);
@@ -691,11 +727,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                     commit_pair(sm.empty + 8 * at.s, leader);
                     at.next(p.stages);
                 }
-                for (int r = req.first_ending_after(tile);
-                     adapters && ok && r < p.requests && req.at(r) < tile + kPairRows; ++r) {
-                    if (req.adapter(r) < 0 || req.at(r + 1) <= req.at(r)) continue;
-                    // this request's rows of the tile
-                    const int r0 = req.at(r) - tile, r1 = req.at(r + 1) - tile;
+                for (RequestsOf w(req, tile, tile + kPairRows); adapters && ok && w.valid(); w.next()) {
+                    if (w.hi <= w.lo || req.adapter(w.r) < 0) continue;
+                    const int r0 = w.lo - tile, r1 = w.hi - tile;  // this request's rows of the tile
                     uint32_t off[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) off[i] = ~lane_bits(r0 - 32 * i, r1 - 32 * i);

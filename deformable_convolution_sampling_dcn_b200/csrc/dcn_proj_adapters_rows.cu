@@ -58,7 +58,8 @@ struct SmallParams {
 // Adapter of row m (-1: none; -2: the row belongs to no request), by a whole warp.
 __device__ __forceinline__ int adapter_of_row(const AdapterArgs &a, int m, int *raw) {
     const int lane = threadIdx.x & 31;
-    for (int s0 = 0; s0 < a.requests; s0 += 128) {
+    constexpr int kNear = 256;  // as many as rows: where there are more, some are empty
+    for (int s0 = 0; s0 < min(a.requests, kNear); s0 += 128) {
         int lo[4], hi[4], ad[4];  // 128 requests in flight: one round trip for most tables
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -79,7 +80,12 @@ __device__ __forceinline__ int adapter_of_row(const AdapterArgs &a, int m, int *
         }
     }
     *raw = -1;
-    return -2;
+    if (a.requests <= kNear) return -2;
+    // the first of the others that ends behind row m (a table filled up with empty requests may be long)
+    const int s = kNear + warp_first(a.requests - kNear, [&](int i) { return a.start[kNear + i + 1] > m; });
+    if (s == a.requests || a.start[s] > m) return -2;
+    *raw = a.which[s];
+    return adapter_of(a.which, s, a.adapters);
 }
 
 // The blocks of CTA c of n: [total * c / n, total * (c + 1) / n).  At most 1024 x 512 blocks and 148 CTAs: the

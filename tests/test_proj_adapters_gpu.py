@@ -492,3 +492,44 @@ def test_both_routes_on_several_streams(cuda_dev):
     assert d._binding.take_device_error() == 0
     for o, y in zip(outs, want):
         assert all(torch.equal(v, y) for v in o)
+
+
+@pytest.mark.parametrize("pad", [300, 900, 5000, (1 << 20) - 5])
+@pytest.mark.parametrize("where", ["end", "middle", "front"])
+@pytest.mark.parametrize("lens", [[30, 1, 9], [300, 1, 90], [1000, 7, 1200]])
+def test_tables_filled_up_with_empty_requests(lens, where, pad, cuda_dev):
+    """A table of a fixed size, as a captured graph keeps it: the empty requests, wherever they are, do not keep a call
+    busy (no wait runs out, and the padded end costs next to nothing)."""
+    s = make(lens, [1, -1, 0], 64, 520, 16, 2, "bf16", 270, rows=sum(lens) + 5)
+    start, which = s["start"].tolist(), s["which"].tolist()
+    i = {"end": 3, "middle": 2, "front": 0}[where]
+    s["start"] = torch.tensor(start[:i] + [start[i]] * pad + start[i:], dtype=torch.int32)
+    s["which"] = torch.tensor(which[:i] + [1] * pad + which[i:], dtype=torch.int32)
+    t = {k: v.cuda() for k, v in s.items()}
+    args = (t["x"], t["weight"], t["bias"], t["a"], t["b"], t["start"], t["which"])
+    out = torch.full((sum(lens) + 5, 520), 7.0, dtype=torch.bfloat16, device="cuda")
+    d.dcn_proj_adapters_forward(*args, scale=t["scale"], out=out)
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    d.dcn_proj_adapters_forward(*args, scale=t["scale"], out=out)
+    end.record()
+    torch.cuda.synchronize()
+    assert d._binding.take_device_error() == 0
+    assert begin.elapsed_time(end) < (5.0 if where == "end" else 500.0)  # ms
+    assert (out[sum(lens):] == 7).all()
+    short = {"start": torch.tensor(start, dtype=torch.int32), "which": torch.tensor(which, dtype=torch.int32)}
+    want, tol = definition(dict(s, **short))
+    assert ((out.double().cpu() - want).abs() <= tol)[:sum(lens)].all()
+
+
+def test_a_table_that_is_not_ascending_ends(cuda_dev):
+    """Wrong values are allowed, a call that runs on is not; the next call is right."""
+    g = torch.Generator().manual_seed(3)
+    for n, rows in ((200, 600), (3000, 600), (3000, 100)):
+        s = make([rows], [0], 64, 264, 16, 2, "f16", 271)
+        bad = dict(s, start=torch.randint(-50, rows + 50, (n + 1,), generator=g).int(),
+                   which=torch.randint(-2, 3, (n,), generator=g).int())
+        call(bad)
+        torch.cuda.synchronize()
+        assert d._binding.take_device_error() in (0, 2)
+        check(s, call(s))
