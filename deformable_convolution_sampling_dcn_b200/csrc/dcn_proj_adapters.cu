@@ -1064,17 +1064,21 @@ cudaError_t launch_adapters_large(const AdapterArgs &a, cudaStream_t stream) {
     return cudaSuccess;
 }
 
-// The route by its time in microseconds, as measured (one B200; cin and cout of 256 to 4096, ranks 16 and 64).  The
+// The route by its time in microseconds, as measured (one B200; cin and cout of 256 to 4096, ranks 16 to 128).  The
 // row-wise route (dcn_proj_adapters_rows.cu): 6.5, the weight at 5 TB/s, 0.02 a row for the partial sums, and 2.4
 // million products a microsecond for t and the adapter term, which do not use the tensor cores.  The tiles of this
-// file: 12, and 0.36 for each block of the contraction and round of tiles.  Up to 64 rows it is always the first.
+// file: 12, 0.36 for each block of the contraction and round of tiles, and for each further request, whose blocks
+// of t and B follow one another, 0.4 and 0.55 for each stage that they take (1024 -> 1024, rank 64, 256 rows: of one
+// request 22.9 and 14.8, of 16 22.9 and 35.8, of 256 24.3 and 395).  Up to 64 rows it is always the first.
 static bool few_rows(const AdapterArgs &a) {
     if (a.rows <= 64) return true;
     if (a.rows > kMaxSmallRows) return false;
     const double rows = 6.5 + 2.0 * a.cin * a.cout / 5.0e6 + 0.02 * (double)a.rows +
                         (double)a.rows * a.rank * ((double)a.cin + a.cout) / 2.4e6;
     const int blocks = (a.cin + kBK - 1) / kBK, tiles = (a.cout + 63) / 64, rounds = (tiles + 73) / 74;
-    return rows <= 12.0 + 0.36 * blocks * rounds;
+    const int further = (int)(a.requests < a.rows ? a.requests : a.rows) - 1;  // as many at most as own rows
+    const int stages = a.rank <= 32 ? 1 : 2 * ((a.rank + kBK - 1) / kBK);
+    return rows <= 12.0 + 0.36 * blocks * rounds + further * (0.4 + 0.55 * stages);
 }
 
 size_t proj_adapters_workspace(const AdapterArgs &a) {

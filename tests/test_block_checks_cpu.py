@@ -194,3 +194,17 @@ def test_adapter_workspaces(lib):
     few = ctypes.byref(adapt(rows=10))
     assert least(few) == full(few)
     assert full(ctypes.byref(adapt(cin=60))) == -1
+
+
+@pytest.mark.parametrize("rank", [16, 64, 128])
+@pytest.mark.parametrize("rows", [80, 128, 256])
+def test_single_tokens_take_the_row_route(lib, rows, rank):
+    """The row route, whose workspace is one size, where every row is a request of its own, whatever the width; a prompt
+    of high rank takes the tiles."""
+    def route(**kw):
+        p = ctypes.byref(adapt(rows=rows, rank=rank, **kw))
+        return "rows" if lib.dcn_proj_adapters_workspace_bytes(p) == lib.dcn_proj_adapters_workspace_full_bytes(p) else "tiles"
+    for cin, cout in ((512, 512), (1024, 1024), (1024, 4096), (4096, 1024), (4096, 4096)):
+        assert route(cin=cin, cout=cout, num_requests=rows) == "rows"
+        assert route(cin=cin, cout=cout, num_requests=1 << 20) == "rows"  # a padded table may hold as many
+    assert rank < 128 or rows < 128 or route(cin=4096, cout=4096, num_requests=1) == "tiles"
