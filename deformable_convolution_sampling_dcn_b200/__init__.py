@@ -93,10 +93,11 @@ class AddRmsNormFunction(torch.autograd.Function):
     def backward(ctx, grad_out, grad_h):
         h, rstd, weight = ctx.saved_tensors
         if grad_out is None:
-            gw = None if weight is None else torch.zeros_like(weight)
+            gw = torch.zeros_like(weight) if ctx.needs_input_grad[2] else None
             return grad_h, (grad_h if ctx.has_residual else None), gw, None
         gx, gw = dcn_add_rms_norm_backward(grad_out.contiguous(), h, rstd, weight, eps=ctx.eps,
-                                           grad_residual_out=None if grad_h is None else grad_h.contiguous())
+                                           grad_residual_out=None if grad_h is None else grad_h.contiguous(),
+                                           need_grad_weight=ctx.needs_input_grad[2])
         return gx, (gx if ctx.has_residual else None), gw, None
 
 

@@ -31,6 +31,7 @@ EXPORTS = ("dcn_core_output_hw", "dcn_core_forward", "dcn_core_backward", "defor
            "dcn_selftest_bounded_wait", "dcn_deform_conv_forward", "dcn_probe_rate",
            "dcn_core_forward_proj_workspace_bytes", "dcn_core_forward_proj_noalloc",
            "dcn_add_rms_norm_forward", "dcn_add_rms_norm_backward", "dcn_add_rms_norm_backward_workspace_bytes",
+           "dcn_add_rms_norm_backward_input",
            "dcn_grad_norm", "dcn_clip_grads", "dcn_grad_norm_workspace_bytes",
            "dcn_proj_adapters_forward", "dcn_proj_adapters_workspace_bytes", "dcn_proj_adapters_workspace_full_bytes")
 ABI_VERSION = 2
@@ -117,11 +118,13 @@ def _declare(lib):
     N, L = ctypes.POINTER(DnormParams), ctypes.POINTER(DclipParams)
     lib.dcn_add_rms_norm_forward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.dcn_add_rms_norm_backward.argtypes = [N, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp]
+    lib.dcn_add_rms_norm_backward_input.argtypes = [N, vp, vp, vp, vp, vp, vp, vp]
     lib.dcn_add_rms_norm_backward_workspace_bytes.argtypes = [N]
     lib.dcn_grad_norm.argtypes = [L, vp, vp, vp, vp, vp, ctypes.c_int64, vp]
     lib.dcn_clip_grads.argtypes = [L, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp]
     lib.dcn_grad_norm_workspace_bytes.argtypes = [ctypes.c_int32]
-    for f in ("dcn_add_rms_norm_forward", "dcn_add_rms_norm_backward", "dcn_grad_norm", "dcn_clip_grads"):
+    for f in ("dcn_add_rms_norm_forward", "dcn_add_rms_norm_backward", "dcn_add_rms_norm_backward_input",
+              "dcn_grad_norm", "dcn_clip_grads"):
         getattr(lib, f).restype = st
     for f in ("dcn_add_rms_norm_backward_workspace_bytes", "dcn_grad_norm_workspace_bytes"):
         getattr(lib, f).restype = ctypes.c_int64
@@ -568,12 +571,15 @@ def _norm_backward_workspace_bytes(rows: int, cols: int, eps: float, code: int) 
 def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
                               weight: Optional[torch.Tensor] = None, *,
                               grad_residual_out: Optional[torch.Tensor] = None, eps: float = 1e-6, grad_x=None,
-                              grad_weight=None, workspace: Optional[torch.Tensor] = None):
+                              grad_weight=None, workspace: Optional[torch.Tensor] = None,
+                              need_grad_weight: bool = True):
     """(grad_x, grad_weight) of dcn_add_rms_norm_forward; see dcn_b200.h.
 
     h is the forward's residual_out (x without a residual), rstd what it saved;
     grad_x is the gradient of x and of the residual alike.  grad_weight is None
-    without a weight.  eps is part of rstd and only checked here."""
+    without a weight, and with need_grad_weight=False (a weight that is not
+    trained), which costs no workspace and no second kernel.  eps is part of rstd
+    and only checked here."""
     _cuda_tensor("h", h)
     dt, dev, shape = h.dtype, h.get_device(), h.shape
     if dt not in _DTYPE_CODE:
@@ -588,6 +594,14 @@ def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: tor
     ws_ptr, ws_bytes = None, 0
     if weight is not None:
         _like("weight", weight, (cols,), dt, dev)
+    if not need_grad_weight:
+        if grad_weight is not None or workspace is not None:
+            raise ValueError("grad_weight and workspace belong to need_grad_weight")
+        _launch(dev, lib().dcn_add_rms_norm_backward_input, ctypes.byref(p), grad_out.data_ptr(), h.data_ptr(),
+                rstd.data_ptr(), None if weight is None else weight.data_ptr(),
+                None if grad_residual_out is None else grad_residual_out.data_ptr(), grad_x.data_ptr())
+        return grad_x, None
+    if weight is not None:
         grad_weight = torch.empty_like(weight) if grad_weight is None else \
             _like("grad_weight", grad_weight, (cols,), dt, dev)
         if workspace is None:

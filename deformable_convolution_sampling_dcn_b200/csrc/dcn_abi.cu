@@ -430,6 +430,19 @@ dcnb::NormArgs norm_args(const dnorm_params *p) {
     return a;
 }
 
+// The backward's tensors but for the weight gradient, of rows > 0.
+dcn_status norm_backward_args(const dnorm_params *p, const void *grad_out, const void *h, const float *rstd,
+                              const void *weight, const void *grad_residual_out, void *grad_x, dcnb::NormArgs *a) {
+    if (!grad_out || !h || !rstd || !grad_x) return fail(DCN_ERR_NULL, "grad_out, h, rstd and grad_x are required");
+    const size_t es = dtype_size(p->dtype);
+    if (!aligned(grad_out, es) || !aligned(h, es) || !aligned(weight, es) || !aligned(grad_residual_out, es) ||
+        !aligned(grad_x, es) || !aligned(rstd, 4))
+        return fail(DCN_ERR_ALIGN, "tensors must be aligned to their element");
+    a->grad_out = grad_out; a->h = h; a->rstd = const_cast<float *>(rstd); a->weight = weight;
+    a->grad_residual_out = grad_residual_out; a->grad_x = grad_x;
+    return DCN_OK;
+}
+
 // The tensor lists of the gradient-norm calls.
 dcn_status check_grads(const dclip_params *p, const void *const *grads, const int64_t *numel, const int32_t *dtypes,
                        const float *norm, const void *workspace, int64_t workspace_bytes) {
@@ -507,6 +520,18 @@ dcn_status dcn_add_rms_norm_forward(const dnorm_params *p, const void *x, const 
     return cuda_status(dcnb::launch_norm_forward(a, (cudaStream_t)stream), "dcn_add_rms_norm_forward launch");
 }
 
+dcn_status dcn_add_rms_norm_backward_input(const dnorm_params *p, const void *grad_out, const void *h, const float *rstd,
+                                           const void *weight, const void *grad_residual_out, void *grad_x,
+                                           dcn_stream_t stream) {
+    const dcn_status s = check_norm(p);
+    if (s != DCN_OK) return s;
+    if (p->rows == 0) return DCN_OK;
+    dcnb::NormArgs a = norm_args(p);
+    const dcn_status t = norm_backward_args(p, grad_out, h, rstd, weight, grad_residual_out, grad_x, &a);
+    if (t != DCN_OK) return t;
+    return cuda_status(dcnb::launch_norm_backward(a, (cudaStream_t)stream), "dcn_add_rms_norm_backward_input launch");
+}
+
 int64_t dcn_add_rms_norm_backward_workspace_bytes(const dnorm_params *p) {
     if (check_norm(p) != DCN_OK) return -1;
     return (int64_t)dcnb::norm_backward_partial_rows(p->rows, p->cols, (dcnb::DType)p->dtype) * p->cols * 4;
@@ -528,11 +553,9 @@ dcn_status dcn_add_rms_norm_backward(const dnorm_params *p, const void *grad_out
         return cuda_status(cudaMemsetAsync(grad_weight, 0, (size_t)p->cols * es, (cudaStream_t)stream),
                            "dcn_add_rms_norm_backward memset");
     }
-    if (!grad_out || !h || !rstd || !grad_x) return fail(DCN_ERR_NULL, "grad_out, h, rstd and grad_x are required");
-    if (!aligned(grad_out, es) || !aligned(h, es) || !aligned(grad_residual_out, es) || !aligned(grad_x, es) ||
-        !aligned(rstd, 4))
-        return fail(DCN_ERR_ALIGN, "tensors must be aligned to their element");
     dcnb::NormArgs a = norm_args(p);
+    const dcn_status t = norm_backward_args(p, grad_out, h, rstd, weight, grad_residual_out, grad_x, &a);
+    if (t != DCN_OK) return t;
     if (grad_weight) {
         if (!workspace) return fail(DCN_ERR_NULL, "workspace is required with a weight");
         if (!aligned(workspace, 16)) return fail(DCN_ERR_ALIGN, "workspace must be 16-byte aligned");
@@ -540,8 +563,7 @@ dcn_status dcn_add_rms_norm_backward(const dnorm_params *p, const void *grad_out
         if (workspace_bytes < need)
             return fail(DCN_ERR_SHAPE, "workspace has %lld bytes, %lld needed", (long long)workspace_bytes, need);
     }
-    a.grad_out = grad_out; a.h = h; a.rstd = const_cast<float *>(rstd); a.weight = weight;
-    a.grad_residual_out = grad_residual_out; a.grad_x = grad_x; a.grad_weight = grad_weight;
+    a.grad_weight = grad_weight;
     a.partial = static_cast<float *>(workspace);
     return cuda_status(dcnb::launch_norm_backward(a, (cudaStream_t)stream), "dcn_add_rms_norm_backward launch");
 }

@@ -401,7 +401,8 @@ dcn_status dcn_add_rms_norm_forward(const dnorm_params *p, const void *x, const 
  *                 (of x and of residual alike)
  *   grad_weight = sum over rows of grad_out * xh
  * h is residual_out of the forward (x without a residual), rstd what it saved.
- * grad_residual_out NULL: zero.  grad_weight is given exactly when weight is.
+ * grad_residual_out NULL: zero.  grad_weight is given exactly when weight is
+ * (dcn_add_rms_norm_backward_input gives grad_x alone, of a weight that is not trained).
  * grad_x may be the same buffer as grad_out or grad_residual_out.  workspace:
  * dcn_add_rms_norm_backward_workspace_bytes(p) bytes, 16-byte aligned, needed
  * with a weight; calls that overlap on the GPU need one each.  Sums are fp32 in
@@ -412,6 +413,14 @@ dcn_status dcn_add_rms_norm_backward(const dnorm_params *p, const void *grad_out
                                      const float *rstd, const void *weight,
                                      const void *grad_residual_out, void *grad_x, void *grad_weight,
                                      void *workspace, int64_t workspace_bytes, dcn_stream_t stream);
+
+/*
+ * grad_x of the call above by itself, where the weight (or NULL) gets no gradient:
+ * one kernel, without a workspace.  rows == 0 is a no-op.
+ */
+dcn_status dcn_add_rms_norm_backward_input(const dnorm_params *p, const void *grad_out, const void *h,
+                                           const float *rstd, const void *weight,
+                                           const void *grad_residual_out, void *grad_x, dcn_stream_t stream);
 
 /* Workspace bytes of dcn_add_rms_norm_backward; -1 for invalid params. */
 int64_t dcn_add_rms_norm_backward_workspace_bytes(const dnorm_params *p);

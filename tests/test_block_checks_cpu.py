@@ -208,3 +208,20 @@ def test_single_tokens_take_the_row_route(lib, rows, rank):
         assert route(cin=cin, cout=cout, num_requests=rows) == "rows"
         assert route(cin=cin, cout=cout, num_requests=1 << 20) == "rows"  # a padded table may hold as many
     assert rank < 128 or rows < 128 or route(cin=4096, cout=4096, num_requests=1) == "tiles"
+
+
+def test_norm_backward_of_a_frozen_weight(lib):
+    f, b = lib.dcn_add_rms_norm_backward_input, ctypes.byref(norm())
+    assert f(None, 16, 16, 16, 16, None, 16, None) == B.DCN_ERR_NULL
+    for i in range(1, 7):
+        if i in (4, 5):  # weight, grad_residual_out
+            continue
+        args = [b, 16, 16, 16, 16, None, 16, None]
+        args[i] = None
+        assert f(*args) == B.DCN_ERR_NULL
+    for i, bad in ((1, 17), (2, 17), (3, 18), (4, 17), (5, 17), (6, 17)):
+        args = [b, 16, 16, 16, 16, None, 16, None]
+        args[i] = bad
+        assert f(*args) == B.DCN_ERR_ALIGN
+    assert f(ctypes.byref(norm(cols=0)), 16, 16, 16, 16, None, 16, None) == B.DCN_ERR_SHAPE
+    assert f(ctypes.byref(norm(rows=0)), None, None, None, None, None, None, None) == B.DCN_OK

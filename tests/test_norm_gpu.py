@@ -539,3 +539,49 @@ def test_codes_are_the_rounded_quotients(cols, k, quant, group, cuda_dev):
         assert torch.equal(o.out8.cpu().view(torch.uint8), v.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
     else:
         assert torch.equal(o.out8.cpu(), v.round().to(torch.int8))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("cols", [40, 61, 256, 512, 1000, 1029, 4096, 12001])
+def test_backward_of_a_frozen_weight(cols, dtype, cuda_dev):
+    """grad_x without the weight's gradient: the same bits, no other launch, no workspace."""
+    h, gh, w = gpu(*inputs(203, cols, DT[dtype], 71))
+    gy = torch.randn(203, cols).to(DT[dtype]).cuda()
+    rstd = definition(h.cpu(), None, None)[2].float().cuda()
+    want, _ = d.dcn_add_rms_norm_backward(gy, h, rstd, w, grad_residual_out=gh)
+    got, gw = d.dcn_add_rms_norm_backward(gy, h, rstd, w, grad_residual_out=gh, need_grad_weight=False)
+    assert gw is None and torch.equal(got, want)
+    got, gw = d.dcn_add_rms_norm_backward(gy, h, rstd, w, grad_residual_out=gh, grad_x=gh, need_grad_weight=False)
+    assert gw is None and got is gh and torch.equal(got, want)
+    with pytest.raises(ValueError):
+        d.dcn_add_rms_norm_backward(gy, h, rstd, w, grad_weight=torch.empty_like(w), need_grad_weight=False)
+    with pytest.raises(ValueError):
+        d.dcn_add_rms_norm_backward(gy, h, rstd, w[1:], need_grad_weight=False)
+    e, _ = d.dcn_add_rms_norm_backward(gy[:0], h[:0], rstd[:0], w, need_grad_weight=False)
+    assert e.shape == (0, cols)
+
+
+def test_autograd_asks_for_no_more_than_it_needs(cuda_dev, monkeypatch):
+    """A frozen weight's gradient is not formed; a trained one beside frozen inputs is."""
+    asked = []
+    real = d.dcn_add_rms_norm_backward
+    monkeypatch.setattr(d, "dcn_add_rms_norm_backward",
+                        lambda *a, **k: asked.append(k.get("need_grad_weight", True)) or real(*a, **k))
+    x, r, w = gpu(*inputs(9, 96, torch.float32, 72))
+    gy = torch.randn_like(x)
+    x.requires_grad_()
+    y, _ = d.AddRmsNormFunction.apply(x, r, w, EPS)
+    y.backward(gy)
+    frozen = x.grad.clone()
+    x.grad = None
+    w.requires_grad_()
+    y, h = d.AddRmsNormFunction.apply(x, r, w, EPS)
+    y.backward(gy)
+    assert asked == [False, True]
+    assert torch.equal(x.grad, frozen) and w.grad is not None
+    y, h = d.AddRmsNormFunction.apply(x.detach(), r, w, EPS)
+    w.grad = None
+    y.backward(gy)
+    assert w.grad is not None and asked[-1]
+    y, h = d.AddRmsNormFunction.apply(x, r, w.detach(), EPS)
+    h.sum().backward()  # the norm's output is not used
