@@ -619,13 +619,24 @@ def dcn_add_rms_norm_backward(grad_out: torch.Tensor, h: torch.Tensor, rstd: tor
     return grad_x, grad_weight
 
 
+_DENSE = {4: (torch.contiguous_format, torch.channels_last), 5: (torch.contiguous_format, torch.channels_last_3d)}
+
+
+def _dense_formats(t: torch.Tensor):
+    """The memory formats in which t is dense: a convolution's weight may lie channels-last, and so its gradient."""
+    if t.dim() not in _DENSE:
+        return (torch.contiguous_format,) if t.is_contiguous() else ()
+    return tuple(f for f in _DENSE[t.dim()] if t.is_contiguous(memory_format=f))
+
+
 class GradList:
     """The table of gradient buffers that dcn_grad_norm and dcn_clip_grads work on.
 
     Made once where the buffers stay in place over a training run (both calls
     also take a plain list and make the table each time).  `out` gives a buffer
     of the same shape for each gradient, of any storage type, that receives the
-    clipped values; without it clipping is in place.  Buffers must not overlap.
+    clipped values; without it clipping is in place.  Buffers are contiguous or
+    channels-last, an `out` buffer in its gradient's way, and must not overlap.
     The list keeps its tensors alive; a tensor that is given other memory
     (resize_, set_) needs a new list."""
 
@@ -643,8 +654,8 @@ class GradList:
                 raise TypeError(f"unsupported dtype {t.dtype}")
             if not t.is_cuda:
                 raise ValueError("gradients must be CUDA tensors (the library has no CPU path)")
-            if not t.is_contiguous():
-                raise ValueError("gradients and out buffers must be contiguous")
+            if not t.is_contiguous() and not _dense_formats(t):
+                raise ValueError("gradients and out buffers must be contiguous or channels-last")
             if self.device is None:
                 self.device = t.get_device()
             elif t.get_device() != self.device:
@@ -654,6 +665,9 @@ class GradList:
             o = None if self.out is None else self.out[i]
             if o is not None and o.shape != g.shape:
                 raise ValueError(f"out[{i}] shape {tuple(o.shape)} != {tuple(g.shape)}")
+            if o is not None and not (o.is_contiguous() and g.is_contiguous()) and \
+                    not set(_dense_formats(o)) & set(_dense_formats(g)):
+                raise ValueError(f"out[{i}] and its gradient lie in different memory formats")
             spans.append((g.data_ptr(), g.numel() * g.element_size()))
             if o is not None and not (o.data_ptr() == g.data_ptr() and o.dtype == g.dtype):
                 spans.append((o.data_ptr(), o.numel() * o.element_size()))

@@ -234,3 +234,33 @@ def test_refusals(cuda_dev):
         with pytest.raises(d.DcnError):
             d.dcn_clip_grads([g], **bad)
     assert (g == 1).all()
+
+
+def test_channels_last(cuda_dev):
+    """Convolution gradients that lie channels-last are as dense as others; an out buffer lies as its gradient does."""
+    g = torch.Generator().manual_seed(31)
+    cl, cl3 = torch.channels_last, torch.channels_last_3d
+    grads = [torch.randn(8, 5, 3, 3, generator=g).cuda().to(memory_format=cl),
+             torch.randn(4, 3, 2, 3, 3, generator=g).cuda().to(memory_format=cl3),
+             torch.randn(7, 9, generator=g).cuda(), torch.randn(6, 1, 3, 3, generator=g).cuda()]
+    assert not grads[0].is_contiguous() and not grads[1].is_contiguous()
+    want = torch.sqrt(sum((t.double() ** 2).sum() for t in grads))
+    c = min(1.0, 0.5 / (float(want) + 1e-6))
+    out = [torch.empty_like(t, dtype=torch.bfloat16) for t in grads]
+    assert out[0].is_contiguous(memory_format=cl)
+    norm = d.dcn_clip_grads(grads, 0.5, out=out)
+    assert abs(float(norm) - float(want)) <= 4 * 2.0 ** -24 * float(want)
+    for t, o in zip(grads, out):
+        exact = t.double() * c
+        assert ((o.double() - exact).abs() <= exact.abs() * (2.0 ** -8 + 8 * 2.0 ** -24)).all()
+    before = [t.clone() for t in grads]
+    d.dcn_clip_grads(grads, 0.5)
+    for t, b in zip(grads, before):
+        assert t.stride() == b.stride()
+        exact = b.double() * c
+        assert ((t.double() - exact).abs() <= exact.abs() * 8 * 2.0 ** -24).all()
+    with pytest.raises(ValueError, match="memory formats"):
+        d.GradList([grads[0]], [torch.empty(8, 5, 3, 3, device="cuda")])
+    d.GradList([grads[3]], [torch.empty(6, 1, 3, 3, device="cuda").to(memory_format=cl)])  # one channel: both at once
+    with pytest.raises(ValueError, match="contiguous"):
+        d.GradList([grads[0].permute(1, 0, 2, 3)])
