@@ -34,12 +34,10 @@
 // Every wait is bounded (1 s); a wait that runs out sets the device error
 // word, stops the CTA's remaining work, drains the copies and products it
 // already issued and frees its tensor memory.
-#include <algorithm>
 #include <type_traits>
 
 #include "dcn_common.cuh"
 #include "dcn_device.h"
-#include "dcn_host.h"
 #include "dcn_launch.h"
 #include "dcn_tcgen05.cuh"
 #include "dcn_tma.cuh"
@@ -819,10 +817,8 @@ cudaError_t launch_t(const ProjArgs &pa, cudaStream_t stream) {
     p.tmem_cols = cols;
 
     // at least half an SM's shared memory, so that one CTA owns the SM's
-    // tensor memory (the largest instance needs about 200 KB), and its share
-    // beside the clusters of other calls
-    const size_t share = tensor_memory_share((size_t)dev->smem_optin, cols);
-    const size_t least_smem = std::max((size_t)dev->smem_per_sm / 2 + 1024, share);
+    // tensor memory (the largest instance needs about 200 KB)
+    const size_t half_sm = (size_t)dev->smem_per_sm / 2 + 1024;
     if (proj_smem(p.npad_max, 2, 9, true) > (size_t)dev->smem_optin) return cudaErrorInvalidConfiguration;
 
     CUtensorMap map;
@@ -836,10 +832,10 @@ cudaError_t launch_t(const ProjArgs &pa, cudaStream_t stream) {
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
     switch (a.C * (int)sizeof(T) / 16) {
-        case 1: return launch_lpi<T, 1>(map, p, least_smem, stream);
-        case 2: return launch_lpi<T, 2>(map, p, least_smem, stream);
-        case 4: return launch_lpi<T, 4>(map, p, least_smem, stream);
-        case 8: return launch_lpi<T, 8>(map, p, least_smem, stream);
+        case 1: return launch_lpi<T, 1>(map, p, half_sm, stream);
+        case 2: return launch_lpi<T, 2>(map, p, half_sm, stream);
+        case 4: return launch_lpi<T, 4>(map, p, half_sm, stream);
+        case 8: return launch_lpi<T, 8>(map, p, half_sm, stream);
         default: return cudaErrorInvalidValue;
     }
 }

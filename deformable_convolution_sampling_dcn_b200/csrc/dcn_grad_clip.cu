@@ -12,8 +12,9 @@
 // to run), derives c and rewrites the gradients.
 //
 // Bound: device memory, the gradients being read twice.  The second pass walks
-// the runs backwards and starts with what the first pass read last, which L2
-// still holds.  Measured (one B200): 301 bf16 tensors of 97 M elements into fp32
+// the runs backwards and starts with what the first pass read last, of which L2
+// still holds a part: of 194 MB of gradients 161 are read from device memory again.
+// Measured (one B200): 301 bf16 tensors of 97 M elements into fp32
 // 142 us, 34 us (5.7 TB/s) of it the norm; 13 fp32 tensors of 1.1 M elements 6.5
 // us, two dependent launches.
 //

@@ -25,6 +25,9 @@ template <typename K> cudaError_t allow_smem(K kern, int bytes, std::atomic<bool
 // different streams could hold each other up for good.  So a CTA takes the same share of the shared memory as of the
 // tensor memory: CTAs that fit an SM together find their columns there, and none waits.  All 512 columns leave 13 KB to
 // CTAs without tensor memory: the smallest share of those with some is 14 KB.
+// The fused core + projection keeps to half an SM's shared memory whatever its columns are (its gather lives on L1:
+// 12800 pixels, 512 -> 512, 66.0 us so and 67.9 with its share), but waits for no other CTA.  It could only get in
+// the way between two CTAs of clusters on its SM: a cluster's take a quarter at least, and two do not fit beside it.
 inline size_t tensor_memory_share(size_t limit, int cols) {
     return cols >= 512 ? limit - 13 * 1024 : limit * cols / 512;
 }

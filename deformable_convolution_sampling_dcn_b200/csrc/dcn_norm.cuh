@@ -4,7 +4,7 @@
 // consecutive vectors: loads and stores are coalesced, and 128 neighbouring
 // columns sit in 16 (16-bit storage) or 32 (fp32) neighbouring lanes.
 //
-// A team is 8 lanes, a warp, or the whole CTA (TPR = 0).
+// A team is 8 lanes, 16 (in the forward), a warp, or the whole CTA (TPR = 0).
 //
 // Rows that do not start on 16 bytes are held by the vectors of the aligned grid
 // (SHIFT): vector v of a row has the columns v * VEC - shift .. + VEC - 1, where
@@ -199,7 +199,8 @@ template <typename T, bool SHIFT> __device__ __forceinline__ uint4 clear_outside
 // The staged vectors of a CTA team's rows.  Shifted, the first is vector 0 of thread 0 and the last, ragged one vector
 // `last` of some thread.  KEEP: their masks are kept, all ones in the other threads, where there are registers for them;
 // masks made row by row in the threads that need them hold the CTA up (fp16 5734 x 4383: backward 84 us against 73,
-// forward 42.8 against 39.7; but to e4m3, which has no registers left, 49.8 against 52.5).
+// forward 42.8 against 39.7; but to e4m3, which has no registers left, 49.8 against 52.5,
+// before its codes were quotients).
 template <typename T, bool SHIFT, bool KEEP> struct RowVecs {
     int cols;
     long long off;  // of the row in its tensor

@@ -11,9 +11,10 @@
 // kernel adds those rows in a fixed order, so the result does not depend on
 // timing (no atomics).
 // Measured (one B200): fp32 12800 x 512 with a gradient of the new residual 20.4
-// us (105 MB: 5.1 TB/s; 16.4 us = 6.4 TB/s without a weight), bf16 102400 x 256
+// us (105 MB: 5.1 TB/s; 17.8 us without the weight's gradient, 16.4 us = 6.4 TB/s without a weight), bf16 102400 x 256
 // 38.2 us (210 MB: 5.5 TB/s); off 16-byte boundaries fp16 5734 x 4383 73 us (201 MB: 2.8 TB/s; one CTA of 9 warps an
-// SM), fp32 4001 x 6001 69 us (384 MB: 5.6 TB/s).
+// SM), fp32 4001 x 6001 69 us (384 MB: 5.6 TB/s), by elements fp16 30011 x 521 64 us (125 MB: 2.0 TB/s), 2000 x 601
+// 9.5 us; wider than 8192 columns bf16 4096 x 12288 239 us (403 MB: 1.7 TB/s).
 #include "dcn_device.h"
 #include "dcn_host.h"
 #include "dcn_launch.h"
@@ -150,8 +151,10 @@ template <typename T> __global__ void __launch_bounds__(kTeamThreads, 2) norm_ba
     store_partial<TPR, 1, VEC, kTeamThreads / 32>(a, gw, sums, t, TPR);
 }
 
-// Rows at any alignment, by elements: warp or CTA teams of C columns a thread.  Also the widest aligned fp32 rows, of
-// which two do not fit the shared memory.  Nothing is loaded ahead: narrow rows take many warps instead, of as few
+// Rows at any alignment, by elements: warp or CTA teams of C columns a thread.  Also aligned rows of more than 8192
+// columns, which 512 threads of 16 columns do not hold (1024 threads have 64 registers each, of which the staged kernel
+// needs up to 128; two slots of three 16-bit rows of 16384 columns would fit the shared memory, of fp32 rows only up to
+// some 9600): bf16 4096 x 12288 239 us, 2048 x 16384 149, fp32 230 and 146, 2 to 4 times their floors.  Nothing is loaded ahead: narrow rows take many warps instead, of as few
 // columns a lane as hold the row (fp16 100000 x 61 24 us, with 8 columns a lane 59; 300000 x 21 55 against 161).
 constexpr int elems_per_sm(int c) { return c <= 4 ? 6 : c <= 8 ? 4 : 2; }
 template <typename T, int TPR, int C>

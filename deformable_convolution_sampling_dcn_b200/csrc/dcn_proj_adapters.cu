@@ -17,16 +17,15 @@
 // 1.84e-3 with one value, 1.66e-3 with two, which is the output's own rounding).
 // fp16 has no room above 65504: eight neighbours of a row of t that go beyond 2^15
 // are scaled down by a power of two, whose exponent is kept, and EXPAND adds what is
-// missing in fp32 when it finishes the row.  Along the rows either the tile or the request
-// advances, so tile + request numbers the pairs.
+// missing in fp32 when it finishes the row.  Along the rows either the tile or the
+// request advances, so tile + request numbers the pairs.
 //
 // EXPAND runs over the tiles of y: the blocks of x and W first, then those of t
 // and B.  A tile is 256 rows x BN channels by a pair of CTAs (cta_group::2):
-// each CTA stages its own 128 rows and half of the channels, 32 KB for every 256
-// x 256 x 64 products, because what an SM can fetch from L2 bounds the kernel
-// (128 x 256 tiles of single CTAs: 48 KB for 128 x 256 x 64).  EXPAND is a
-// programmatic dependent of SHRINK and waits for it only before its first load
-// of t.
+// each CTA stages its own 128 rows and half of the channels, 64 KB by both for
+// 256 x 256 x 64 products (single CTAs with 128 x 256 tiles stage 96 KB for as many,
+// and took 138 us where pairs took 122).  EXPAND is a programmatic dependent of
+// SHRINK and waits for it before its first load of t and, in fp16, of the exponents.
 //
 // The two values of t take twice the least workspace of a call.  With less than
 // that the rows go in several passes, two launches each, with t of one pass at a
@@ -40,14 +39,16 @@
 // Both are persistent and warp-specialised: warp 0 streams the 64-wide blocks
 // of both operands by TMA (128-byte swizzle, zero fill past every edge) through
 // a ring, one thread of warp 1 (of the pair's first CTA) issues tcgen05.mma into
-// one of two tensor-memory accumulators, warps 2..5 read the finished one back,
-// finish it and store.  Every wait is bounded and gives up when another role of
+// one of two tensor-memory accumulators, the others (four warps in SHRINK, eight in
+// EXPAND) read the finished one back, finish it and store.  Every wait is bounded and gives up when another role of
 // the CTA has aborted.
 //
-// Measured (one B200): fp16 12800 rows 512 -> 512, rank 16 21.5 us (330 TFLOP/s,
-// bound by the chain of latencies of the two launches and by fetches from L2);
-// bf16 16111 rows 2048 -> 2048, rank 64 128 us (1.1 PFLOP/s), 97 us of it the
-// products with W.  With t rounded to one value they took 21.1 and 121 us.
+// Measured (one B200): fp16 12800 rows 512 -> 512, rank 16 21.6 us (330 TFLOP/s,
+// bound by the chain of latencies of the two launches; the tensor pipe is busy for
+// a fifth of EXPAND); bf16 16111 rows 2048 -> 2048, rank 64 127 us (1.1 PFLOP/s), 97
+// us of it the products with W, the tensor pipe busy for 71 % of EXPAND and L2 at 40 %
+// of its rate.  With t rounded to one value they took 21.1 and 120 us.  Every request
+// in a tile is a set of blocks of its own: 512 single tokens 1024 -> 4096 246 us.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
@@ -940,7 +941,8 @@ size_t plan_smem(LargeParams &p, size_t sbytes, size_t sums, size_t extra, size_
     if (p.splits > 1)
         while (p.stages * sbytes < sums && p.stages < kMaxStages) ++p.stages;
     const size_t need = other + p.stages * sbytes, share = tensor_memory_share(limit, p.tmem_cols);
-    return need > share ? need : share;
+    const size_t least = p.splits > 1 && share < limit / 4 ? limit / 4 : share;  // (a pair's staged output takes more)
+    return need > least ? need : least;
 }
 
 // Bytes of t for one row: two values of the storage type for each rank, and in fp16 the exponents.

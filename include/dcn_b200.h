@@ -312,9 +312,10 @@ dcn_status deform_roi_pool_forward(const droi_params *p, const void *x, const fl
  * with more it may be (and above 256 rows is) the sum of two values of the
  * storage dtype, the operands of the second tensor-core product: off by at most
  * 2^-22 |t| + 2^-25 in fp16 (2^-39 of the largest of eight neighbouring ranks
- * instead of 2^-25 where that exceeds 2^15) and 2^-16 |t| in bf16, over all of fp32's range.  What
- * other requests' rows and adapters hold does not reach a row's values; how many
- * rows the call has may change their last bits (the order of the sums).
+ * instead of 2^-25 where that exceeds 2^15) and 2^-16 |t| in bf16, over all of
+ * fp32's range.  What other requests' rows and adapters hold does not reach a
+ * row's values; how many rows the call has may change their last bits (the order
+ * of the sums).
  * cin, cout and rank are multiples of 8, cin and cout up to 65536, rank up to
  * 128; rows up to 2^30; num_requests and num_adapters up to 2^20, with
  * num_adapters * cout and num_adapters * rank up to 2^30.  x, weight, bias, a, b
@@ -322,8 +323,9 @@ dcn_status deform_roi_pool_forward(const droi_params *p, const void *x, const fl
  * workspace: dcn_proj_adapters_workspace_bytes(p) bytes at least, 16-byte aligned;
  * with less than dcn_proj_adapters_workspace_full_bytes(p) the rows may be worked
  * on in several passes, one after the other; calls that overlap on the GPU need
- * one each.  rows == 0 or num_requests == 0 is a
- * no-op; num_adapters may be 0 (a and b may then be NULL).
+ * one each.  Empty requests cost next to nothing at the end of the table (one
+ * that is filled up to a fixed size), and a search each elsewhere.  rows == 0 or
+ * num_requests == 0 is a no-op; num_adapters may be 0 (a and b may then be NULL).
  */
 typedef struct {
     int64_t rows;
