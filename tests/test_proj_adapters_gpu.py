@@ -533,3 +533,52 @@ def test_a_table_that_is_not_ascending_ends(cuda_dev):
         torch.cuda.synchronize()
         assert d._binding.take_device_error() in (0, 2)
         check(s, call(s))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("byte", [0x00, 0x7f, 0xff])
+@pytest.mark.parametrize("lens,first,rows", [([90, 0, 60, 5], 3, 170), ([300, 1, 200, 40], 7, 600), ([1] * 4, 0, 4),
+                                             ([250, 0, 10, 40], 0, 300)])
+def test_what_the_workspace_held_does_not_matter(lens, first, rows, byte, dtype, cuda_dev):
+    """NaN, infinities and exponents of earlier calls lie in the workspace, also for rows with no adapter or request."""
+    s = make(lens, [1, 0, -1, 0], 520, 136, 24, 2, dtype, 280, rows=rows, first=first)
+    p = d._binding.DadaptParams(rows, 520, 136, 24, 2, 4, 1 if dtype == "f16" else 2)
+    ws = torch.full((d.lib().dcn_proj_adapters_workspace_full_bytes(p),), byte, dtype=torch.uint8, device="cuda")
+    out = torch.full((rows, 136), 7.0, dtype=DT[dtype], device="cuda")
+    end = first + sum(lens)
+    for _ in range(2):
+        y = call(s, out=out, workspace=ws)
+        check(s, y, slice(first, end))
+        want, tol = definition_32(s)
+        assert ((y.double().cpu() - want).abs() <= tol)[first:end].all()
+        assert (out[:first] == 7).all() and (out[end:] == 7).all()
+
+
+def test_large_t_in_captured_calls(cuda_dev):
+    """Exponents are of the call: a graph replayed on other inputs, and two of them in flight."""
+    sets = [make([300, 40, 200], [0, 1, -1], 64, 136, 16, 2, "f16", 290 + i) for i in range(2)]
+    sets[1]["x"][100:320] *= 2.0 ** 10
+    for s in sets:
+        s["a"] *= 2.0 ** 6
+        s["b"] *= 2.0 ** -12
+        s["weight"] *= 2.0 ** -4
+    t = {k: v.cuda() for k, v in sets[0].items()}
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = d.dcn_proj_adapters_forward(t["x"], t["weight"], t["bias"], t["a"], t["b"], t["start"], t["which"],
+                                            scale=t["scale"])
+        graphs.append((g, o))
+    for i in (1, 0, 1):
+        for k, v in sets[i].items():
+            t[k].copy_(v)
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in graphs]
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        want, tol = definition_32(sets[i])
+        for _, o in graphs:
+            assert ((o.double().cpu() - want).abs() <= tol).all()
