@@ -40,8 +40,8 @@
 // of both operands by TMA (128-byte swizzle, zero fill past every edge) through
 // a ring, one thread of warp 1 (of the pair's first CTA) issues tcgen05.mma into
 // one of two tensor-memory accumulators, the others (four warps in SHRINK, eight in
-// EXPAND) read the finished one back, finish it and store.  Every wait is bounded and gives up when another role of
-// the CTA has aborted.
+// EXPAND) read the finished one back, finish it and store.  Every wait is bounded
+// and gives up when another role of the CTA has aborted.
 //
 // Measured (one B200): fp16 12800 rows 512 -> 512, rank 16 21.6 us (330 TFLOP/s,
 // bound by the chain of latencies of the two launches; the tensor pipe is busy for
@@ -76,7 +76,7 @@ struct LargeParams {
     const float *scale;
     const void *bias;
     // this pass: rows row0 .. row0 + rows - 1 of the request table, t [2, rows, rank] and (fp16) the exponents of its
-    // eighths [rows, 16], both for rows with an adapter only; out starts at row0
+    // groups of eight ranks [rows, 16], both for rows with an adapter only; out starts at row0
     int row0;
     void *t;
     unsigned char *shift;
@@ -455,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mine) {
                     uint32_t shift = store_t<T>(dst + c, rest + c, v);
                     if (c + 8 < p.rank) shift |= store_t<T>(dst + c + 8, rest + c + 8, v + 8) << 8;
-                    if (kShifted) *reinterpret_cast<uint16_t *>(p.shift + (long long)row * kShiftBytes + c / 8) = (uint16_t)shift;
+                    if (kShifted)
+                        *reinterpret_cast<uint16_t *>(p.shift + (long long)row * kShiftBytes + c / 8) = (uint16_t)shift;
                 }
             }
             tc_fence_before();
